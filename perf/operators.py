@@ -424,8 +424,7 @@ def _prepare_attn(case, seed):
         rows.append([i * W + r for r in range(win_len[i] - keep, win_len[i])] +
                     [S * W + int(first[i]) + t for t in p])
     st = {"case": case, "codes": codes.view(S * cap, -1), "scales": scales.view(S * cap, -1),
-          "layers": layers, "idx": idx, "rows": _padded(rows, W),
-          "win_len": torch.tensor(win_len, dtype=torch.int32, device=DEV)}
+          "layers": layers, "idx": idx, "rows": _padded(rows, W)}
     st.update(_plan(case, g))
     if own:
         st["cache"], st["tree"] = _cache(
@@ -504,7 +503,7 @@ def _run_attn(st):
         wins, drafts = [l["win"] for l in ls], [l["draft"] for l in ls]
         return C.csa2_sparse_attn_tree_layers(
             st["cache"], st["tree"], [l["q"] for l in ls], None if fp8 else wins,
-            None if fp8 else drafts, st["idx"], scale, st["outs"], swa_len=st["win_len"],
+            None if fp8 else drafts, st["idx"], scale, st["outs"],
             sinks=[l["sink"] for l in ls] if case["sink"] else None, rope_out=case["rope"],
             rope_base=BASE, swa_fp8s=wins if fp8 else None, draft_fp8s=drafts if fp8 else None)
     idx, rows = st["idx"].long(), st["rows"]
