@@ -69,6 +69,29 @@ class CacheViews(ctypes.Structure):
                 ("idx_codes", ctypes.c_void_p), ("idx_scales", ctypes.c_void_p)]
 
 
+class TreeStruct(ctypes.Structure):
+    """csa2_tree_t."""
+    _fields_ = [("n_seqs", ctypes.c_int32), ("seq_ids", ctypes.c_void_p),
+                ("n_draft", ctypes.c_void_p), ("pos0", ctypes.c_void_p),
+                ("parent", ctypes.c_void_p)]
+
+
+class TreeLayer(ctypes.Structure):
+    """csa2_tree_layer_t: one layer of a drafted tree's readout."""
+    _fields_ = [(f, ctypes.c_void_p) for f in
+                ("q", "swa_kv", "draft_kv", "out", "lse", "sink", "swa_codes", "swa_rope",
+                 "swa_scales", "draft_codes", "draft_rope", "draft_scales")]
+
+
+class NormPart(ctypes.Structure):
+    """csa2_norm_part_t: one tensor of a norm + rotation call."""
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "out", "weight", "pos")] +
+                [(f, ctypes.c_int64) for f in ("n_tokens", "x_token_stride", "x_head_stride",
+                                               "out_token_stride", "out_head_stride")] +
+                [(f, ctypes.c_int32) for f in ("n_heads", "dim", "rope_dim", "norm", "x_fp32",
+                                               "out_fp32")])
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
@@ -122,6 +145,13 @@ def _load():
         "csa2_sparse_attn_prefill": ([P, i32, i32, i64, P, P, i64, i64, P, ctypes.c_float, P, P,
                                       P], i32),
         "csa2_get_device_error": ([P, P, ctypes.POINTER(i32)], i32),
+        "csa2_norm_rope": ([i32, P, ctypes.c_float, ctypes.c_double, P], i32),
+        "csa2_tree_paths": ([i32, P, P, P], i32),
+        "csa2_index_scores_tree": ([P, P, P, P, P, i64, P, P], i32),
+        "csa2_index_topk_tree": ([P, P, P, P, P, P, P, sz, P], i32),
+        "csa2_sparse_attn_tree": ([P, P, i32, P, P, P, ctypes.c_float, i32, ctypes.c_double, P,
+                                   sz, P], i32),
+        "csa2_cache_accept_tree": ([P, P, P, P], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -632,3 +662,263 @@ def csa2_swa_fp8_quantise(rows: torch.Tensor, stream=None):
     _check(lib.csa2_swa_fp8_quantise(n, _ptr(r), _ptr(codes), _ptr(rope), _ptr(scales),
                                      _stream(stream)), "csa2_swa_fp8_quantise")
     return codes, rope, scales
+
+
+# ------------------------------------------------------------------ norms and rotation
+def _shaped(t: torch.Tensor, shape, dtype, what: str):
+    """Device pointer of a dense CUDA tensor of this shape and type on the
+    current device."""
+    if (t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda
+            or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _scratch(nbytes: int, device, stream):
+    """A workspace that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
+def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=None, norms=None,
+                   rope_dim=64, eps: float = 1e-6, rope_base: float = 0.0, stream=None) -> list:
+    """RMS norm of every head and the rotation of its last rope_dim channels
+    by its token's position, for up to 8 tensors in one launch.
+
+    xs: bf16 or fp32 tensors [n, heads, dim] or [n, dim], channels contiguous
+    (slices of a wider projection are taken as they are); positions: int64
+    [n], or one per tensor; weights: per tensor None or fp32 [dim]; outs: per
+    tensor the output, bf16 or fp32 (None: like x; x itself: in place);
+    norms: per tensor whether to norm (default: all); rope_dim: one number or
+    one per tensor, 0 for no rotation.  Returns the outputs."""
+    n = len(xs)
+    if n > 8:
+        raise ValueError("csa2_norm_rope: at most 8 tensors")
+    if outs is None:
+        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+    if weights is None:
+        weights = (None,) * n
+    one_pos, one_dim = isinstance(positions, torch.Tensor), isinstance(rope_dim, int)
+    if (len(outs) != n or len(weights) != n or (norms is not None and len(norms) != n)
+            or (not one_pos and len(positions) != n) or (not one_dim and len(rope_dim) != n)):
+        raise ValueError("csa2_norm_rope: one entry per tensor expected")
+    parts = (NormPart * max(n, 1))()
+    dev = torch.cuda.current_device()
+    bf16, f32 = torch.bfloat16, torch.float32
+    for i in range(n):
+        x, y, w, d = xs[i], outs[i], weights[i], parts[i]
+        pos = positions if one_pos else positions[i]
+        shape, xt, yt = x.shape, x.dtype, y.dtype
+        if (x.dim() not in (2, 3) or y.shape != shape or x.get_device() != dev
+                or y.get_device() != dev or (xt != bf16 and xt != f32)
+                or (yt != bf16 and yt != f32)):
+            raise ValueError("csa2_norm_rope: bf16 or fp32 tensors [n, heads, dim] or [n, dim] on "
+                             "the current device expected")
+        sx, sy = x.stride(), y.stride()
+        if (sx[-1] != 1 or sy[-1] != 1) and shape[-1] > 1:
+            raise ValueError("csa2_norm_rope: the channels of a head must be contiguous")
+        d.x, d.out = x.data_ptr(), y.data_ptr()
+        if w is not None:
+            d.weight = _shaped(w, shape[-1:], f32, "weight")
+        r = rope_dim if one_dim else rope_dim[i]
+        if r:
+            d.pos = _shaped(pos, shape[:1], torch.int64, "positions")
+        d.n_tokens, d.dim, d.rope_dim = shape[0], shape[-1], r
+        d.x_token_stride, d.out_token_stride = sx[0], sy[0]
+        if len(shape) == 3:
+            if shape[1] == 0:
+                d.n_tokens, d.n_heads = 0, 1
+            else:
+                d.n_heads, d.x_head_stride, d.out_head_stride = shape[1], sx[1], sy[1]
+        else:
+            d.n_heads = 1
+        d.norm = 1 if norms is None or norms[i] else 0
+        d.x_fp32, d.out_fp32 = xt == f32, yt == f32
+    _check(lib.csa2_norm_rope(n, parts, eps, rope_base, _stream(stream)), "csa2_norm_rope")
+    return list(outs)
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+class Tree:
+    """The trees of drafted tokens of one step (csa2_tree_t), kept on the host.
+
+    parents: per sequence the parent of each draft (an earlier draft of the
+    same tree, or -1 for the last committed token); pos0: committed tokens of
+    each sequence; seq_ids: the cache's sequences (default: 0, 1, ...).
+    Queries are the drafts of all sequences in order."""
+
+    def __init__(self, parents: Sequence[Sequence[int]], pos0: Sequence[int],
+                 seq_ids: Optional[Sequence[int]] = None):
+        self.n_seqs = len(parents)
+        if len(pos0) != self.n_seqs or (seq_ids is not None and len(seq_ids) != self.n_seqs):
+            raise ValueError("Tree: one pos0 (and sequence) per tree expected")
+        self.n_draft = [len(p) for p in parents]
+        self.n_queries = sum(self.n_draft)
+        self.pos0 = [int(p) for p in pos0]
+        self._n = _i32_array(self.n_draft)
+        self._pos0 = _i64_array(pos0)
+        self._parent = _i32_array([a for p in parents for a in p])
+        self._seq = _i32_array(seq_ids)
+        addr = ctypes.addressof
+        self.struct = TreeStruct(self.n_seqs, addr(self._seq) if self._seq is not None else None,
+                                 addr(self._n), addr(self._pos0), addr(self._parent))
+        self.ref = ctypes.byref(self.struct)
+        self.depths, self.paths = [], []
+        for p in parents:
+            d, m = (ctypes.c_int32 * 64)(), (ctypes.c_uint64 * 64)()
+            _check(lib.csa2_tree_paths(len(p), _i32_array(p), d, m), "csa2_tree_paths")
+            self.depths.append(list(d[:len(p)]))
+            self.paths.append(list(m[:len(p)]))
+
+    def positions(self, device=None) -> torch.Tensor:
+        """int64 [n_queries]: the drafts' positions (for csa2_norm_rope)."""
+        pos = [p + d for p, ds in zip(self.pos0, self.depths) for d in ds]
+        return torch.tensor(pos, dtype=torch.int64,
+                            device=torch.device("cuda") if device is None else device)
+
+    def owners(self, ratio: int) -> list:
+        """Per sequence the drafts that complete a block of `ratio` tokens:
+        the ones whose entries are appended before the step, in this order."""
+        return [[t for t, d in enumerate(ds) if (p + d + 1) % ratio == 0]
+                for p, ds in zip(self.pos0, self.depths)]
+
+
+def csa2_index_scores_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: torch.Tensor,
+                           scores: torch.Tensor, key_hist: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Index scores of the drafts: q_idx bf16 [n_queries, 32, 128], w fp32
+    [n_queries, 32], scores fp32 [n_queries, ld]: the committed entries' scores,
+    then those of the draft's path; key_hist: int32 [n_queries, 2048] (bf16
+    keys)."""
+    nq, c = tree.n_queries, cache.cfg
+    ld = scores.shape[-1]
+    _check(lib.csa2_index_scores_tree(
+        cache.handle, tree.ref,
+        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx"),
+        _shaped(w, (nq, c.idx_heads), torch.float32, "w"),
+        _shaped(scores, (nq, ld), torch.float32, "scores"), ld,
+        None if key_hist is None else _shaped(key_hist, (nq, 2048), torch.int32, "key_hist"),
+        _stream(stream)), "csa2_index_scores_tree")
+    return scores
+
+
+def csa2_index_topk_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: torch.Tensor,
+                         topk_idx: Optional[torch.Tensor] = None,
+                         topk_score: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Selection of the drafts among the committed entries and their path's;
+    int32 [n_queries, topk] entries of the cache, ascending, -1 padded."""
+    nq, c = tree.n_queries, cache.cfg
+    if topk_idx is None:
+        topk_idx = torch.empty(nq, c.topk, dtype=torch.int32, device=q_idx.device)
+    ws = workspace
+    if ws is None:
+        ws = _scratch(csa2_index_workspace_bytes(cache, nq), q_idx.device, stream)
+    _check(lib.csa2_index_topk_tree(
+        cache.handle, tree.ref,
+        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx"),
+        _shaped(w, (nq, c.idx_heads), torch.float32, "w"),
+        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx"),
+        None if topk_score is None else _shaped(topk_score, (nq, c.topk), torch.float32,
+                                                "topk_score"),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "csa2_index_topk_tree")
+    return topk_idx
+
+
+def csa2_sparse_attn_tree(cache: Cache, tree: Tree, q: torch.Tensor,
+                          swa_kv: Optional[torch.Tensor], draft_kv: Optional[torch.Tensor],
+                          topk_idx: torch.Tensor, scale: float,
+                          swa_len: Optional[Sequence[int]] = None,
+                          out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None,
+                          sink: Optional[torch.Tensor] = None, rope_out: bool = False,
+                          rope_base: float = 0.0, swa_fp8=None, draft_fp8=None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Readout of the drafts of one layer; see csa2_sparse_attn_tree_layers."""
+    return csa2_sparse_attn_tree_layers(
+        cache, tree, [q], None if swa_kv is None else [swa_kv],
+        None if draft_kv is None else [draft_kv], topk_idx, scale,
+        None if out is None else [out], lses=None if lse is None else [lse], swa_len=swa_len,
+        sinks=None if sink is None else [sink], rope_out=rope_out, rope_base=rope_base,
+        swa_fp8s=None if swa_fp8 is None else [swa_fp8],
+        draft_fp8s=None if draft_fp8 is None else [draft_fp8], workspace=workspace,
+        stream=stream)[0]
+
+
+def csa2_sparse_attn_tree_layers(cache: Cache, tree: Tree, qs: Sequence[torch.Tensor],
+                                 swa_kvs: Optional[Sequence[torch.Tensor]],
+                                 draft_kvs: Optional[Sequence[torch.Tensor]],
+                                 topk_idx: torch.Tensor, scale: float,
+                                 outs: Optional[Sequence[torch.Tensor]] = None,
+                                 lses: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                                 swa_len: Optional[Sequence[int]] = None,
+                                 sinks: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                                 rope_out: bool = False, rope_base: float = 0.0,
+                                 swa_fp8s=None, draft_fp8s=None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None) -> list:
+    """Readout of the drafts for several layers of a group in one launch.
+
+    Per layer: q bf16 [n_queries, heads, 512]; committed window rows swa_kv
+    bf16 [n_seqs, swa, 512] (the first swa_len[i] rows are the newest
+    committed rows, in position order) and the drafts' rows draft_kv bf16
+    [n_queries, 512], or both as the triples of csa2_swa_fp8_quantise;
+    swa_len: host, default min(swa, pos0); topk_idx from
+    csa2_index_topk_tree; rope_out rotates each output by minus its draft's
+    position.  workspace as for csa2_sparse_attn_decode.  Returns the
+    outputs."""
+    nq, S, c, L = tree.n_queries, tree.n_seqs, cache.cfg, len(qs)
+    H, D, W, bf16 = c.n_heads, c.head_dim, c.swa, torch.bfloat16
+    if outs is None:
+        outs = [torch.empty(q.shape, dtype=q.dtype, device=q.device) for q in qs]
+    for name, xs in (("outs", outs), ("lses", lses), ("sinks", sinks), ("swa_kvs", swa_kvs),
+                     ("draft_kvs", draft_kvs), ("swa_fp8s", swa_fp8s),
+                     ("draft_fp8s", draft_fp8s)):
+        if xs is not None and len(xs) != L:
+            raise ValueError(f"csa2_sparse_attn_tree_layers: one of {name} per layer expected")
+    if (swa_fp8s is None) != (draft_fp8s is None):
+        raise ValueError("csa2_sparse_attn_tree_layers: window and drafted rows of one format")
+    if swa_len is not None and len(swa_len) != S:
+        raise ValueError("csa2_sparse_attn_tree_layers: one swa_len per tree expected")
+    layers = (TreeLayer * L)()
+    for l in range(L):
+        y = layers[l]
+        y.q = _shaped(qs[l], (nq, H, D), bf16, "q")
+        y.out = _shaped(outs[l], (nq, H, D), bf16, "out")
+        if lses is not None and lses[l] is not None:
+            y.lse = _shaped(lses[l], (nq, H), torch.float32, "lse")
+        if sinks is not None and sinks[l] is not None:
+            y.sink = _shaped(sinks[l], (H,), torch.float32, "sink")
+        if W == 0:
+            continue
+        if swa_fp8s is not None:
+            u8 = torch.uint8
+            for rows, n, kind in ((swa_fp8s[l], S * W, "swa"), (draft_fp8s[l], nq, "draft")):
+                codes, rope, scales = (r.view(n, r.shape[-1]) for r in rows)
+                setattr(y, kind + "_codes", _shaped(codes, (n, 448), u8, kind + "_fp8 codes"))
+                setattr(y, kind + "_rope", _shaped(rope, (n, 64), bf16, kind + "_fp8 rope"))
+                setattr(y, kind + "_scales", _shaped(scales, (n, 8), u8, kind + "_fp8 scales"))
+        else:
+            if swa_kvs is None or draft_kvs is None:
+                raise ValueError("csa2_sparse_attn_tree_layers: window and drafted rows expected")
+            y.swa_kv = _shaped(swa_kvs[l], (S, W, D), bf16, "swa_kv")
+            y.draft_kv = _shaped(draft_kvs[l], (nq, D), bf16, "draft_kv")
+    # the two-CTA split only asks for a token workspace; its memory is not written
+    ws, nbytes = (topk_idx.data_ptr(), 16) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(lib.csa2_sparse_attn_tree(
+        cache.handle, tree.ref, L, layers, _i32_array(swa_len),
+        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx"), scale, 1 if rope_out else 0,
+        rope_base, ws if nbytes else None, nbytes, _stream(stream)), "csa2_sparse_attn_tree")
+    return list(outs)
+
+
+def csa2_cache_accept_tree(cache: Cache, tree: Tree, accepted: Sequence[int], stream=None):
+    """Commits, per sequence, the path of draft accepted[i] (-1: none): its
+    entries stay, the other drafts' are dropped."""
+    if len(accepted) != tree.n_seqs:
+        raise ValueError("csa2_cache_accept_tree: one accepted draft (or -1) per tree expected")
+    _check(lib.csa2_cache_accept_tree(cache.handle, tree.ref, _i32_array(accepted),
+                                      _stream(stream)), "csa2_cache_accept_tree")

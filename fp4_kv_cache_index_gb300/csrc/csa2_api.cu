@@ -53,6 +53,7 @@ struct csa2_cache {
   CUtensorMap tm_k8;   // indexer keys, one 8-key block per box (pool mode)
   CUtensorMap tm_kq;   // MXFP4 key codes, 128-key tiles in the permuted row order
   CUtensorMap tm_kc8;  // MXFP4 key codes, one 8-key block per box (pool mode)
+  int dev;             // device of the cache
   int num_sms;
   int index_sms;       // SMs the indexer's persistent grid may occupy
   int64_t wait_cycles; // bounded-wait limit of the kernels (0: their default)
@@ -385,6 +386,7 @@ csa2_status_t csa2_cache_create(const csa2_config_t* cfg, int32_t batch, const i
     delete c;
     return CSA2_ERR_CUDA;
   }
+  c->dev = dev;
   c->index_sms = c->num_sms;
   c->wait_cycles = 0;
   c->inject = 0;
@@ -1398,6 +1400,504 @@ csa2_status_t csa2_index_topk_reindex_decode(const csa2_cache_t* c, int32_t nq, 
   delete hp;
   return st;
 }
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- trees of drafts
+namespace {
+
+// A tree call's queries, one record per draft in call order: the fields of
+// TreeQuery with `rows` the whole path (self included) and win_n the depth;
+// win_row is the sequence's position in the call.
+struct TreePlan {
+  TreeQuery* q = nullptr;
+  int64_t nq = 0;
+  int32_t max_draft = 0;
+  ~TreePlan() { delete[] q; }
+};
+
+// Depth and path (bit a: draft a is on it, self included) of each draft.
+bool tree_paths(int32_t n, const int32_t* parent, int32_t* depth, uint64_t* path) {
+  for (int t = 0; t < n; ++t) {
+    const int32_t a = parent[t];
+    if (a < -1 || a >= t) return false;
+    depth[t] = a < 0 ? 0 : depth[a] + 1;
+    path[t] = (a < 0 ? 0ull : path[a]) | (1ull << t);
+  }
+  return true;
+}
+
+// Checks a tree against the cache and fills the plan.  Every sequence at
+// most once; its cache must hold exactly floor(pos0 / ratio) committed
+// entries and the entries of its drafts.
+csa2_status_t plan_tree(const csa2_cache* c, const csa2_tree_t* t, TreePlan* plan) {
+  if (!c || !t || t->n_seqs < 0) return CSA2_ERR_INVALID_ARG;
+  if (t->n_seqs == 0) return CSA2_OK;
+  if (!t->n_draft || !t->pos0 || t->n_seqs > c->batch) return CSA2_ERR_INVALID_ARG;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
+  if (dev != c->dev) return CSA2_ERR_INVALID_ARG;
+  uint64_t seen[4096 / 64] = {};
+  int64_t nq = 0;
+  for (int i = 0; i < t->n_seqs; ++i) {
+    const int32_t s = t->seq_ids ? t->seq_ids[i] : i, n = t->n_draft[i];
+    if (s < 0 || s >= c->batch || n < 0 || t->pos0[i] < 0 ||
+        t->pos0[i] > INT64_MAX - CSA2_MAX_DRAFT)
+      return CSA2_ERR_INVALID_ARG;
+    if (n > CSA2_MAX_DRAFT) return CSA2_ERR_UNSUPPORTED;
+    if ((seen[s >> 6] >> (s & 63)) & 1u) return CSA2_ERR_INVALID_ARG;
+    seen[s >> 6] |= 1ull << (s & 63);
+    nq += n;
+    plan->max_draft = std::max(plan->max_draft, n);
+  }
+  if (nq > 0 && !t->parent) return CSA2_ERR_INVALID_ARG;
+  plan->q = new (std::nothrow) TreeQuery[(size_t)std::max<int64_t>(nq, 1)];
+  if (!plan->q) return CSA2_ERR_OOM;
+  plan->nq = nq;
+  int64_t first = 0;
+  for (int i = 0; i < t->n_seqs; ++i) {
+    const int32_t s = t->seq_ids ? t->seq_ids[i] : i, n = t->n_draft[i];
+    int32_t depth[CSA2_MAX_DRAFT];
+    uint64_t path[CSA2_MAX_DRAFT];
+    if (!tree_paths(n, t->parent ? t->parent + first : nullptr, depth, path))
+      return CSA2_ERR_INVALID_ARG;
+    const int64_t m = c->cfg.ratio, pos0 = t->pos0[i];
+    uint64_t own = 0;   // drafts that complete a block, and so own an entry
+    for (int j = 0; j < n; ++j)
+      if ((pos0 + depth[j] + 1) % m == 0) own |= 1ull << j;
+    const int64_t n_com = pos0 / m;
+    if (c->len[s] != n_com + __builtin_popcountll(own)) return CSA2_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+      TreeQuery& q = plan->q[first + j];
+      q.base = c->off[s];
+      q.pos = pos0 + depth[j];
+      q.rows = path[j];
+      q.ents = 0;
+      for (uint64_t b = path[j] & own; b; b &= b - 1) {
+        const uint64_t bit = b & (~b + 1);
+        q.ents |= 1ull << __builtin_popcountll(own & (bit - 1));
+      }
+      q.len = (int32_t)c->len[s];
+      q.n_com = (int32_t)n_com;
+      q.win_row = i;
+      q.win_n = depth[j];
+      q.draft0 = (int32_t)first;
+    }
+    first += n;
+  }
+  return CSA2_OK;
+}
+
+int64_t tree_columns(const TreeQuery& q) { return q.n_com + __builtin_popcountll(q.ents); }
+
+// Scores of a planned tree into rows of stride ld.
+csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const TreePlan& plan,
+                             const void* q_idx, const float* w, float* scores, int64_t ld,
+                             uint32_t* key_hist, csa2_stream_t stream) {
+  const int64_t nq = plan.nq;
+  const bool mx = c->cfg.idx_layout == CSA2_IDX_MXFP4;
+  TreeIndexParams* ip = new (std::nothrow) TreeIndexParams();
+  if (!ip) return CSA2_ERR_OOM;
+  csa2_status_t st = CSA2_OK;
+  if (plan.max_draft == 1) {
+    // a single draft a sequence sees every entry: the decode indexer
+    int32_t* ids = new (std::nothrow) int32_t[(size_t)nq];
+    if (!ids) { delete ip; return CSA2_ERR_OOM; }
+    int64_t k = 0;
+    for (int i = 0; i < t->n_seqs; ++i)
+      if (t->n_draft[i]) ids[k++] = t->seq_ids ? t->seq_ids[i] : i;
+    st = run_index_decode(c, (int32_t)nq, q_idx, w, ids, scores, ld, key_hist, stream, ip);
+    delete[] ids;
+    delete ip;
+    return st;
+  }
+  if (key_hist &&
+      cudaMemsetAsync(key_hist, 0, (size_t)nq * kKeyHistBinsHost * sizeof(uint32_t), S(stream)) !=
+          cudaSuccess) {
+    delete ip;
+    return CSA2_ERR_CUDA;
+  }
+  // queries that share a tile of keys
+  const int qpg = mx ? 4 : plan.max_draft <= 2 ? 2 : plan.max_draft <= 4 ? 4 : 8;
+  const uint16_t* qb = static_cast<const uint16_t*>(q_idx);
+  int64_t q0 = 0, done = 0;   // queries before this launch, queries of the sequence already taken
+  int seq = 0;
+  while (seq < t->n_seqs && st == CSA2_OK) {
+    std::memset(ip, 0, sizeof(TreeIndexParams));
+    int n = 0, groups = 0;
+    while (seq < t->n_seqs) {
+      const int T = t->n_draft[seq];
+      if (done >= T) { ++seq; done = 0; continue; }
+      // a sequence's drafts in groups of nearly equal size
+      const int ng = (T + qpg - 1) / qpg;
+      const int g = (int)(done * ng / T) + (done * ng % T != 0);
+      const int size = (int)((int64_t)(g + 1) * T / ng - done);
+      if (n + size > kMaxTreeQueries || groups >= kMaxTreeQueries) break;
+      const TreeQuery& q = plan.q[q0 + n];
+      ip->q_first[groups] = n;
+      ip->n_com[groups] = q.n_com;
+      ip->entry_base[groups] = q.base;
+      ip->nvis[groups] = q.len;
+      for (int j = 0; j < size; ++j) ip->ents[n + j] = plan.q[q0 + n + j].ents;
+      const int64_t lead = (mx && q.len > 0) ? (q.base & 127) : 0;
+      ip->tile_prefix[groups + 1] =
+          ip->tile_prefix[groups] + (int32_t)((q.len + lead + 127) / 128);
+      n += size;
+      ++groups;
+      done += size;
+    }
+    ip->q_first[groups] = n;
+    if (n == 0) break;
+    ip->w = w + q0 * kIdxHeads;
+    ip->scores = scores + q0 * ld;
+    ip->ld = ld;
+    ip->key_hist = key_hist ? key_hist + q0 * kKeyHistBinsHost : nullptr;
+    ip->err = c->d_err;
+    ip->nq = n;
+    ip->qpg = qpg;
+    ip->n_groups = groups;
+    ip->ratio = c->cfg.ratio;
+    ip->wait_cycles = c->wait_cycles;
+    ip->inject = c->inject;
+    const uint16_t* qn = qb + q0 * kIdxHeads * kIdxDim;
+    const int tiles = ip->tile_prefix[groups];
+    q0 += n;
+    if (tiles == 0) continue;
+    const int grid = std::min(c->index_sms, tiles);
+    cudaError_t e;
+    if (mx) {
+      ip->idx_codes = c->idx_codes;
+      ip->idx_scales = c->idx_scales;
+      ip->idx_total = c->total;
+      ip->q_idx = qn;
+      e = launch_index_fp4_tree(*ip, c->tm_kq, grid, S(stream));
+    } else {
+      CUtensorMap tm_q;
+      if (!make_map(&tm_q, qn, (uint64_t)n * kIdxHeads, kIdxDim, 64, 32 * qpg)) {
+        st = CSA2_ERR_CUDA;
+        break;
+      }
+      e = launch_index_tree(*ip, c->tm_k, tm_q, grid, S(stream));
+    }
+    if (e != cudaSuccess) st = CSA2_ERR_CUDA;
+  }
+  delete ip;
+  return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+csa2_status_t csa2_tree_paths(int32_t n_draft, const int32_t* parent, int32_t* depth,
+                              uint64_t* path) {
+  CSA2_RANGE();
+  if (n_draft < 0) return CSA2_ERR_INVALID_ARG;
+  if (n_draft > CSA2_MAX_DRAFT) return CSA2_ERR_UNSUPPORTED;
+  if (n_draft == 0) return CSA2_OK;
+  if (!parent) return CSA2_ERR_INVALID_ARG;
+  int32_t d[CSA2_MAX_DRAFT];
+  uint64_t pt[CSA2_MAX_DRAFT];
+  if (!tree_paths(n_draft, parent, d, pt)) return CSA2_ERR_INVALID_ARG;
+  if (depth) std::memcpy(depth, d, sizeof(int32_t) * n_draft);
+  if (path) std::memcpy(path, pt, sizeof(uint64_t) * n_draft);
+  return CSA2_OK;
+}
+
+csa2_status_t csa2_index_scores_tree(const csa2_cache_t* c, const csa2_tree_t* tree,
+                                     const void* q_idx, const float* w, float* scores, int64_t ld,
+                                     uint32_t* key_hist, csa2_stream_t stream) {
+  CSA2_RANGE();
+  TreePlan plan;
+  csa2_status_t st = plan_tree(c, tree, &plan);
+  if (st != CSA2_OK || plan.nq == 0) return st;
+  if (!q_idx || !w || !scores || !aligned16(q_idx) || !aligned16(w) || !aligned16(scores) ||
+      ld % 4 != 0 || (key_hist && !aligned16(key_hist)))
+    return CSA2_ERR_INVALID_ARG;
+  if (key_hist && c->cfg.idx_layout == CSA2_IDX_MXFP4) return CSA2_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < plan.nq; ++i)
+    if (tree_columns(plan.q[i]) > ld) return CSA2_ERR_CAPACITY;
+  return run_index_tree(c, tree, plan, q_idx, w, scores, ld, key_hist, stream);
+}
+
+csa2_status_t csa2_index_topk_tree(const csa2_cache_t* c, const csa2_tree_t* tree,
+                                   const void* q_idx, const float* w, int32_t* topk_idx,
+                                   float* topk_score, void* workspace, size_t ws_bytes,
+                                   csa2_stream_t stream) {
+  CSA2_RANGE();
+  TreePlan plan;
+  csa2_status_t st = plan_tree(c, tree, &plan);
+  if (st != CSA2_OK || plan.nq == 0) return st;
+  if (!q_idx || !w || !aligned16(q_idx) || !aligned16(w) || !topk_idx || !aligned16(topk_idx) ||
+      !workspace || !aligned16(workspace))
+    return CSA2_ERR_INVALID_ARG;
+  const int64_t nq = plan.nq;
+  if (ws_bytes < csa2_index_workspace_bytes(c, (int32_t)nq)) return CSA2_ERR_CAPACITY;
+  const int64_t ld = score_ld(c->max_cap);
+  const bool mx = c->cfg.idx_layout == CSA2_IDX_MXFP4;
+  float* scores = static_cast<float*>(workspace);
+  uint32_t* hist = reinterpret_cast<uint32_t*>(scores + nq * ld);
+  uint32_t* seg_ws = hist + nq * kKeyHistBinsHost;
+  // the histograms come from the bf16 indexer's epilogue
+  uint32_t* key_hist = mx ? nullptr : hist;
+  st = run_index_tree(c, tree, plan, q_idx, w, scores, ld, key_hist, stream);
+  if (st != CSA2_OK) return st;
+  TopkParams* tp = new (std::nothrow) TopkParams();
+  TreeMapParams* mp = new (std::nothrow) TreeMapParams();
+  if (!tp || !mp) { delete tp; delete mp; return CSA2_ERR_OOM; }
+  const int k = c->cfg.topk;
+  for (int64_t q0 = 0; q0 < nq && st == CSA2_OK; q0 += kTopkTab) {
+    const int n = (int)std::min<int64_t>(kTopkTab, nq - q0);
+    std::memset(tp, 0, sizeof(TopkParams));
+    tp->scores = scores + q0 * ld;
+    tp->ld = ld;
+    tp->rows = n;
+    tp->k = k;
+    tp->idx_out = topk_idx + q0 * k;
+    tp->score_out = topk_score ? topk_score + q0 * k : nullptr;
+    tp->key_hist = key_hist ? key_hist + q0 * kKeyHistBinsHost : nullptr;
+    const int n_seg = topk_segments(c->max_cap);
+    const bool seg = key_hist && n_seg > 2 && n_seg <= 1024;
+    tp->seg_ws = seg ? seg_ws + (size_t)q0 * topk_seg_bytes(1, c->max_cap) / sizeof(uint32_t)
+                     : nullptr;
+    tp->n_seg = seg ? n_seg : 0;
+    tp->err = c->d_err;
+    // columns of a path whose entries are the first drafts' are entries already
+    bool map = false;
+    mp->rows = n;
+    mp->k = k;
+    mp->idx = tp->idx_out;
+    for (int i = 0; i < n; ++i) {
+      const TreeQuery& q = plan.q[q0 + i];
+      tp->n_valid[i] = tree_columns(q);
+      mp->n_com[i] = q.n_com;
+      mp->ents[i] = q.ents;
+      map = map || (q.ents & (q.ents + 1)) != 0;
+    }
+    if (launch_topk(*tp, S(stream)) != cudaSuccess ||
+        (map && launch_tree_map(*mp, S(stream)) != cudaSuccess))
+      st = CSA2_ERR_CUDA;
+  }
+  delete tp;
+  delete mp;
+  return st;
+}
+
+csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* c, const csa2_tree_t* tree,
+                                    int32_t n_layers, const csa2_tree_layer_t* layers,
+                                    const int32_t* swa_len, const int32_t* topk_idx, float scale,
+                                    int32_t rope_out, double rope_base, void* workspace,
+                                    size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_RANGE();
+  TreePlan plan;
+  csa2_status_t st = plan_tree(c, tree, &plan);
+  if (st != CSA2_OK) return st;
+  if (n_layers < 1 || n_layers > CSA2_MAX_ATTN_LAYERS || !layers) return CSA2_ERR_INVALID_ARG;
+  if (rope_out && !(rope_base >= 0.0 && std::isfinite(rope_base))) return CSA2_ERR_INVALID_ARG;
+  const int W = c->cfg.swa;
+  for (int i = 0; swa_len && i < tree->n_seqs; ++i)
+    if (swa_len[i] < 0 || swa_len[i] > W || swa_len[i] > tree->pos0[i]) return CSA2_ERR_INVALID_ARG;
+  const int64_t nq = plan.nq;
+  if (nq == 0) return CSA2_OK;
+  if (!topk_idx || !aligned16(topk_idx) || (workspace && !aligned16(workspace)))
+    return CSA2_ERR_INVALID_ARG;
+  auto off16 = [](const void* x) { return !x || !aligned16(x); };
+  for (int l = 0; l < n_layers; ++l) {
+    const csa2_tree_layer_t& y = layers[l];
+    if (off16(y.q) || off16(y.out) || (y.lse && !aligned16(y.lse))) return CSA2_ERR_INVALID_ARG;
+    if (W == 0) continue;
+    if (y.swa_codes || y.swa_rope || y.swa_scales || y.draft_codes || y.draft_rope ||
+        y.draft_scales) {
+      if (off16(y.swa_codes) || off16(y.swa_rope) || off16(y.draft_codes) ||
+          off16(y.draft_rope) || !y.swa_scales || !y.draft_scales ||
+          (reinterpret_cast<uintptr_t>(y.swa_scales) & 7u) ||
+          (reinterpret_cast<uintptr_t>(y.draft_scales) & 7u))
+        return CSA2_ERR_INVALID_ARG;
+    } else if (off16(y.swa_kv) || off16(y.draft_kv)) {
+      return CSA2_ERR_INVALID_ARG;
+    }
+  }
+  const int H = c->cfg.n_heads, k = c->cfg.topk, G = H / kAttnHeadGroup;
+  TreeAttnParams* p = new (std::nothrow) TreeAttnParams();
+  AttnMaps* maps = new (std::nothrow) AttnMaps();
+  if (!p || !maps) { delete p; delete maps; return CSA2_ERR_OOM; }
+  for (int64_t q0 = 0; q0 < nq && st == CSA2_OK; q0 += kMaxTreeQueries) {
+    const int n = (int)std::min<int64_t>(kMaxTreeQueries, nq - q0);
+    std::memset(p, 0, sizeof(TreeAttnParams));
+    p->topk_idx = topk_idx + q0 * k;
+    p->codes = c->codes;
+    p->scales = c->scales;
+    p->n_layers = n_layers;
+    p->err = c->d_err;
+    p->nq = n;
+    p->n_heads = H;
+    p->topk = k;
+    p->swa = W;
+    p->layout = c->cfg.layout;
+    p->scale = scale;
+    p->scale_log2 = scale * 1.4426950408889634f;
+    // as in decode: two CTAs per (query, head group) while the pairs fit the
+    // SMs in one wave
+    p->splits = workspace && ws_bytes >= kAttnSplitToken &&
+                        2 * (int64_t)n_layers * n * G <= c->num_sms
+                    ? 2
+                    : 1;
+    p->wait_cycles = c->wait_cycles;
+    if (rope_out) {
+      p->rope_out = 1;
+      const double base = rope_base > 0.0 ? rope_base : 10000.0;
+      for (int t = 0; t < 32; ++t) p->rope_theta[t] = std::pow(base, -(double)t / 32.0);
+    }
+    for (int i = 0; i < n; ++i) {
+      TreeQuery& q = p->tq[i];
+      q = plan.q[q0 + i];
+      // the window: the deepest W drafts of the path, then committed rows
+      // back to W rows in all
+      const int s = q.win_row;
+      while (__builtin_popcountll(q.rows) > W) q.rows &= q.rows - 1;
+      const int have = swa_len ? swa_len[s] : (int)std::min<int64_t>(W, tree->pos0[s]);
+      q.win_n = std::max(0, std::min(have, W - (int)__builtin_popcountll(q.rows)));
+      q.win_row = s * W + have - q.win_n;
+    }
+    for (int l = 0; l < n_layers && st == CSA2_OK; ++l) {
+      const csa2_tree_layer_t& y = layers[l];
+      AttnLayer& ly = p->layer[l];
+      ly.out = static_cast<uint16_t*>(y.out) + q0 * H * kHeadDim;
+      ly.lse = y.lse ? y.lse + q0 * H : nullptr;
+      ly.sink = y.sink;
+      TreeLayer& tl = p->tree[l];
+      const uint16_t* qb = static_cast<const uint16_t*>(y.q) + q0 * H * kHeadDim;
+      if (!make_map(&maps->q[l], qb, (uint64_t)n * H, kHeadDim, 64, kAttnHeadGroup)) {
+        st = CSA2_ERR_CUDA;
+        break;
+      }
+      maps->swa[l] = maps->q[l];
+      if (W == 0) continue;
+      if (y.swa_codes) {
+        ly.swa_codes = y.swa_codes;
+        ly.swa_rope = static_cast<const uint16_t*>(y.swa_rope);
+        ly.swa_scales = y.swa_scales;
+        tl.draft_codes = y.draft_codes;
+        tl.draft_rope = static_cast<const uint16_t*>(y.draft_rope);
+        tl.draft_scales = y.draft_scales;
+      } else {
+        tl.draft = static_cast<const uint16_t*>(y.draft_kv);
+        if (!make_map(&maps->swa[l], y.swa_kv, (uint64_t)tree->n_seqs * W, kHeadDim, 64, 128)) {
+          st = CSA2_ERR_CUDA;
+          break;
+        }
+      }
+    }
+    if (st == CSA2_OK && launch_attn_tree(*p, *maps, S(stream)) != cudaSuccess) st = CSA2_ERR_CUDA;
+  }
+  delete p;
+  delete maps;
+  return st;
+}
+
+csa2_status_t csa2_cache_accept_tree(csa2_cache_t* c, const csa2_tree_t* tree,
+                                     const int32_t* accepted, csa2_stream_t stream) {
+  CSA2_RANGE();
+  TreePlan plan;
+  csa2_status_t st = plan_tree(c, tree, &plan);
+  if (st != CSA2_OK) return st;
+  if (tree->n_seqs == 0) return CSA2_OK;
+  if (!accepted) return CSA2_ERR_INVALID_ARG;
+  for (int i = 0; i < tree->n_seqs; ++i)
+    if (accepted[i] < -1 || accepted[i] >= tree->n_draft[i]) return CSA2_ERR_INVALID_ARG;
+  AcceptParams* p = new (std::nothrow) AcceptParams();
+  if (!p) return CSA2_ERR_OOM;
+  int64_t first = 0;
+  for (int i0 = 0; i0 < tree->n_seqs && st == CSA2_OK; i0 += kAcceptTab) {
+    const int n = std::min(kAcceptTab, tree->n_seqs - i0);
+    p->n_segs = n;
+    p->scale_bytes = c->scale_bytes;
+    p->codes = c->codes;
+    p->scales = c->scales;
+    p->idxk = c->idxk;
+    p->idx_codes = c->idx_codes;
+    p->idx_scales = c->idx_scales;
+    p->d_len = c->d_len;
+    for (int i = 0; i < n; ++i) {
+      const int t = i0 + i, s = tree->seq_ids ? tree->seq_ids[t] : t;
+      const int64_t n_com = tree->pos0[t] / c->cfg.ratio;
+      const uint64_t keep = accepted[t] >= 0 ? plan.q[first + accepted[t]].ents : 0;
+      first += tree->n_draft[t];
+      p->seg[i] = {c->off[s] + n_com, keep, s, (int32_t)(n_com + __builtin_popcountll(keep))};
+    }
+    if (launch_accept(*p, S(stream)) != cudaSuccess) { st = CSA2_ERR_CUDA; break; }
+    for (int i = 0; i < n; ++i) c->len[p->seg[i].seq] = p->seg[i].new_len;
+  }
+  delete p;
+  return st;
+}
+
+// ---------------------------------------------------------------- norm + rotation
+csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, float eps,
+                             double rope_base, csa2_stream_t stream) {
+  CSA2_RANGE();
+  if (n_parts < 0 || n_parts > CSA2_MAX_NORM_PARTS || (n_parts > 0 && !parts))
+    return CSA2_ERR_INVALID_ARG;
+  if (!(eps >= 1e-30f) || !std::isfinite(eps) || !(rope_base >= 0.0) || !std::isfinite(rope_base))
+    return CSA2_ERR_INVALID_ARG;
+  NormParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.eps = eps;
+  const double base = rope_base > 0.0 ? rope_base : 10000.0;
+  for (int i = 0; i < n_parts; ++i) {
+    const csa2_norm_part_t& a = parts[i];
+    if (a.n_tokens < 0 || a.n_heads < 1) return CSA2_ERR_INVALID_ARG;
+    if (a.dim != 64 && a.dim != 128 && a.dim != 256 && a.dim != 512) return CSA2_ERR_UNSUPPORTED;
+    if (a.rope_dim < 0 || a.rope_dim > a.dim || a.rope_dim % 8 != 0) return CSA2_ERR_INVALID_ARG;
+    if (a.rope_dim > 2 * kNormMaxPairs) return CSA2_ERR_UNSUPPORTED;
+    if ((a.x_fp32 != 0 && a.x_fp32 != 1) || (a.out_fp32 != 0 && a.out_fp32 != 1))
+      return CSA2_ERR_INVALID_ARG;
+    if (a.n_tokens == 0) continue;
+    if (!a.x || !a.out || !aligned16(a.x) || !aligned16(a.out) ||
+        (a.weight && !aligned16(a.weight)) || (a.rope_dim > 0 && !a.pos) ||
+        (reinterpret_cast<uintptr_t>(a.pos) & 7u))
+      return CSA2_ERR_INVALID_ARG;
+    const int64_t xa = a.x_fp32 ? 4 : 8, oa = a.out_fp32 ? 4 : 8;   // elements of 16 bytes
+    // the stride of an axis of one is not used
+    if ((a.n_tokens > 1 && (a.x_token_stride % xa || a.out_token_stride % oa)) ||
+        (a.n_heads > 1 && (a.x_head_stride % xa || a.out_head_stride % oa)))
+      return CSA2_ERR_INVALID_ARG;
+    NormPart& d = p.part[p.n_parts];
+    d.x = a.x;
+    d.out = a.out;
+    d.weight = a.weight;
+    d.pos = a.pos;
+    d.n_tokens = a.n_tokens;
+    d.n_heads = a.n_heads;
+    d.dim = a.dim;
+    d.rope_dim = a.rope_dim;
+    d.norm = a.norm;
+    d.x_fp32 = a.x_fp32;
+    d.out_fp32 = a.out_fp32;
+    d.x_token = a.x_token_stride;
+    d.x_head = a.x_head_stride;
+    d.out_token = a.out_token_stride;
+    d.out_head = a.out_head_stride;
+    // parts of one rotated width share a row of frequencies
+    int row = 0;
+    while (row < p.n_parts && p.part[row].rope_dim != a.rope_dim) ++row;
+    d.rope_table = row;
+    if (row == p.n_parts)
+      for (int t = 0; t < a.rope_dim / 2; ++t) {
+        // 2^64 * base^(-2t / rope_dim) / (2 pi); below one turn for any base
+        // >= 1, and only the fraction of a turn counts otherwise
+        const double f = std::pow(base, -2.0 * t / a.rope_dim) * 0.15915494309189535;
+        p.turns[row][t] = (uint64_t)((f - std::floor(f)) * 18446744073709551616.0);
+      }
+    ++p.n_parts;
+  }
+  if (p.n_parts == 0) return CSA2_OK;
+  return cuda_status(launch_norm_rope(p, S(stream)));
+}
+
+}  // extern "C"
+
+extern "C" {
 
 csa2_status_t csa2_swa_fp8_quantise(int64_t n_rows, const void* rows, uint8_t* codes, void* rope,
                                     uint8_t* scales, csa2_stream_t stream) {

@@ -96,7 +96,22 @@ struct IndexParams {
   int64_t entry_base[kMaxIdxGroups];       // decode: entry offset of the group's sequence
   int32_t nvis[kMaxIdxGroups];             // decode: visible entries of the group's query
 };
+// Trees of drafted tokens: a group is up to qpg consecutive queries of one
+// sequence; tiles cover the sequence's committed entries and the drafts'
+// entries after them.  Query q sees the committed entries (columns 0 ..
+// n_com - 1 of its row) and the drafts' entries of its own path (bit e of
+// ents[q]: entry n_com + e), which follow in order without gaps.  Tables of
+// at most kMaxTreeQueries queries a launch, so that all of the parameters
+// stay below 32764 bytes.
+constexpr int kMaxTreeQueries = 512;
+struct TreeIndexParams : IndexParams {
+  int32_t q_first[kMaxTreeQueries + 1];  // first query of each group
+  int32_t n_com[kMaxTreeQueries];        // committed entries of the group's sequence
+  uint64_t ents[kMaxTreeQueries];        // per query: its path's entries
+};
 int index_smem_bytes(int qpg);
+cudaError_t launch_index_tree(const TreeIndexParams& p, const CUtensorMap& tm_k,
+                              const CUtensorMap& tm_q, int grid, cudaStream_t s);
 cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
                          int grid, cudaStream_t s);
 // MXFP4 keys (codes [idx_rows, 64], scales [idx_rows, 4], idx_rows a
@@ -111,6 +126,71 @@ cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CU
 int index_fp4_smem_bytes();
 cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
                              const CUtensorMap& tm_kc8, int grid, cudaStream_t s);
+cudaError_t launch_index_fp4_tree(const TreeIndexParams& p, const CUtensorMap& tm_kq, int grid,
+                                  cudaStream_t s);
+
+// ---------------------------------------------------------------- trees of drafts
+// Selected columns of the rows above back to entries: column c >= n_com of
+// row r becomes entry n_com + (the (c - n_com)-th set bit of ents[r]).
+constexpr int kTreeMapTab = 1024;
+struct TreeMapParams {
+  int32_t rows;   // <= kTreeMapTab
+  int32_t k;
+  int32_t* idx;   // [rows, k], rewritten
+  int32_t n_com[kTreeMapTab];
+  uint64_t ents[kTreeMapTab];
+};
+cudaError_t launch_tree_map(const TreeMapParams& p, cudaStream_t s);
+
+// Accepted paths: of the drafts' entries at rows row0 .. of a sequence, those
+// of `keep` (bit e: row row0 + e) move up to row0, row0 + 1, ...
+constexpr int kAcceptTab = 512;
+struct AcceptSeg {
+  int64_t row0;
+  uint64_t keep;
+  int32_t seq;
+  int32_t new_len;
+};
+struct AcceptParams {
+  int32_t n_segs;       // <= kAcceptTab
+  int32_t scale_bytes;  // 16 or 32 per entry
+  uint8_t* codes;
+  uint8_t* scales;
+  uint16_t* idxk;       // bf16 indexer keys, or null: idx_codes and idx_scales
+  uint8_t* idx_codes;
+  uint8_t* idx_scales;
+  int32_t* d_len;
+  AcceptSeg seg[kAcceptTab];
+};
+cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
+
+// ---------------------------------------------------------------- norm + rotation
+constexpr int kNormMaxParts = 8;
+constexpr int kNormMaxPairs = 64;     // rotated channels / 2
+struct NormPart {
+  const void* x;
+  void* out;
+  const float* weight;      // nullable [dim]
+  const int64_t* pos;       // [n_tokens], null without rotation
+  int64_t n_tokens;
+  int64_t x_token, x_head, out_token, out_head;   // strides in elements
+  int32_t n_heads;
+  int32_t dim;              // 64, 128, 256 or 512
+  int32_t rope_dim;         // rotated channels (the last of the head)
+  int32_t norm;             // 0: no norm (weight still applies)
+  int32_t x_fp32, out_fp32;
+  int32_t rope_table;       // row of NormParams::turns
+};
+struct NormParams {
+  NormPart part[kNormMaxParts];
+  int64_t block0[kNormMaxParts + 1];   // first block of each part
+  int32_t n_parts;
+  float eps;
+  // frequency of channel pair t in turns per position, as a 64-bit fraction:
+  // base^(-2t / rope_dim) / (2 pi) * 2^64
+  uint64_t turns[kNormMaxParts][kNormMaxPairs];
+};
+cudaError_t launch_norm_rope(const NormParams& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- HSI
 constexpr int kHsiBlock = 8;   // positions per block of the candidate pool
@@ -183,7 +263,7 @@ struct AttnMaps {
   CUtensorMap q[kAttnMaxLayers];
   CUtensorMap swa[kAttnMaxLayers];
 };
-struct AttnParams {
+struct AttnCommon {
   const int32_t* topk_idx;   // [nq, topk]
   const int32_t* swa_len;    // decode: nullable [nq]
   const uint8_t* codes;
@@ -208,8 +288,33 @@ struct AttnParams {
   double rope_theta[32];     // RoPE frequencies base^(-2t/64) of the 32 channel pairs
   int64_t wait_cycles;       // bounded-wait limit in cycles (0: the default, ~2^31)
   AttnLayer layer[kAttnMaxLayers];
+};
+struct AttnParams : AttnCommon {
   int64_t q_base[kAttnTab];  // decode: entry offset of each query's sequence
   int32_t q_len[kAttnTab];   // decode: entries of each query's sequence
+};
+// Trees of drafted tokens: one record per query (at most kMaxTreeQueries a
+// launch: the parameters stay below 32764 bytes).
+struct TreeQuery {
+  int64_t base;              // entry offset of the sequence
+  int64_t pos;               // position of the draft
+  uint64_t ents;             // drafts' entries on the query's path (bit e: entry n_com + e)
+  uint64_t rows;             // drafts whose window rows it sees (bit t: draft t)
+  int32_t len;               // entries of the sequence, the drafts' among them
+  int32_t n_com;             // committed entries
+  int32_t win_row;           // first committed window row it sees
+  int32_t win_n;             // committed window rows it sees
+  int32_t draft0;            // row of the sequence's first draft
+};
+struct TreeLayer {
+  const uint16_t* draft;         // bf16 rows of the drafts [n_queries, 512], or the FP8 form:
+  const uint8_t* draft_codes;
+  const uint16_t* draft_rope;
+  const uint8_t* draft_scales;
+};
+struct TreeAttnParams : AttnCommon {
+  TreeLayer tree[kAttnMaxLayers];
+  TreeQuery tq[kMaxTreeQueries];
 };
 cudaError_t launch_swa_fp8(const uint16_t* rows, int64_t n, uint8_t* codes, uint16_t* rope,
                            uint8_t* scales, cudaStream_t s);
@@ -219,5 +324,8 @@ constexpr int kAttnHeadGroup = 64;
 // passing a workspace of at least this many bytes.
 constexpr size_t kAttnSplitToken = 16;
 cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, cudaStream_t s);
+cudaError_t launch_attn_tree(const TreeAttnParams& p, const AttnMaps& maps, cudaStream_t s);
+static_assert(sizeof(TreeIndexParams) + 2 * sizeof(CUtensorMap) < 32764, "kernel parameters");
+static_assert(sizeof(TreeAttnParams) + sizeof(AttnMaps) < 32764, "kernel parameters");
 
 }  // namespace csa2

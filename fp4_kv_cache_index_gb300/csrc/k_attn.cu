@@ -29,10 +29,19 @@
 // second, and P^T is written by the softmax one candidate row per thread.  The single KV buffer is refilled in two channel halves: the next
 // tile's first half as soon as the O^T products that read it are done (while
 // the others run), and S^T of that half while the second half is written.
+// Trees of drafted tokens (TreeAttnParams): one query per draft.  Its window
+// tile holds the committed rows still in reach of its position, then the rows
+// of its own path, in position order: the rows that decoding the path token
+// by token would read, in the same tile rows, so the two agree bit for bit.
+// The committed rows come by TMA and the few rows after them (the path's, and
+// zeros up to the tile's end) are written by the workers over what the box
+// brought there, so rows outside the window are never read by the MMAs.
 // Online softmax (base 2) runs across TMEM lanes: each thread holds one
 // candidate row; a head's running maximum moves (with a reduce-scatter over
 // the rows and a rescale of O^T in TMEM) only when a tile holds a logit more
 // than 2^8 above it, and the row sums are kept per thread and reduced once.
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
@@ -64,6 +73,7 @@ struct Small {
   float rope_c[32], rope_s[32];  // output RoPE(-i): cos, sin of each channel pair
   uint32_t tmem;
   uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2];   // [h]: channel half h
+  int32_t draft_row[64];         // trees: row of the j-th draft in the window
 };
 constexpr int kSmemBytes = kSmallOff + (int)sizeof(Small) + 1024;
 
@@ -107,8 +117,10 @@ __device__ __forceinline__ float warp_reduce_scatter16(float (&v)[16], int lane)
   return kMax ? fmaxf(v[0], r) : v[0] + r;
 }
 
+template <class P>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn(const __grid_constant__ AttnParams p, const __grid_constant__ AttnMaps maps) {
+    k_attn(const __grid_constant__ P p, const __grid_constant__ AttnMaps maps) {
+  constexpr bool kTree = std::is_same<P, TreeAttnParams>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -147,7 +159,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t base;
   int32_t len;
   int32_t swa_row0, swa_count;
-  if (p.prefill) {
+  [[maybe_unused]] int32_t n_com = 0, win_n = 0;   // trees: committed entries, committed window rows
+  [[maybe_unused]] uint64_t ents = 0;              // trees: the path's entries
+  if constexpr (kTree) {
+    const TreeQuery& t = p.tq[q];
+    base = t.base;
+    len = t.len;
+    n_com = t.n_com;
+    ents = t.ents;
+    swa_row0 = t.win_row;
+    win_n = t.win_n;
+    swa_count = win_n + __popcll(t.rows);
+    if (tid < 64 && ((t.rows >> tid) & 1u))
+      sm.draft_row[__popcll(t.rows & ((1ull << tid) - 1ull))] = t.draft0 + tid;
+  } else if (p.prefill) {
     base = p.pre_base;
     len = p.pre_len;
     const int64_t pos = p.pos0 + q;
@@ -161,6 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t c = p.swa_len ? p.swa_len[q] : p.swa;
     swa_count = c < 0 ? 0 : (c > p.swa ? p.swa : c);
   }
+  // trees: whether a TMA box brings committed rows
+  const bool swa_box = !kTree || win_n > 0;
 
   // The window tile is always first in the tile list: the CTA that owns it
   // (split 0) loads it now, with the query rows, before anything else.  Both
@@ -179,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&sm.bar_q[h], kHG * kHeadDim);
       for (int c = 4 * h; c < 4 * h + 4; ++c)
         tma_load_2d(qs + c * (kHG * 128), tm_q, 64 * c, q * p.n_heads + hg * kHG, &sm.bar_q[h]);
-      if (swa_first && !ly.swa_codes) {
+      if (swa_first && !ly.swa_codes && swa_box) {
         mbar_arrive_expect_tx(&sm.bar_kv[h], kRows * kHeadDim);
         for (int c = 4 * h; c < 4 * h + 4; ++c)
           tma_load_2d(kv + c * (kRows * 128), tm_swa, 64 * c, swa_row0, &sm.bar_kv[h]);
@@ -205,6 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = tid + j * kThreads;
     if (i >= p.topk) break;
     int32_t s = idx_pre[j];
+    if constexpr (kTree) {
+      // a draft's entry off the query's path is not visible to it
+      if (s >= n_com && s < len && !((ents >> (s - n_com)) & 1u)) s = len;
+    }
     if (s >= 0 && s < len) sm.tile_any[i / kRows] = 1;
     else {
       if (s >= len) bad = true;
@@ -382,6 +413,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto window_piece = [&](int e, int c, int k) -> uint4 {
     const bool live = e < swa_count;
     if (!live) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kTree) {
+      if (e >= win_n) {
+        const TreeLayer& tl = p.tree[layer];
+        const int64_t row = sm.draft_row[e - win_n];
+        if (c == 7) return __ldg(reinterpret_cast<const uint4*>(tl.draft_rope + row * 64) + k);
+        const float sc = ue8m0_value(__ldg(tl.draft_scales + row * 8 + c));
+        const uint2 cc =
+            __ldg(reinterpret_cast<const uint2*>(tl.draft_codes + row * 448 + 64 * c + 8 * k));
+        return e4m3_piece(cc.x, cc.y, sc);
+      }
+    }
     const int64_t row = (int64_t)swa_row0 + e;
     if (c == 7) return __ldg(reinterpret_cast<const uint4*>(ly.swa_rope + row * 64) + k);
     const float sc = ue8m0_value(__ldg(ly.swa_scales + row * 8 + c));
@@ -438,7 +480,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tile < 0 && !ly.swa_codes) {
       // bf16 window rows: loaded by TMA at kernel entry
       if (tid < kRows) sm.row_valid[tid] = tid < swa_count;
-      if (tid == 0) {
+      if constexpr (kTree) {
+        // rows win_n ..: the path's rows, then zeros (a masked row has
+        // weight 0, and 0 times whatever the box brought must stay 0)
+        const uint16_t* draft = p.tree[layer].draft;
+        const int n_pieces = (kRows - win_n) * 64;
+        constexpr int kMine = kRows * 64 / kThreads;
+        auto piece_of = [&](int i) -> uint4 {
+          const int e = win_n + i / 64;
+          if (e >= swa_count) return make_uint4(0u, 0u, 0u, 0u);
+          return __ldg(reinterpret_cast<const uint4*>(
+                           draft + (int64_t)sm.draft_row[e - win_n] * kHeadDim) + (i & 63));
+        };
+        // the first pieces are in flight while the box arrives
+        const uint4 first = tid < n_pieces ? piece_of(tid) : make_uint4(0u, 0u, 0u, 0u);
+        if (win_n > 0) {
+          ok = mbar_wait(&sm.bar_kv[0], 0, p.err, wl) && ok;
+          ok = mbar_wait(&sm.bar_kv[1], 0, p.err, wl) && ok;
+        }
+#pragma unroll 1
+        for (int j = 0; j < kMine; ++j) {
+          const int i = tid + j * kThreads;
+          if (i >= n_pieces) break;
+          *piece_at(win_n + i / 64, (i & 63) >> 3, i & 7) = j == 0 ? first : piece_of(i);
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+          for (int h = 0; h < 2; ++h) {
+            ok = mbar_wait(&sm.bar_q[h], 0, p.err, wl) && ok;
+            tc_fence_after();
+            for (int k = 0; k < 16; ++k) mma_s(16 * h + k);
+          }
+          umma_commit(&sm.bar_mma);
+        }
+      } else if (tid == 0) {
         for (int h = 0; h < 2; ++h) {
           ok = mbar_wait(&sm.bar_kv[h], 0, p.err, wl) && ok;
           ok = mbar_wait(&sm.bar_q[h], 0, p.err, wl) && ok;
@@ -631,7 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // reduced modulo 2 pi in fp64, then its sine and cosine are taken in fp32.
   const bool rope = p.rope_out != 0;
   if (rope && tid < 32) {
-    const double pos = p.prefill ? (double)(p.pos0 + q) : (double)p.rope_pos[q];
+    double pos;
+    if constexpr (kTree) pos = (double)p.tq[q].pos;
+    else pos = p.prefill ? (double)(p.pos0 + q) : (double)p.rope_pos[q];
     const double phi = -pos * p.rope_theta[tid];
     const double turns = rint(phi * 0.15915494309189535);       // 1 / (2 pi)
     const float r = (float)fma(-turns, 6.283185307179586, phi);  // in [-pi, pi]
@@ -806,9 +884,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 int attn_smem_bytes() { return kSmemBytes; }
-cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, cudaStream_t s) {
+namespace {
+template <class P>
+cudaError_t launch_any(const P& p, const AttnMaps& maps, cudaStream_t s) {
   if (p.n_layers < 1 || p.n_layers > kAttnMaxLayers) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_attn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_attn<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (int64_t)p.n_layers * p.nq * (p.n_heads / kHG) * p.splits;
@@ -829,7 +909,16 @@ cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, cudaStream_t 
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, k_attn, p, maps);
+  return cudaLaunchKernelEx(&cfg, k_attn<P>, p, maps);
+}
+}  // namespace
+
+cudaError_t launch_attn(const AttnParams& p, const AttnMaps& maps, cudaStream_t s) {
+  return launch_any(p, maps, s);
+}
+
+cudaError_t launch_attn_tree(const TreeAttnParams& p, const AttnMaps& maps, cudaStream_t s) {
+  return launch_any(p, maps, s);
 }
 
 }  // namespace csa2

@@ -22,6 +22,13 @@
 // apart; pool slots past the sequence score -inf.  Block ids of the next
 // tile are loaded one tile ahead by the producer and by the epilogue.
 //
+// Trees of drafted tokens (TreeIndexParams): the groups are up to qpg
+// consecutive drafts of one sequence, whose tiles cover the committed entries
+// and the drafts' own entries after them.  A draft sees the committed entries
+// and those of its path, whose scores follow the committed ones without gaps
+// (column n_com + rank among the path's entries), so that the row is the one
+// decoding the path token by token would give and the top-k needs no mask.
+//
 // Scores are stored as fp32, or (selector precision of the V4 blog reading,
 // section 7) rounded to bf16 with the histogram taken on the rounded value.
 //
@@ -33,6 +40,8 @@
 // each taking a quarter of the group's queries, so that the ReLU and head sums
 // of a tile's 256 columns run on every scheduler with enough warps to cover
 // the TMEM load latency).  Every wait is bounded.
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
@@ -107,10 +116,11 @@ struct GroupCursor {
 };
 
 // kEpiW epilogue warps: 8 for one query per group, 16 for several.
-template <int kEpiW>
+template <int kEpiW, class P>
 __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
-    k_index(const __grid_constant__ IndexParams p, const __grid_constant__ CUtensorMap tm_k,
+    k_index(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_q) {
+  constexpr bool kTree = std::is_same<P, TreeIndexParams>::value;
   constexpr int kEpiThreads = 32 * kEpiW;
   constexpr int kParts = kEpiW / 4;                      // warps per TMEM lane quadrant
   constexpr int kMaxQ = (kMaxQpg + kParts - 1) / kParts;   // queries of one epilogue thread
@@ -201,9 +211,11 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
         if (lane == 0) {
           ok = mbar_wait(q_empty, qph ^ 1, p.err, wl);
           if (ok) {
+            int q_row = g * qrows;
+            if constexpr (kTree) q_row = p.q_first[g] * 32;
             mbar_arrive_expect_tx(q_full, (uint32_t)(qrows * kIdxDim * 2));
-            tma_load_2d(qbuf, &tm_q, 0, g * qrows, q_full);
-            tma_load_2d(qbuf + qrows * 128, &tm_q, 64, g * qrows, q_full);
+            tma_load_2d(qbuf, &tm_q, 0, q_row, q_full);
+            tma_load_2d(qbuf + qrows * 128, &tm_q, 64, q_row, q_full);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -409,12 +421,22 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     // adds this CTA's counts of group `gg`'s queries to the global
     // histograms and clears hs
     auto esync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); };
+    // first query of group gg, and one past its last
+    auto q_begin = [&](int gg) -> int {
+      if constexpr (kTree) return p.q_first[gg];
+      return gg * p.qpg;
+    };
+    auto q_end = [&](int gg) -> int {
+      if constexpr (kTree) return p.q_first[gg + 1];
+      return p.nq;
+    };
     auto flush = [&](int gg) {
       esync();
+      const int q0 = q_begin(gg), q1 = q_end(gg);
       for (int i = et; i < hbins; i += kEpiThreads) {
         const uint32_t v = hs[i];
-        const int q = gg * p.qpg + i / kKeyHistBins;
-        if (v && q < p.nq) atomicAdd(p.key_hist + (int64_t)q * kKeyHistBins + (i % kKeyHistBins), v);
+        const int q = q0 + i / kKeyHistBins;
+        if (v && q < q1) atomicAdd(p.key_hist + (int64_t)q * kKeyHistBins + (i % kKeyHistBins), v);
         hs[i] = 0u;
       }
       esync();
@@ -426,6 +448,9 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     int cur = -1, acc = 0;
     uint32_t aph = 0;
     int nvis[kMaxQ];   // visible entries of this thread's queries in the current group
+    uint64_t ents[kMaxQ];       // trees: the path's entries of this thread's queries
+    int ncom = 0;               // trees: committed entries of the sequence
+    int qg = 0, qe = 0;         // the group's queries [qg, qe)
     int32_t blk_nxt = (p.pool && begin < end) ? pool_blk(begin, c0, row >> 3) : -1;
     for (int it = begin; it < end; ++it) {
       gc.advance(p, it);
@@ -435,15 +460,23 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       if (g != cur) {
         if (use_hist && cur >= 0) flush(cur);
         esync();
+        qg = q_begin(g);
+        qe = q_end(g);
         for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = g * p.qpg + (i >> 5);
-          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          const int q = qg + (i >> 5);
+          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
         }
         esync();
         cur = g;
 #pragma unroll
         for (int jj = 0; jj < kMaxQ; ++jj)
           nvis[jj] = (j0 + jj < j1) ? group_nvis_query(p, g, j0 + jj) : 0;
+        if constexpr (kTree) {
+          ncom = p.n_com[g];
+#pragma unroll
+          for (int jj = 0; jj < kMaxQ; ++jj)
+            ents[jj] = (j0 + jj < j1 && qg + j0 + jj < qe) ? p.ents[qg + j0 + jj] : 0u;
+        }
       }
       if (!mbar_wait(acc_full + acc, aph, p.err, wl)) break;
       tc_fence_after();
@@ -452,8 +485,22 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       // score of query j of the group from its 32 head columns r
       auto emit = [&](int j, int jj, const uint32_t (&r)[32]) {
         const float s = relu_dot32(wbuf + j * 32, r);
-        const int q = g * p.qpg + j;
+        const int q = qg + j;
         const int nv = nvis[jj];
+        if constexpr (kTree) {
+          if (q >= qe || e >= nv) return;
+          int col = e;
+          if (e >= ncom) {
+            // a draft's entry: the path's only, in the order of the path
+            const int b = e - ncom;
+            if (!((ents[jj] >> b) & 1u)) return;
+            col = ncom + __popcll(ents[jj] & ((1ull << b) - 1ull));
+          }
+          if (!CSA2_IN_BOUNDS(col < p.ld, p.err)) return;
+          p.scores[(int64_t)q * p.ld + col] = s;
+          if (use_hist) atomicAdd(hs + j * kKeyHistBins + (score_key(s) >> 21), 1u);
+          return;
+        }
         if (p.pool) {
           // slot t * 128 + row of the pool; its entry decides validity
           const int64_t ent = (int64_t)blk * 8 + (row & 7);
@@ -528,13 +575,12 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
 
 int index_smem_bytes(int qpg) { return smem_layout(qpg).total; }
 
-cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
-                         int grid, cudaStream_t s) {
-  // the epilogue covers at most kMaxQpg queries per tile (N <= 256)
-  if (p.qpg < 1 || p.qpg > kMaxQpg) return cudaErrorInvalidValue;
+namespace {
+template <class P>
+cudaError_t launch_any(void (*kern)(P, CUtensorMap, CUtensorMap), int epi_warps, const P& p,
+                       const CUtensorMap& tm_k, const CUtensorMap& tm_q, int grid,
+                       cudaStream_t s) {
   const int smem = index_smem_bytes(p.qpg);
-  const int epi_warps = p.qpg == 1 ? 8 : 16;
-  auto* kern = p.qpg == 1 ? k_index<8> : k_index<16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -546,6 +592,21 @@ cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CU
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p, tm_k, tm_q);
+}
+}  // namespace
+
+cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_q,
+                         int grid, cudaStream_t s) {
+  // the epilogue covers at most kMaxQpg queries per tile (N <= 256)
+  if (p.qpg < 1 || p.qpg > kMaxQpg) return cudaErrorInvalidValue;
+  return p.qpg == 1 ? launch_any(k_index<8, IndexParams>, 8, p, tm_k, tm_q, grid, s)
+                    : launch_any(k_index<16, IndexParams>, 16, p, tm_k, tm_q, grid, s);
+}
+
+cudaError_t launch_index_tree(const TreeIndexParams& p, const CUtensorMap& tm_k,
+                              const CUtensorMap& tm_q, int grid, cudaStream_t s) {
+  if (p.qpg < 2 || p.qpg > kMaxQpg) return cudaErrorInvalidValue;
+  return launch_any(k_index<16, TreeIndexParams>, 16, p, tm_k, tm_q, grid, s);
 }
 
 }  // namespace csa2

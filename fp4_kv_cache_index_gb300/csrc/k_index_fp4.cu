@@ -50,7 +50,13 @@
 // Tiles: 512 keys (four M = 128 groups) for one query per group over
 // contiguous keys (decode), 512 pool slots (four M-groups) in pool mode, 128
 // keys for four queries per group (prefill, N = 128).
+// Trees of drafted tokens (TreeIndexParams): four consecutive drafts of one
+// sequence per group; the drafts' own entries follow the committed ones in
+// the cache, and a draft stores the scores of its path's entries after the
+// committed ones without gaps (as in the bf16 indexer).
 // Every wait is bounded.
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
@@ -249,9 +255,11 @@ __device__ __forceinline__ void prep_query_block(const uint16_t* src, bool live,
   batom[(n & 31) * 16 + ((n >> 5) & 3) * 4 + b] = (uint8_t)sb;
 }
 
+template <class P>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_index_fp4(const __grid_constant__ IndexParams p, const __grid_constant__ CUtensorMap tm_kq,
+    k_index_fp4(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_kq,
                 const __grid_constant__ CUtensorMap tm_kc8) {
+  constexpr bool kTree = std::is_same<P, TreeIndexParams>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -275,7 +283,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int N = 32 * p.qpg;                      // MMA N
-  const bool pool = p.pool != nullptr;
+  const bool pool = !kTree && p.pool != nullptr;
+  // first query of group g, and one past its last
+  auto q_begin = [&](int g) -> int {
+    if constexpr (kTree) return p.q_first[g];
+    return g * p.qpg;
+  };
+  auto q_end = [&](int g) -> int {
+    if constexpr (kTree) return p.q_first[g + 1];
+    return p.nq;
+  };
   // keys (pool slots) per tile: 512 for one query (contiguous keys, or 64
   // pool blocks of 8), 128 for four queries
   const int tile_e = p.qpg == 1 ? 512 : 128;
@@ -460,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync 2, 64;" ::: "memory");   // both warps: zeroed before any scale byte
       for (int item = pt; item < qrows * 4; item += kPrepThreads) {
         const int n = item >> 2, b = item & 3;
-        const int q = cur * p.qpg + (n >> 5);
-        const bool live = q < p.nq;
+        const int q = q_begin(cur) + (n >> 5);
+        const bool live = q < q_end(cur);
         const uint16_t* src = p.q_idx + ((int64_t)q * kIdxHeads + (n & 31)) * kIdxDim + b * 32;
         prep_query_block(src, live, bc, ba, n, b);
       }
@@ -577,15 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cur = -1, acc = 0, t_first = 0;
     uint32_t aph = 0;
     int nv[2] = {0, 0};   // visible entries of this thread's queries
+    uint64_t ents[2] = {0, 0};   // trees: the path's entries of this thread's queries
+    int ncom = 0;                // trees: committed entries of the sequence
+    int qg = 0, qe = 0;          // the group's queries [qg, qe)
     for (int it = begin; it < end; ++it) {
       gc.advance(p, it);
       const int g = gc.g;
       if (g != cur) {
         if (use_hist && cur >= 0) flush(cur);
         esync();
+        qg = q_begin(g);
+        qe = q_end(g);
         for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = g * p.qpg + (i >> 5);
-          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          const int q = qg + (i >> 5);
+          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
         }
         if (pool) {
           // the block ids of this CTA's tiles of the group, loaded once
@@ -604,16 +626,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           nv[0] = group_nvis_query(p, g, 2 * half);
           nv[1] = group_nvis_query(p, g, 2 * half + 1);
         }
+        if constexpr (kTree) {
+          ncom = p.n_com[g];
+          const int q = qg + 2 * half;
+          ents[0] = q < qe ? p.ents[q] : 0u;
+          ents[1] = q + 1 < qe ? p.ents[q + 1] : 0u;
+        }
       }
       if (!mbar_wait_sleep(acc_full + acc, aph, p.err, wl)) break;
       tc_fence_after();
       const int t = it - gc.lo;
       const int lead = lead_of(gc);
       const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * acc_cols);
-      // score s of query q at slot `row` of the tile: entry e (pool mode: the
+      // score s of query q (trees: with the entries `path`) at slot `row` of the tile: entry e (pool mode: the
       // pool slot, whose block decides validity)
-      auto store = [&](int row, int q, int nvis, float s) {
+      auto store = [&](int row, int q, int nvis, uint64_t path, float s) {
         const int e = t * tile_e + slot_key(row) - lead;
+        if constexpr (kTree) {
+          if (q >= qe || e < 0 || e >= nvis) return;
+          int col = e;
+          if (e >= ncom) {
+            // a draft's entry: the path's only, in the order of the path
+            const int b = e - ncom;
+            if (!((path >> b) & 1u)) return;
+            col = ncom + __popcll(path & ((1ull << b) - 1ull));
+          }
+          if (CSA2_IN_BOUNDS(col < p.ld, p.err)) p.scores[(int64_t)q * p.ld + col] = s;
+          return;
+        }
         if (pool) {
           int32_t blk = -1;
           if (t * blocks_per_tile + (row >> 3) < p.pool_blocks)
@@ -641,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, g, nv[0], relu_dot32(wbuf, r));
+        store(slot0, g, nv[0], ents[0], relu_dot32(wbuf, r));
       } else if (p.qpg == 1) {
         // M-groups 2 half and 2 half + 1: columns N apart
         uint32_t ra[32], rb[32];
@@ -650,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, g, nv[0], relu_dot32(wbuf, ra));
-        store(slot0 + 128, g, nv[0], relu_dot32(wbuf, rb));
+        store(slot0, g, nv[0], ents[0], relu_dot32(wbuf, ra));
+        store(slot0 + 128, g, nv[0], ents[0], relu_dot32(wbuf, rb));
       } else {
         uint32_t ra[32], rb[32];
         const int j = 2 * half;
@@ -659,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, g * p.qpg + j, nv[0], relu_dot32(wbuf + j * 32, ra));
-        store(slot0, g * p.qpg + j + 1, nv[1], relu_dot32(wbuf + (j + 1) * 32, rb));
+        store(slot0, qg + j, nv[0], ents[0], relu_dot32(wbuf + j * 32, ra));
+        store(slot0, qg + j + 1, nv[1], ents[1], relu_dot32(wbuf + (j + 1) * 32, rb));
       }
       if (++acc == nacc) { acc = 0; aph ^= 1; }
     }
@@ -679,11 +719,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int index_fp4_smem_bytes() { return smem_layout().total; }
 
-cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
-                             const CUtensorMap& tm_kc8, int grid, cudaStream_t s) {
-  if (p.qpg != 1 && p.qpg != kMaxQpg) return cudaErrorInvalidValue;
+namespace {
+template <class P>
+cudaError_t launch_any(const P& p, const CUtensorMap& tm_kq, const CUtensorMap& tm_kc8, int grid,
+                       cudaStream_t s) {
   const int smem = index_fp4_smem_bytes();
-  cudaError_t e = cudaFuncSetAttribute(k_index_fp4, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(k_index_fp4<P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -694,7 +735,20 @@ cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_index_fp4, p, tm_kq, tm_kc8);
+  return cudaLaunchKernelEx(&cfg, k_index_fp4<P>, p, tm_kq, tm_kc8);
+}
+}  // namespace
+
+cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
+                             const CUtensorMap& tm_kc8, int grid, cudaStream_t s) {
+  if (p.qpg != 1 && p.qpg != kMaxQpg) return cudaErrorInvalidValue;
+  return launch_any(p, tm_kq, tm_kc8, grid, s);
+}
+
+cudaError_t launch_index_fp4_tree(const TreeIndexParams& p, const CUtensorMap& tm_kq, int grid,
+                                  cudaStream_t s) {
+  if (p.qpg != kMaxQpg) return cudaErrorInvalidValue;
+  return launch_any(p, tm_kq, tm_kq, grid, s);
 }
 
 }  // namespace csa2

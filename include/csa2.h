@@ -623,6 +623,152 @@ csa2_status_t csa2_sparse_attn_prefill_layers(const csa2_cache_t* cache, int32_t
                                               const csa2_attn_opts_t* const* opts,
                                               csa2_stream_t stream);
 
+/* ---- norms and rotation before the attention ----------------------------
+ * RMS norm of every head and the position rotation of its last channels, for
+ * several tensors in one launch (a step's queries, KV rows, indexer queries
+ * and indexer keys):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (norm 0: y = x * weight),
+ *   channel pairs (dim - rope_dim + 2t, dim - rope_dim + 2t + 1) of y rotated
+ *   by the angle pos * rope_base^(-2t / rope_dim),
+ * in fp32, rounded once to the output's type.  The readout's output RoPE(-i)
+ * (csa2_attn_opts_t) undoes the rotation at the query's position.  The pages
+ * norm queries and KV rows per head and quantise after the rotation ([V41 sec
+ * 2.4.4], [V4B sec 4.3]); they give no norm for the indexer's tensors: the
+ * caller chooses per part.
+ *   x, out: dev bf16, or fp32 with x_fp32 / out_fp32 = 1; [n_tokens, n_heads,
+ *     dim] with the given strides in elements (the channels of a head are
+ *     contiguous); every head 16-byte aligned.  out may be x with the same
+ *     type and strides; any other overlap is not allowed, nor may two heads
+ *     of an output overlap.
+ *   weight: nullable dev fp32 [dim];  pos: dev int64 [n_tokens] (may be NULL
+ *     without rotation), any value;  dim: 64, 128, 256 or 512 (else
+ *     CSA2_ERR_UNSUPPORTED);  rope_dim: 0 (no rotation) up to dim, a multiple
+ *     of 8, at most 128.
+ *   eps: at least 1e-30 (finite);  rope_base: 0 means 10000.
+ * A head that holds an infinity or a NaN gives what the formula gives.      */
+#define CSA2_MAX_NORM_PARTS 8
+typedef struct {
+  const void* x;
+  void* out;
+  const float* weight;
+  const int64_t* pos;
+  int64_t n_tokens;
+  int64_t x_token_stride, x_head_stride, out_token_stride, out_head_stride;
+  int32_t n_heads;
+  int32_t dim;
+  int32_t rope_dim;
+  int32_t norm;
+  int32_t x_fp32, out_fp32;
+} csa2_norm_part_t;
+csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, float eps,
+                             double rope_base, csa2_stream_t stream);
+
+/* ---- trees of drafted tokens --------------------------------------------
+ * Speculative decoding checks a tree of drafted tokens per sequence in one
+ * step.  The pages decode with drafts ([V41], speculative decoding) but give
+ * no kernel for it: these calls compute for every draft exactly what the
+ * decode calls would compute if the draft's path were decoded token by token.
+ *
+ * Sequence seq_ids[i] holds pos0[i] committed tokens, and draft t < n_draft[i]
+ * of its tree continues draft parent[t] (an index in the same tree, below t)
+ * or, with -1, the last committed token.  A draft at depth d (0 for parent
+ * -1) sits at position pos0[i] + d; its path is itself and its ancestors.
+ *
+ * The drafts' entries are appended to the cache before the calls: a draft
+ * whose position completes a block, (position + 1) % ratio == 0, owns one
+ * entry (at ratio 1 every draft does), appended after the committed ones in
+ * draft order, compressed from its path's last `ratio` tokens.  The sequence
+ * then holds floor(pos0 / ratio) committed entries and the drafts' entries;
+ * any other length is CSA2_ERR_INVALID_ARG (so is a sequence listed twice).
+ * A draft sees the committed entries and its path's entries.
+ *
+ * Queries are the drafts of all sequences in call order, sum n_draft of them.
+ *   seq_ids: host [n_seqs], or NULL (tree i belongs to sequence i);  n_draft:
+ *   host [n_seqs], 0 .. CSA2_MAX_DRAFT;  pos0: host int64 [n_seqs];  parent:
+ *   host [sum n_draft].                                                     */
+#define CSA2_MAX_DRAFT 64
+typedef struct {
+  int32_t n_seqs;
+  const int32_t* seq_ids;
+  const int32_t* n_draft;
+  const int64_t* pos0;
+  const int32_t* parent;
+} csa2_tree_t;
+
+/* Depth of each draft of one tree and its path as a bit mask (bit t: draft t
+ * is on it, itself included); host only.  depth, path: nullable host
+ * [n_draft].                                                                */
+csa2_status_t csa2_tree_paths(int32_t n_draft, const int32_t* parent, int32_t* depth,
+                              uint64_t* path);
+
+/* Index scores of the drafts (as csa2_index_scores_decode): row q of scores
+ * holds the committed entries' scores at columns 0 .. n_com - 1, then those
+ * of its path's entries in path order: the row that decoding the path token
+ * by token would give.  Columns past them are left untouched.
+ *   q_idx: dev bf16 [n_queries, idx_heads, idx_dim];  w: dev fp32 [n_queries,
+ *   idx_heads];  scores: dev fp32 [n_queries, ld], ld a multiple of 4 and at
+ *   least the longest row (else CSA2_ERR_CAPACITY);  key_hist: nullable dev
+ *   uint32 [n_queries, 2048], the rows' score-key histograms (bf16 indexer
+ *   keys only: CSA2_ERR_UNSUPPORTED with MXFP4 keys).                        */
+csa2_status_t csa2_index_scores_tree(const csa2_cache_t* cache, const csa2_tree_t* tree,
+                                     const void* q_idx, const float* w, float* scores,
+                                     int64_t ld, uint32_t* key_hist, csa2_stream_t stream);
+
+/* Full-mode selection for the drafts: the top-k of those rows (rule and
+ * output of csa2_index_topk_decode), as entries of the cache: an index >=
+ * floor(pos0 / ratio) names a draft's entry.  topk_score: nullable;
+ * workspace: csa2_index_workspace_bytes(cache, n_queries).                  */
+csa2_status_t csa2_index_topk_tree(const csa2_cache_t* cache, const csa2_tree_t* tree,
+                                   const void* q_idx, const float* w, int32_t* topk_idx,
+                                   float* topk_score, void* workspace, size_t workspace_bytes,
+                                   csa2_stream_t stream);
+
+/* Readout of the drafts for n_layers layers of a group in one launch (as
+ * csa2_sparse_attn_decode_layers).  A draft's window is the rows of the swa
+ * newest positions up to its own: the rows of its path, and before them the
+ * committed rows still in reach.  Layer l:
+ *   q, out: dev bf16 [n_queries, n_heads, head_dim];  lse: nullable dev fp32
+ *   [n_queries, n_heads];  sink: nullable dev fp32 [n_heads];
+ *   swa_kv: dev bf16 [n_seqs, swa, head_dim], the first swa_len[i] rows of
+ *   tree i are its newest committed rows in position order (the last one at
+ *   position pos0[i] - 1);  draft_kv: dev bf16 [n_queries, head_dim], the
+ *   drafts' own rows;  or both in FP8 (csa2_swa_fp8_quantise): all six FP8
+ *   pointers, swa_kv and draft_kv then ignored.  None are read at swa = 0.
+ * swa_len: host [n_seqs], at most swa and pos0 (NULL: as many as that);
+ * topk_idx: dev int32 [n_queries, topk] from csa2_index_topk_tree (an index
+ * of an entry that the draft does not see is skipped and sets CSA2_ERR_DEVICE
+ * in the device error word);  rope_out: 1 rotates each output by minus its
+ * draft's position (csa2_attn_opts_t), rope_base 0 means 10000;  workspace:
+ * as for csa2_sparse_attn_decode.
+ * The result is the decode readout's of the same path, bit for bit when both
+ * split a query's candidates over the same number of CTAs.                  */
+typedef struct {
+  const void* q;
+  const void* swa_kv;
+  const void* draft_kv;
+  void* out;
+  float* lse;
+  const float* sink;
+  const uint8_t* swa_codes;
+  const void* swa_rope;
+  const uint8_t* swa_scales;
+  const uint8_t* draft_codes;
+  const void* draft_rope;
+  const uint8_t* draft_scales;
+} csa2_tree_layer_t;
+csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t* tree,
+                                    int32_t n_layers, const csa2_tree_layer_t* layers,
+                                    const int32_t* swa_len, const int32_t* topk_idx, float scale,
+                                    int32_t rope_out, double rope_base, void* workspace,
+                                    size_t workspace_bytes, csa2_stream_t stream);
+
+/* Ends the step: of tree i the path of draft accepted[i] (-1: none) becomes
+ * committed.  Its entries move up behind the committed ones, the other
+ * drafts' entries are dropped and the sequence's length follows; a next
+ * tree's pos0 is pos0[i] + the path's length.  accepted: host [n_seqs].     */
+csa2_status_t csa2_cache_accept_tree(csa2_cache_t* cache, const csa2_tree_t* tree,
+                                     const int32_t* accepted, csa2_stream_t stream);
+
 /* ---- errors ------------------------------------------------------------ */
 
 /* Reads and clears the cache's sticky device error word (synchronises
