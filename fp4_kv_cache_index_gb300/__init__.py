@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -77,19 +78,27 @@ class TreeStruct(ctypes.Structure):
 
 
 class TreeLayer(ctypes.Structure):
-    """csa2_tree_layer_t: one layer of a drafted tree's readout."""
+    """csa2_tree_layer_t: one layer of a drafted tree's readout (_TREE_LAYER
+    packs the same fields)."""
     _fields_ = [(f, ctypes.c_void_p) for f in
                 ("q", "swa_kv", "draft_kv", "out", "lse", "sink", "swa_codes", "swa_rope",
                  "swa_scales", "draft_codes", "draft_rope", "draft_scales")]
 
 
 class NormPart(ctypes.Structure):
-    """csa2_norm_part_t: one tensor of a norm + rotation call."""
+    """csa2_norm_part_t: one tensor of a norm + rotation call (_NORM_PART packs
+    the same fields)."""
     _fields_ = ([(f, ctypes.c_void_p) for f in ("x", "out", "weight", "pos")] +
                 [(f, ctypes.c_int64) for f in ("n_tokens", "x_token_stride", "x_head_stride",
                                                "out_token_stride", "out_head_stride")] +
                 [(f, ctypes.c_int32) for f in ("n_heads", "dim", "rope_dim", "norm", "x_fp32",
                                                "out_fp32")])
+
+
+_NORM_PART = struct.Struct("@4P5q6i")
+_TREE_LAYER = struct.Struct("@12P")
+assert _NORM_PART.size == ctypes.sizeof(NormPart)
+assert _TREE_LAYER.size == ctypes.sizeof(TreeLayer)
 
 
 def _load():
@@ -176,7 +185,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None):
+def _stream(stream=None, device: Optional[int] = None):
+    """The launch stream; `device`: the current device where the caller has
+    it, which spares the lookup."""
+    if stream is None and device is not None:
+        return torch._C._cuda_getCurrentRawStream(device)
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -665,11 +678,10 @@ def csa2_swa_fp8_quantise(rows: torch.Tensor, stream=None):
 
 
 # ------------------------------------------------------------------ norms and rotation
-def _shaped(t: torch.Tensor, shape, dtype, what: str):
-    """Device pointer of a dense CUDA tensor of this shape and type on the
-    current device."""
-    if (t.shape != shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda
-            or t.get_device() != torch.cuda.current_device()):
+def _shaped(t: torch.Tensor, shape, dtype, what: str, dev: int):
+    """Device pointer of a dense tensor of this shape and type on CUDA device
+    `dev`, the current one."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
                          f"the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -699,45 +711,43 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
         raise ValueError("csa2_norm_rope: at most 8 tensors")
     if outs is None:
         outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-    if weights is None:
-        weights = (None,) * n
     one_pos, one_dim = isinstance(positions, torch.Tensor), isinstance(rope_dim, int)
-    if (len(outs) != n or len(weights) != n or (norms is not None and len(norms) != n)
+    if (len(outs) != n or (weights is not None and len(weights) != n)
+            or (norms is not None and len(norms) != n)
             or (not one_pos and len(positions) != n) or (not one_dim and len(rope_dim) != n)):
         raise ValueError("csa2_norm_rope: one entry per tensor expected")
-    parts = (NormPart * max(n, 1))()
     dev = torch.cuda.current_device()
     bf16, f32 = torch.bfloat16, torch.float32
+    parts, pos, pos_at, n_pos = [], None, 0, -1
     for i in range(n):
-        x, y, w, d = xs[i], outs[i], weights[i], parts[i]
-        pos = positions if one_pos else positions[i]
-        shape, xt, yt = x.shape, x.dtype, y.dtype
-        if (x.dim() not in (2, 3) or y.shape != shape or x.get_device() != dev
+        x, y = xs[i], outs[i]
+        shape, xt, yt, sx, sy = x.shape, x.dtype, y.dtype, x.stride(), y.stride()
+        if (len(shape) not in (2, 3) or y.shape != shape or x.get_device() != dev
                 or y.get_device() != dev or (xt != bf16 and xt != f32)
                 or (yt != bf16 and yt != f32)):
             raise ValueError("csa2_norm_rope: bf16 or fp32 tensors [n, heads, dim] or [n, dim] on "
                              "the current device expected")
-        sx, sy = x.stride(), y.stride()
         if (sx[-1] != 1 or sy[-1] != 1) and shape[-1] > 1:
             raise ValueError("csa2_norm_rope: the channels of a head must be contiguous")
-        d.x, d.out = x.data_ptr(), y.data_ptr()
-        if w is not None:
-            d.weight = _shaped(w, shape[-1:], f32, "weight")
-        r = rope_dim if one_dim else rope_dim[i]
+        tokens, dim, r, w = shape[0], shape[-1], rope_dim if one_dim else rope_dim[i], 0
         if r:
-            d.pos = _shaped(pos, shape[:1], torch.int64, "positions")
-        d.n_tokens, d.dim, d.rope_dim = shape[0], shape[-1], r
-        d.x_token_stride, d.out_token_stride = sx[0], sy[0]
+            p = positions if one_pos else positions[i]
+            if p is not pos or tokens != n_pos:   # once for tensors that share them
+                pos, n_pos = p, tokens
+                pos_at = _shaped(p, (tokens,), torch.int64, "positions", dev)
+        if weights is not None and weights[i] is not None:
+            w = _shaped(weights[i], (dim,), f32, "weight", dev)
         if len(shape) == 3:
-            if shape[1] == 0:
-                d.n_tokens, d.n_heads = 0, 1
-            else:
-                d.n_heads, d.x_head_stride, d.out_head_stride = shape[1], sx[1], sy[1]
+            heads, xh, yh = shape[1], sx[1], sy[1]
+            if heads == 0:
+                tokens, heads = 0, 1
         else:
-            d.n_heads = 1
-        d.norm = 1 if norms is None or norms[i] else 0
-        d.x_fp32, d.out_fp32 = xt == f32, yt == f32
-    _check(lib.csa2_norm_rope(n, parts, eps, rope_base, _stream(stream)), "csa2_norm_rope")
+            heads, xh, yh = 1, 0, 0
+        parts.append(_NORM_PART.pack(x.data_ptr(), y.data_ptr(), w, pos_at if r else 0, tokens,
+                                     sx[0], xh, sy[0], yh, heads, dim, r,
+                                     1 if norms is None or norms[i] else 0, xt == f32, yt == f32))
+    _check(lib.csa2_norm_rope(n, b"".join(parts), eps, rope_base, _stream(stream, dev)),
+           "csa2_norm_rope")
     return list(outs)
 
 
@@ -793,15 +803,15 @@ def csa2_index_scores_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: tor
     [n_queries, 32], scores fp32 [n_queries, ld]: the committed entries' scores,
     then those of the draft's path; key_hist: int32 [n_queries, 2048] (bf16
     keys)."""
-    nq, c = tree.n_queries, cache.cfg
+    nq, c, dev = tree.n_queries, cache.cfg, torch.cuda.current_device()
     ld = scores.shape[-1]
     _check(lib.csa2_index_scores_tree(
         cache.handle, tree.ref,
-        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx"),
-        _shaped(w, (nq, c.idx_heads), torch.float32, "w"),
-        _shaped(scores, (nq, ld), torch.float32, "scores"), ld,
-        None if key_hist is None else _shaped(key_hist, (nq, 2048), torch.int32, "key_hist"),
-        _stream(stream)), "csa2_index_scores_tree")
+        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx", dev),
+        _shaped(w, (nq, c.idx_heads), torch.float32, "w", dev),
+        _shaped(scores, (nq, ld), torch.float32, "scores", dev), ld,
+        None if key_hist is None else _shaped(key_hist, (nq, 2048), torch.int32, "key_hist", dev),
+        _stream(stream, dev)), "csa2_index_scores_tree")
     return scores
 
 
@@ -811,7 +821,7 @@ def csa2_index_topk_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: torch
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Selection of the drafts among the committed entries and their path's;
     int32 [n_queries, topk] entries of the cache, ascending, -1 padded."""
-    nq, c = tree.n_queries, cache.cfg
+    nq, c, dev = tree.n_queries, cache.cfg, torch.cuda.current_device()
     if topk_idx is None:
         topk_idx = torch.empty(nq, c.topk, dtype=torch.int32, device=q_idx.device)
     ws = workspace
@@ -819,12 +829,12 @@ def csa2_index_topk_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: torch
         ws = _scratch(csa2_index_workspace_bytes(cache, nq), q_idx.device, stream)
     _check(lib.csa2_index_topk_tree(
         cache.handle, tree.ref,
-        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx"),
-        _shaped(w, (nq, c.idx_heads), torch.float32, "w"),
-        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx"),
+        _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx", dev),
+        _shaped(w, (nq, c.idx_heads), torch.float32, "w", dev),
+        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx", dev),
         None if topk_score is None else _shaped(topk_score, (nq, c.topk), torch.float32,
-                                                "topk_score"),
-        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "csa2_index_topk_tree")
+                                                "topk_score", dev),
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, dev)), "csa2_index_topk_tree")
     return topk_idx
 
 
@@ -871,47 +881,48 @@ def csa2_sparse_attn_tree_layers(cache: Cache, tree: Tree, qs: Sequence[torch.Te
     outputs."""
     nq, S, c, L = tree.n_queries, tree.n_seqs, cache.cfg, len(qs)
     H, D, W, bf16 = c.n_heads, c.head_dim, c.swa, torch.bfloat16
+    dev = torch.cuda.current_device()
     if outs is None:
         outs = [torch.empty(q.shape, dtype=q.dtype, device=q.device) for q in qs]
-    for name, xs in (("outs", outs), ("lses", lses), ("sinks", sinks), ("swa_kvs", swa_kvs),
-                     ("draft_kvs", draft_kvs), ("swa_fp8s", swa_fp8s),
-                     ("draft_fp8s", draft_fp8s)):
+    for xs in (outs, lses, sinks, swa_kvs, draft_kvs, swa_fp8s, draft_fp8s):
         if xs is not None and len(xs) != L:
-            raise ValueError(f"csa2_sparse_attn_tree_layers: one of {name} per layer expected")
+            raise ValueError("csa2_sparse_attn_tree_layers: one entry per layer expected")
     if (swa_fp8s is None) != (draft_fp8s is None):
         raise ValueError("csa2_sparse_attn_tree_layers: window and drafted rows of one format")
     if swa_len is not None and len(swa_len) != S:
         raise ValueError("csa2_sparse_attn_tree_layers: one swa_len per tree expected")
-    layers = (TreeLayer * L)()
+    if W and swa_fp8s is None and (swa_kvs is None or draft_kvs is None):
+        raise ValueError("csa2_sparse_attn_tree_layers: window and drafted rows expected")
+
+    def fp8(rows, n, what):
+        codes, rope, scales = rows
+        return (_shaped(codes.view(n, codes.shape[-1]), (n, 448), torch.uint8, what, dev),
+                _shaped(rope.view(n, rope.shape[-1]), (n, 64), bf16, what, dev),
+                _shaped(scales.view(n, scales.shape[-1]), (n, 8), torch.uint8, what, dev))
+
+    layers = []
     for l in range(L):
-        y = layers[l]
-        y.q = _shaped(qs[l], (nq, H, D), bf16, "q")
-        y.out = _shaped(outs[l], (nq, H, D), bf16, "out")
-        if lses is not None and lses[l] is not None:
-            y.lse = _shaped(lses[l], (nq, H), torch.float32, "lse")
-        if sinks is not None and sinks[l] is not None:
-            y.sink = _shaped(sinks[l], (H,), torch.float32, "sink")
-        if W == 0:
-            continue
-        if swa_fp8s is not None:
-            u8 = torch.uint8
-            for rows, n, kind in ((swa_fp8s[l], S * W, "swa"), (draft_fp8s[l], nq, "draft")):
-                codes, rope, scales = (r.view(n, r.shape[-1]) for r in rows)
-                setattr(y, kind + "_codes", _shaped(codes, (n, 448), u8, kind + "_fp8 codes"))
-                setattr(y, kind + "_rope", _shaped(rope, (n, 64), bf16, kind + "_fp8 rope"))
-                setattr(y, kind + "_scales", _shaped(scales, (n, 8), u8, kind + "_fp8 scales"))
-        else:
-            if swa_kvs is None or draft_kvs is None:
-                raise ValueError("csa2_sparse_attn_tree_layers: window and drafted rows expected")
-            y.swa_kv = _shaped(swa_kvs[l], (S, W, D), bf16, "swa_kv")
-            y.draft_kv = _shaped(draft_kvs[l], (nq, D), bf16, "draft_kv")
+        lse = None if lses is None else lses[l]
+        sink = None if sinks is None else sinks[l]
+        swa = draft = 0
+        f8 = (0, 0, 0, 0, 0, 0)
+        if W and swa_fp8s is not None:
+            f8 = fp8(swa_fp8s[l], S * W, "swa_fp8") + fp8(draft_fp8s[l], nq, "draft_fp8")
+        elif W:
+            swa = _shaped(swa_kvs[l], (S, W, D), bf16, "swa_kv", dev)
+            draft = _shaped(draft_kvs[l], (nq, D), bf16, "draft_kv", dev)
+        layers.append(_TREE_LAYER.pack(
+            _shaped(qs[l], (nq, H, D), bf16, "q", dev), swa, draft,
+            _shaped(outs[l], (nq, H, D), bf16, "out", dev),
+            0 if lse is None else _shaped(lse, (nq, H), torch.float32, "lse", dev),
+            0 if sink is None else _shaped(sink, (H,), torch.float32, "sink", dev), *f8))
     # the two-CTA split only asks for a token workspace; its memory is not written
     ws, nbytes = (topk_idx.data_ptr(), 16) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib.csa2_sparse_attn_tree(
-        cache.handle, tree.ref, L, layers, _i32_array(swa_len),
-        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx"), scale, 1 if rope_out else 0,
-        rope_base, ws if nbytes else None, nbytes, _stream(stream)), "csa2_sparse_attn_tree")
+        cache.handle, tree.ref, L, b"".join(layers), _i32_array(swa_len),
+        _shaped(topk_idx, (nq, c.topk), torch.int32, "topk_idx", dev), scale, 1 if rope_out else 0,
+        rope_base, ws if nbytes else None, nbytes, _stream(stream, dev)), "csa2_sparse_attn_tree")
     return list(outs)
 
 

@@ -23,37 +23,64 @@
 // product are the fraction of a turn, exact for any position), so far
 // positions lose nothing and no 64-bit floating point is needed; sincospif
 // then takes an argument in [-1, 1].
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
 namespace csa2 {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kIters = 2;   // row groups of a warp, all loaded before the first is used
+// Blocks and row groups, measured on 8192 tokens of 98 heads in four tensors
+// (1.24 GB read and written, 183 us at the measured copy bandwidth): blocks
+// of 128 threads, 8 of them an SM at 64 registers, three row groups (48 bytes
+// a lane) requested before the first is used: 202 us.  256 threads: 211 us
+// (the sine table's barrier idles more warps), 512: 229; two row groups: 216;
+// four, with six blocks: 205; streaming hints on the loads: 218, on the
+// stores: no change.  The first form of this kernel (fp32 values held in
+// registers, 64-bit divisions per row, 3 blocks of 256 threads): 448 us.
+constexpr int kNormThreads = 128;
+constexpr int kNormBlocks = 8;   // per SM
 
-__host__ __device__ constexpr int rows_per_block(int dim) {
-  return kNormThreads / (dim / 16) * kIters;
+// Row groups of a warp, all requested before the first is used.
+template <bool kF32>
+__host__ __device__ constexpr int iters_of() { return kF32 ? 1 : 3; }
+
+__host__ __device__ constexpr int rows_per_block(int dim, bool fp32) {
+  return kNormThreads / (dim / 16) * (fp32 ? iters_of<true>() : iters_of<false>());
 }
 
-// Eight channels.  Plain loads, not the read-only path: the output may be
-// the input.
-__device__ __forceinline__ void load8(const void* base, int64_t i, bool fp32, float (&v)[8]) {
-  if (fp32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight channels as they are in memory.  Plain loads, not the read-only path:
+// the output may be the input.
+template <bool kF32>
+struct Raw {
+  uint4 a[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) +
+                                                    i * (kF32 ? 4 : 2));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    for (int k = 0; k < (kF32 ? 2 : 1); ++k) a[k] = s[k];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < (kF32 ? 2 : 1); ++k) a[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < (kF32 ? 2 : 1); ++k) {
+      const uint32_t w[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kF32) {
+          v[4 * k + i] = __uint_as_float(w[i]);
+        } else {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
     }
   }
-}
+};
 
 __device__ __forceinline__ void store8(void* base, int64_t i, bool fp32, const float (&v)[8]) {
   if (fp32) {
@@ -63,49 +90,48 @@ __device__ __forceinline__ void store8(void* base, int64_t i, bool fp32, const f
   } else {
     uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = float_to_bf16_bits(v[2 * k]) | (float_to_bf16_bits(v[2 * k + 1]) << 16);
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    }
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <int kDim>
-__device__ __forceinline__ void norm_rows(const NormParams& p, const NormPart& t, int64_t row0,
+template <int kDim, bool kF32>
+__device__ __forceinline__ void norm_rows(const NormParams& p, const NormPart& t, uint32_t block,
                                           float2* tab) {
+  constexpr int kIters = iters_of<kF32>();
   constexpr int kLanes = kDim / 16;               // lanes of a row
   constexpr int kRowsIter = kNormThreads / kLanes;
-  const int tid = threadIdx.x, l = tid % kLanes;
-  const int64_t n_rows = t.n_tokens * t.n_heads;
+  constexpr int kRows = kRowsIter * kIters;
+  const uint32_t tid = threadIdx.x, l = tid % kLanes;
+  const uint32_t H = (uint32_t)t.n_heads;
+  // the block's first row as (token, head); its other rows are few, so their
+  // places come from 32-bit arithmetic relative to it
+  const int64_t row0 = (int64_t)block * kRows;
+  const int64_t tok0 = row0 / H;
+  const uint32_t head0 = (uint32_t)(row0 - tok0 * H);
+  const int64_t left = t.n_tokens * t.n_heads - row0;
+  const uint32_t n_rows = left < kRows ? (uint32_t)left : (uint32_t)kRows;
   const int pairs = t.rope_dim / 2;
-  const int64_t tok0 = row0 / t.n_heads;
 
-  float v[kIters][2][8];
-  int64_t tok[kIters];
-  int head[kIters];
-  bool live[kIters];
+  Raw<kF32> x[kIters][2];
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
-    const int64_t row = row0 + it * kRowsIter + tid / kLanes;
-    live[it] = row < n_rows;
-    tok[it] = live[it] ? row / t.n_heads : tok0;
-    head[it] = live[it] ? (int)(row - tok[it] * t.n_heads) : 0;
-    const int64_t at = tok[it] * t.x_token + head[it] * t.x_head;
+    const uint32_t r = it * kRowsIter + tid / kLanes, hr = head0 + r, tk = hr / H;
+    const int64_t at = (tok0 + tk) * t.x_token + (int64_t)(hr - tk * H) * t.x_head;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      if (live[it]) {
-        load8(t.x, at + 8 * (l + c * kLanes), t.x_fp32 != 0, v[it][c]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[it][c][i] = 0.0f;
-      }
+      if (r < n_rows) x[it][c].load(t.x, at + 8 * (l + c * kLanes));
+      else x[it][c].zero();
     }
   }
   if (pairs > 0) {
-    // the block's tokens: sine and cosine of every channel pair
-    const int64_t last = min(row0 + rows_per_block(kDim), n_rows) - 1;
-    const int n = ((int)(last / t.n_heads - tok0) + 1) * pairs;
-    for (int i = tid; i < n; i += kNormThreads) {
-      const int k = i / pairs;
+    // sine and cosine of every channel pair of the block's tokens
+    const uint32_t n = ((head0 + n_rows - 1) / H + 1) * (uint32_t)pairs;
+    for (uint32_t i = tid; i < n; i += kNormThreads) {
+      const uint32_t k = i / (uint32_t)pairs;
       const uint64_t turn = (uint64_t)__ldg(t.pos + tok0 + k) * p.turns[t.rope_table][i - k * pairs];
       float sn, cs;
       sincospif((float)(int64_t)turn * 0x1p-63f, &sn, &cs);
@@ -113,75 +139,93 @@ __device__ __forceinline__ void norm_rows(const NormParams& p, const NormPart& t
     }
     __syncthreads();
   }
-  float wt[2][8];
-  if (t.weight) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) load8(t.weight, 8 * (l + c * kLanes), true, wt[c]);
-  }
+  float scale[kIters];
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
-    float r = 1.0f;
+    scale[it] = 1.0f;
     if (t.norm) {
       auto squares = [&](float s) -> float {
         float ss = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          float v[8];
+          x[it][c].values(v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[it][c][i] * s, v[it][c][i] * s, ss);
+          for (int i = 0; i < 8; ++i) ss = fmaf(v[i] * s, v[i] * s, ss);
+        }
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         return ss;
       };
-      float ss = squares(1.0f);
+      const float ss = squares(1.0f);
+      scale[it] = rsqrtf(fmaf(ss, 1.0f / kDim, p.eps));
       // squares beyond fp32: again with the row scaled by 2^-80 (eps is then
       // far below half a step of the mean)
       const bool big = !(ss < 0x1p120f);
       if (__any_sync(0xffffffffu, big)) {
         const float s2 = squares(0x1p-80f);
-        r = big ? rsqrtf(s2 * (1.0f / kDim)) * 0x1p-80f : rsqrtf(fmaf(ss, 1.0f / kDim, p.eps));
-      } else {
-        r = rsqrtf(fmaf(ss, 1.0f / kDim, p.eps));
+        if (big) scale[it] = rsqrtf(s2 * (1.0f / kDim)) * 0x1p-80f;
       }
     }
-    if (!live[it]) continue;
-    const int64_t at = tok[it] * t.out_token + head[it] * t.out_head;
-    const float2* row_tab = tab + (tok[it] - tok0) * pairs;
+  }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int ch = 8 * (l + c * kLanes);
+  for (int c = 0; c < 2; ++c) {
+    const int ch = 8 * (int)(l + c * kLanes);
+    const int pr = (ch - (kDim - t.rope_dim)) / 2;
+    const bool rotate = pairs > 0 && ch >= kDim - t.rope_dim;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    if (t.weight) {
+      const float4* w4 = reinterpret_cast<const float4*>(t.weight + ch);
+      const float4 a = __ldg(w4), b = __ldg(w4 + 1);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const uint32_t r = it * kRowsIter + tid / kLanes, hr = head0 + r, tk = hr / H;
+      if (r >= n_rows) continue;
       float y[8];
+      x[it][c].values(y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = v[it][c][i] * r;
-        if (t.weight) y[i] *= wt[c][i];
-      }
-      const int pr = (ch - (kDim - t.rope_dim)) / 2;
-      if (pairs > 0 && ch >= kDim - t.rope_dim) {
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * scale[it] * w[i];
+      if (rotate) {
+        const float4* cs4 = reinterpret_cast<const float4*>(tab + tk * pairs + pr);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 cs = row_tab[pr + i];
-          const float a = y[2 * i], b = y[2 * i + 1];
-          y[2 * i] = fmaf(a, cs.x, -(b * cs.y));
-          y[2 * i + 1] = fmaf(a, cs.y, b * cs.x);
+        for (int i = 0; i < 2; ++i) {
+          const float4 cs = cs4[i];   // (cos, sin) of two pairs
+          const float a = y[4 * i], b = y[4 * i + 1], d = y[4 * i + 2], e = y[4 * i + 3];
+          y[4 * i] = fmaf(a, cs.x, -(b * cs.y));
+          y[4 * i + 1] = fmaf(a, cs.y, b * cs.x);
+          y[4 * i + 2] = fmaf(d, cs.z, -(e * cs.w));
+          y[4 * i + 3] = fmaf(d, cs.w, e * cs.z);
         }
       }
-      store8(t.out, at + ch, t.out_fp32 != 0, y);
+      store8(t.out, (tok0 + tk) * t.out_token + (int64_t)(hr - tk * H) * t.out_head + ch,
+             t.out_fp32 != 0, y);
     }
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constant__ NormParams p) {
-  extern __shared__ float2 tab[];
+__global__ void __launch_bounds__(kNormThreads, kNormBlocks)
+    k_norm_rope(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(16) float2 tab[];
   int i = 0;
   while (i + 1 < p.n_parts && p.block0[i + 1] <= (int64_t)blockIdx.x) ++i;
   const NormPart& t = p.part[i];
-  const int64_t row0 = ((int64_t)blockIdx.x - p.block0[i]) * rows_per_block(t.dim);
+  const uint32_t block = (uint32_t)((int64_t)blockIdx.x - p.block0[i]);
   griddep_wait();
+  auto rows = [&](auto dim) {
+    constexpr int kDim = decltype(dim)::value;
+    if (t.x_fp32) norm_rows<kDim, true>(p, t, block, tab);
+    else norm_rows<kDim, false>(p, t, block, tab);
+  };
   switch (t.dim) {
-    case 512: norm_rows<512>(p, t, row0, tab); break;
-    case 256: norm_rows<256>(p, t, row0, tab); break;
-    case 128: norm_rows<128>(p, t, row0, tab); break;
-    default: norm_rows<64>(p, t, row0, tab); break;
+    case 512: rows(std::integral_constant<int, 512>()); break;
+    case 256: rows(std::integral_constant<int, 256>()); break;
+    case 128: rows(std::integral_constant<int, 128>()); break;
+    default: rows(std::integral_constant<int, 64>()); break;
   }
 }
 
@@ -193,7 +237,7 @@ cudaError_t launch_norm_rope(const NormParams& p_in, cudaStream_t s) {
   size_t smem = 0;
   for (int i = 0; i < p.n_parts; ++i) {
     const NormPart& t = p.part[i];
-    const int64_t rows = t.n_tokens * t.n_heads, per = rows_per_block(t.dim);
+    const int64_t rows = t.n_tokens * t.n_heads, per = rows_per_block(t.dim, t.x_fp32 != 0);
     p.block0[i] = blocks;
     blocks += (rows + per - 1) / per;
     // tokens that a block of `per` rows touches at most
