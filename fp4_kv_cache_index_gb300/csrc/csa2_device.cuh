@@ -303,6 +303,25 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+// The load alone, and the wait for every load of the thread so far: between
+// the two the registers hold nothing yet.  The wait names them, so that no use
+// can be scheduled before it.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%"
+      "14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
 // Two 16-column loads (addresses ta, tb), one wait.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&a)[16],
                                             uint32_t (&b)[16]) {
@@ -590,17 +609,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Indexer score of one entry from its 32 head logits r (fp32 bits) and the
-// query's head weights w (shared memory, 16-byte aligned):
-//     sum_h w[h] * max(r[h], 0)
-// summed in four fp32 chains (chain c takes heads h = c mod 4, in order),
-// then (c0 + c1) + (c2 + c3).  Chains (0, 1) and (2, 3) run as the two lanes
-// of packed f32x2 FMAs (each lane an fp32 fma, round to nearest), which
-// halves the FMA issues; the ReLU stays one fmax per head.
-__device__ __forceinline__ float relu_dot32(const float* w, const uint32_t (&r)[32]) {
-  uint64_t a = 0, b = 0;   // (c0, c1), (c2, c3); +0.0f bits
+// Sixteen heads of an indexer score: a += (w[h] max(r[h], 0), ...) in four
+// fp32 chains (chain c takes heads h = c mod 4, in order), chains (0, 1) in
+// `a` and (2, 3) in `b`.  The chains run as the two lanes of packed f32x2
+// FMAs (each lane an fp32 fma, round to nearest), which halves the FMA
+// issues; the ReLU stays one fmax per head.
+__device__ __forceinline__ void relu_dot_chains(const float* w, const uint32_t* r, int n, uint64_t& a,
+                                                uint64_t& b) {
 #pragma unroll
-  for (int h = 0; h < 32; h += 4) {
+  for (int h = 0; h < n; h += 4) {
     const float4 wv = *reinterpret_cast<const float4*>(w + h);
     uint64_t w01, w23, x01, x23;
     asm("mov.b64 %0, {%1, %2};" : "=l"(w01) : "f"(wv.x), "f"(wv.y));
@@ -612,10 +629,22 @@ __device__ __forceinline__ float relu_dot32(const float* w, const uint32_t (&r)[
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(w01), "l"(x01));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(b) : "l"(w23), "l"(x23));
   }
+}
+// The sum of the chains: (c0 + c1) + (c2 + c3).
+__device__ __forceinline__ float relu_dot_sum(uint64_t a, uint64_t b) {
   float c0, c1, c2, c3;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(a));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(c2), "=f"(c3) : "l"(b));
   return (c0 + c1) + (c2 + c3);
+}
+
+// Indexer score of one entry from its 32 head logits r (fp32 bits) and the
+// query's head weights w (shared memory, 16-byte aligned):
+//     sum_h w[h] * max(r[h], 0)
+__device__ __forceinline__ float relu_dot32(const float* w, const uint32_t (&r)[32]) {
+  uint64_t a = 0, b = 0;   // +0.0f bits
+  relu_dot_chains(w, r, 32, a, b);
+  return relu_dot_sum(a, b);
 }
 
 }  // namespace csa2

@@ -407,6 +407,133 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       }
     }
     if (use_hist && cur >= 0) flush(cur);
+  } else if (kTree && warp >= 2) {
+    // ------------------------------------------------ epilogue, trees of drafts
+    // Four warps per TMEM lane quadrant, each with a quarter of the group's
+    // queries (two at most).  The epilogue bounds this kernel, so its loads of
+    // tensor memory run one half row (16 heads) ahead of the arithmetic, from
+    // one tile to the next too, and a tile of committed entries, all but a
+    // sequence's last, is stored without any test.
+    if constexpr (kTree) {
+      const int quad = warp & 3, row = quad * 32 + lane;
+      const int et = threadIdx.x - 64;
+      const int jq = (p.qpg + kParts - 1) / kParts;   // 1 or 2
+      const int j0 = ((warp - 2) >> 2) * jq;
+      const bool use_hist = p.key_hist != nullptr;
+      const int hbins = p.qpg * kKeyHistBins;
+      auto esync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); };
+      auto flush = [&](int gg) {
+        esync();
+        const int q0 = p.q_first[gg], q1 = p.q_first[gg + 1];
+        for (int i = et; i < hbins; i += kEpiThreads) {
+          const uint32_t v = hs[i];
+          const int q = q0 + i / kKeyHistBins;
+          if (v && q < q1)
+            atomicAdd(p.key_hist + (int64_t)q * kKeyHistBins + (i % kKeyHistBins), v);
+          hs[i] = 0u;
+        }
+        esync();
+      };
+      if (use_hist)
+        for (int i = et; i < hbins; i += kEpiThreads) hs[i] = 0u;
+      GroupCursor gc = c0;
+      int cur = -1, acc = 0;
+      uint32_t aph = 0;
+      int mine = 0;                  // this warp's queries of the group
+      int ncom = 0, nvis = 0;        // committed entries, and with the drafts'
+      float* out[2] = {nullptr, nullptr};
+      uint64_t ents[2] = {0, 0};
+      uint32_t ra[16], rb[16];
+      const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(j0 * 32);
+      bool ready = false;            // ra holds, or is receiving, the tile's first half row
+      for (int it = begin; it < end; ++it) {
+        gc.advance(p, it);
+        const int g = gc.g;
+        if (g != cur) {
+          if (use_hist && cur >= 0) flush(cur);
+          esync();
+          const int qg = p.q_first[g], qe = p.q_first[g + 1];
+          for (int i = et; i < qrows; i += kEpiThreads) {
+            const int q = qg + (i >> 5);
+            wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          }
+          esync();
+          cur = g;
+          ncom = p.n_com[g];
+          nvis = p.nvis[g];
+          mine = max(0, min(jq, qe - qg - j0));
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int q = min(qg + j0 + jj, p.nq - 1);
+            out[jj] = p.scores + (int64_t)q * p.ld;
+            ents[jj] = p.ents[q];
+          }
+        }
+        const int e0 = (it - gc.lo) * kTileE, e = e0 + row;
+        auto store = [&](int jj, float s) {
+          int col = e;
+          if (e0 + kTileE > ncom) {   // the sequence's last tiles
+            if (e >= nvis) return;
+            if (e >= ncom) {
+              // a draft's entry: the path's only, in the order of the path
+              const int b = e - ncom;
+              if (!((ents[jj] >> b) & 1u)) return;
+              col = ncom + __popcll(ents[jj] & ((1ull << b) - 1ull));
+            }
+          }
+          if (!CSA2_IN_BOUNDS(col < p.ld, p.err)) return;
+          out[jj][col] = s;
+          if (use_hist) atomicAdd(hs + (j0 + jj) * kKeyHistBins + (score_key(s) >> 21), 1u);
+        };
+        const uint32_t ta = ta0 + (uint32_t)(acc * acc_cols);
+        if (!ready) {
+          if (!mbar_wait(acc_full + acc, aph, p.err, wl)) break;
+          tc_fence_after();
+          tmem_ld16_issue(ta, ra);
+        }
+        ready = false;
+        tmem_ld16_wait(ra);
+        // the accumulator is free once this warp's last columns are read;
+        // the next tile's first half row is requested if its MMAs are done
+        const int nacc_ = acc ^ 1;
+        const uint32_t naph = aph ^ (uint32_t)(acc == 1);
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty + acc);
+          if (it + 1 < end) {
+            ready = __all_sync(0xffffffffu, mbar_try_wait(acc_full + nacc_, naph));
+            if (ready) tc_fence_after();
+          }
+        };
+        if (mine == 0) {
+          release();
+          if (ready) tmem_ld16_issue(ta0 + (uint32_t)(nacc_ * acc_cols), ra);
+        }
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          if (jj >= mine) break;
+          const float* w = wbuf + (j0 + jj) * 32;
+          uint64_t a = 0, b = 0;
+          tmem_ld16_issue(ta + 32 * jj + 16, rb);
+          relu_dot_chains(w, ra, 16, a, b);
+          tmem_ld16_wait(rb);
+          if (jj + 1 < mine) {
+            tmem_ld16_issue(ta + 32 * (jj + 1), ra);
+          } else {
+            release();
+            if (ready) tmem_ld16_issue(ta0 + (uint32_t)(nacc_ * acc_cols), ra);
+          }
+          relu_dot_chains(w + 16, rb, 16, a, b);
+          if (jj + 1 < mine) tmem_ld16_wait(ra);
+          store(jj, relu_dot_sum(a, b));
+        }
+        acc = nacc_;
+        aph = naph;
+      }
+      if (ready) tmem_ld16_wait(ra);
+      if (use_hist && cur >= 0) flush(cur);
+    }
   } else if (warp >= 2) {
     // ------------------------------------------------ epilogue
     const int quad = warp & 3;                 // TMEM lane quadrant of this warp
@@ -421,22 +548,12 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     // adds this CTA's counts of group `gg`'s queries to the global
     // histograms and clears hs
     auto esync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); };
-    // first query of group gg, and one past its last
-    auto q_begin = [&](int gg) -> int {
-      if constexpr (kTree) return p.q_first[gg];
-      return gg * p.qpg;
-    };
-    auto q_end = [&](int gg) -> int {
-      if constexpr (kTree) return p.q_first[gg + 1];
-      return p.nq;
-    };
     auto flush = [&](int gg) {
       esync();
-      const int q0 = q_begin(gg), q1 = q_end(gg);
       for (int i = et; i < hbins; i += kEpiThreads) {
         const uint32_t v = hs[i];
-        const int q = q0 + i / kKeyHistBins;
-        if (v && q < q1) atomicAdd(p.key_hist + (int64_t)q * kKeyHistBins + (i % kKeyHistBins), v);
+        const int q = gg * p.qpg + i / kKeyHistBins;
+        if (v && q < p.nq) atomicAdd(p.key_hist + (int64_t)q * kKeyHistBins + (i % kKeyHistBins), v);
         hs[i] = 0u;
       }
       esync();
@@ -448,9 +565,6 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     int cur = -1, acc = 0;
     uint32_t aph = 0;
     int nvis[kMaxQ];   // visible entries of this thread's queries in the current group
-    uint64_t ents[kMaxQ];       // trees: the path's entries of this thread's queries
-    int ncom = 0;               // trees: committed entries of the sequence
-    int qg = 0, qe = 0;         // the group's queries [qg, qe)
     int32_t blk_nxt = (p.pool && begin < end) ? pool_blk(begin, c0, row >> 3) : -1;
     for (int it = begin; it < end; ++it) {
       gc.advance(p, it);
@@ -460,23 +574,15 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       if (g != cur) {
         if (use_hist && cur >= 0) flush(cur);
         esync();
-        qg = q_begin(g);
-        qe = q_end(g);
         for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = qg + (i >> 5);
-          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          const int q = g * p.qpg + (i >> 5);
+          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
         }
         esync();
         cur = g;
 #pragma unroll
         for (int jj = 0; jj < kMaxQ; ++jj)
           nvis[jj] = (j0 + jj < j1) ? group_nvis_query(p, g, j0 + jj) : 0;
-        if constexpr (kTree) {
-          ncom = p.n_com[g];
-#pragma unroll
-          for (int jj = 0; jj < kMaxQ; ++jj)
-            ents[jj] = (j0 + jj < j1 && qg + j0 + jj < qe) ? p.ents[qg + j0 + jj] : 0u;
-        }
       }
       if (!mbar_wait(acc_full + acc, aph, p.err, wl)) break;
       tc_fence_after();
@@ -485,22 +591,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       // score of query j of the group from its 32 head columns r
       auto emit = [&](int j, int jj, const uint32_t (&r)[32]) {
         const float s = relu_dot32(wbuf + j * 32, r);
-        const int q = qg + j;
+        const int q = g * p.qpg + j;
         const int nv = nvis[jj];
-        if constexpr (kTree) {
-          if (q >= qe || e >= nv) return;
-          int col = e;
-          if (e >= ncom) {
-            // a draft's entry: the path's only, in the order of the path
-            const int b = e - ncom;
-            if (!((ents[jj] >> b) & 1u)) return;
-            col = ncom + __popcll(ents[jj] & ((1ull << b) - 1ull));
-          }
-          if (!CSA2_IN_BOUNDS(col < p.ld, p.err)) return;
-          p.scores[(int64_t)q * p.ld + col] = s;
-          if (use_hist) atomicAdd(hs + j * kKeyHistBins + (score_key(s) >> 21), 1u);
-          return;
-        }
         if (p.pool) {
           // slot t * 128 + row of the pool; its entry decides validity
           const int64_t ent = (int64_t)blk * 8 + (row & 7);
