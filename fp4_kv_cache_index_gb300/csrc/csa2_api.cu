@@ -1519,6 +1519,8 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
   }
   // queries that share a tile of keys
   const int qpg = mx ? 4 : plan.max_draft <= 2 ? 2 : plan.max_draft <= 4 ? 4 : 8;
+  // keys of a tile
+  const int tile = mx ? 512 : 128;
   const uint16_t* qb = static_cast<const uint16_t*>(q_idx);
   int64_t q0 = 0, done = 0;   // queries before this launch, queries of the sequence already taken
   int seq = 0;
@@ -1539,9 +1541,9 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
       ip->entry_base[groups] = q.base;
       ip->nvis[groups] = q.len;
       for (int j = 0; j < size; ++j) ip->ents[n + j] = plan.q[q0 + n + j].ents;
-      const int64_t lead = (mx && q.len > 0) ? (q.base & 127) : 0;
+      const int64_t lead = (mx && q.len > 0) ? (q.base & (tile - 1)) : 0;
       ip->tile_prefix[groups + 1] =
-          ip->tile_prefix[groups] + (int32_t)((q.len + lead + 127) / 128);
+          ip->tile_prefix[groups] + (int32_t)((q.len + lead + tile - 1) / tile);
       n += size;
       ++groups;
       done += size;
@@ -1556,6 +1558,7 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
     ip->nq = n;
     ip->qpg = qpg;
     ip->n_groups = groups;
+    ip->tile_keys = tile;
     ip->ratio = c->cfg.ratio;
     ip->wait_cycles = c->wait_cycles;
     ip->inject = c->inject;

@@ -57,19 +57,14 @@
 // Every wait is bounded.
 #include <type_traits>
 
+#include <cuda_fp4.h>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 416;
-constexpr int kEpiThreads = 256;   // warps 2-9
-constexpr int kEpiWarps = kEpiThreads / 32;
-constexpr int kPrepBase = 320;     // warps 10-11
-constexpr int kSfWarp = 12;        // scale-atom copies
-constexpr int kPrepThreads = 64;
-constexpr int kPrepWarps = kPrepThreads / 32;
 #ifndef CSA2_FP4_STAGES
 #define CSA2_FP4_STAGES 5
 #endif
@@ -215,6 +210,9 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint6
 // MXFP4 (UE8M0 scale of the block's largest magnitude, OCP MX rule; E2M1
 // code of x / scale, nearest, ties to even, saturating) -> 16 code bytes in
 // the B slot's swizzled row and the scale byte in its atom.
+// kCvt: the codes by the hardware's conversion (the same rounding; without it
+// a comparison per grid point).
+template <bool kCvt>
 __device__ __forceinline__ void prep_query_block(const uint16_t* src, bool live, uint8_t* bcodes,
                                                  uint8_t* batom, int n, int b) {
   float x[32];
@@ -246,8 +244,17 @@ __device__ __forceinline__ void prep_query_block(const uint16_t* src, bool live,
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     uint32_t w = 0;
+    if constexpr (kCvt) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= e2m1_encode(__fmul_rn(x[8 * k + i], inv)) << (4 * i);
+      for (int i = 0; i < 4; ++i)
+        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(x[8 * k + 2 * i], inv),
+                                                            __fmul_rn(x[8 * k + 2 * i + 1], inv)),
+                                                __NV_E2M1, cudaRoundNearest)
+             << (8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w |= e2m1_encode(__fmul_rn(x[8 * k + i], inv)) << (4 * i);
+    }
     c[k] = w;
   }
   uint8_t* row = bcodes + (n >> 3) * 512 + (n & 7) * 64;
@@ -255,11 +262,29 @@ __device__ __forceinline__ void prep_query_block(const uint16_t* src, bool live,
   batom[(n & 31) * 16 + ((n >> 5) & 3) * 4 + b] = (uint8_t)sb;
 }
 
+// Warp roles behind the two first warps: epilogue, query preparation, scale
+// copies (trees: sixteen epilogue warps and one that prepares queries).
 template <class P>
-__global__ void __launch_bounds__(kThreads, 1)
+struct Roles {
+  static constexpr bool kTree = std::is_same<P, TreeIndexParams>::value;
+  static constexpr int kEpiWarps = kTree ? 16 : 8;
+  static constexpr int kEpiThreads = 32 * kEpiWarps;
+  static constexpr int kPrepWarp = 2 + kEpiWarps;
+  static constexpr int kPrepWarps = kTree ? 1 : 2;
+  static constexpr int kPrepThreads = 32 * kPrepWarps;
+  static constexpr int kSfWarp = kPrepWarp + kPrepWarps;
+  static constexpr int kThreads = 32 * (kSfWarp + 1);
+};
+
+template <class P>
+__global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     k_index_fp4(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_kq,
                 const __grid_constant__ CUtensorMap tm_kc8) {
-  constexpr bool kTree = std::is_same<P, TreeIndexParams>::value;
+  using R = Roles<P>;
+  constexpr bool kTree = R::kTree;
+  constexpr int kEpiThreads = R::kEpiThreads, kEpiWarps = R::kEpiWarps;
+  constexpr int kPrepThreads = R::kPrepThreads, kPrepWarps = R::kPrepWarps;
+  constexpr int kSfWarp = R::kSfWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -278,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* b_empty = bars + 50;           // [2]
   uint64_t* drain = bars + 52;
   uint64_t* sf_drain = bars + 53;
+  uint64_t* b_first = bars + 54;           // trees: the first group's queries
   uint64_t* sf_full = bars + 56;           // [kStages]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 62);
 
@@ -295,9 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // keys (pool slots) per tile: 512 for one query (contiguous keys, or 64
   // pool blocks of 8), 128 for four queries
-  const int tile_e = p.qpg == 1 ? 512 : 128;
+  int tile_e = p.qpg == 1 ? 512 : 128;
+  if constexpr (kTree) tile_e = p.tile_keys;
   const int mgroups = tile_e / 128;
-  const int acc_cols = mgroups * N;              // 128, 64 or 128 columns
+  // columns of an accumulator: a tile's (128, 64 or 128), trees: an M-group's
+  const int acc_cols = kTree ? N : mgroups * N;
   const int nacc = min(kNAcc, (int)kAccCols / acc_cols);   // 3, 4 or 3 accumulators
   const int blocks_per_tile = tile_e / 8;
   // Contiguous keys: tiles are aligned chunks of tile_e key rows, so a
@@ -309,7 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // decode over contiguous keys: the key scale copies run on their own warp
   // (elsewhere the epilogue bounds the pipeline and the MMA issuer copies
   // them itself)
-  const bool sf_warp = perm && p.qpg == 1;
+  const bool sf_warp = kTree || (perm && p.qpg == 1);
+  // trees: whether M-group mg of tile t holds any entry of the sequence
+  auto unit_live = [&](int t, int mg, int lead, int nvis) -> bool {
+    const int e = t * tile_e + mg * 128 - lead;
+    return e < nvis && e + 128 > 0;
+  };
   auto slot_key = [&](int sl) -> int {
     return perm ? (sl & ~127) + 4 * (sl & 31) + ((sl >> 5) & 3) : sl;
   };
@@ -322,11 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // k_full: the copies' transaction bytes with lane 0's arrival, plus in
     // pool mode one arrival per producer lane once its scale copies landed
     for (int i = 0; i < kStages; ++i) { mbar_init(k_full + i, pool ? 33 : 1); mbar_init(k_empty + i, 1); }
-    for (int i = 0; i < kNAcc; ++i) { mbar_init(acc_full + i, 1); mbar_init(acc_empty + i, kEpiWarps); }
+    for (int i = 0; i < kNAcc; ++i) { mbar_init(acc_full + i, 1); mbar_init(acc_empty + i, kTree ? kEpiWarps / 2 : kEpiWarps); }
     for (int i = 0; i < 2; ++i) { mbar_init(b_full + i, kPrepWarps); mbar_init(b_empty + i, 1); }
     for (int i = 0; i < kStages; ++i) mbar_init(sf_full + i, 1);
     mbar_init(drain, 1);
     mbar_init(sf_drain, 1);
+    mbar_init(b_first, kEpiWarps);
     fence_barrier_init();
     tma_prefetch_desc(pool ? &tm_kc8 : &tm_kq);
   }
@@ -354,6 +388,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.advance(p, it);
     const int left = p.pool_blocks - (it - c.lo) * blocks_per_tile;
     return left < blocks_per_tile ? left : blocks_per_tile;
+  };
+
+  // query head rows n = item / 4, blocks item % 4 of group g into a B slot
+  auto prep_items = [&](int g, int slot, int first, int step) {
+    uint8_t* bc = bslots + slot * kBSlotBytes;
+    for (int item = first; item < 32 * p.qpg * 4; item += step) {
+      const int n = item >> 2, b = item & 3;
+      const int q = q_begin(g) + (n >> 5);
+      const uint16_t* src = p.q_idx + ((int64_t)q * kIdxHeads + (n & 31)) * kIdxDim + b * 32;
+      prep_query_block<kTree>(src, q < q_end(g), bc, bc + kBRows * (kIdxDim / 2), n, b);
+    }
   };
 
   if (warp == 0 && begin < end) {
@@ -457,10 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (armed & (1u << s)) mbar_wait(k_full + s, (armed_ph >> s) & 1u, p.err, wl);
     }
     __syncwarp();
-  } else if (warp >= kPrepBase / 32 && warp < kSfWarp && begin < end) {
+  } else if (warp >= R::kPrepWarp && warp < kSfWarp && begin < end) {
     // ------------------------------------------------ query preparation
-    const int pt = threadIdx.x - kPrepBase;
-    const int qrows = 32 * p.qpg;
+    const int pt = threadIdx.x - 32 * R::kPrepWarp;
     Cursor gc = c0;
     int cur = -1, gi = 0;
     bool ok = true;
@@ -471,16 +515,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = gi & 1;
       ok = mbar_wait_sleep(b_empty + slot, (uint32_t)(((gi >> 1) & 1) ^ 1), p.err, wl);
       if (!ok) break;
-      uint8_t* bc = bslots + slot * kBSlotBytes;
-      uint8_t* ba = bc + kBRows * (kIdxDim / 2);
-      for (int i = pt; i < kSfAtom / 4; i += kPrepThreads) reinterpret_cast<uint32_t*>(ba)[i] = 0u;
-      asm volatile("bar.sync 2, 64;" ::: "memory");   // both warps: zeroed before any scale byte
-      for (int item = pt; item < qrows * 4; item += kPrepThreads) {
-        const int n = item >> 2, b = item & 3;
-        const int q = q_begin(cur) + (n >> 5);
-        const bool live = q < q_end(cur);
-        const uint16_t* src = p.q_idx + ((int64_t)q * kIdxHeads + (n & 31)) * kIdxDim + b * 32;
-        prep_query_block(src, live, bc, ba, n, b);
+      // trees: the epilogue warps, idle until then, prepare the first group
+      if (!kTree || gi > 0) {
+        uint8_t* ba = bslots + slot * kBSlotBytes + kBRows * (kIdxDim / 2);
+        for (int i = pt; i < kSfAtom / 4; i += kPrepThreads) reinterpret_cast<uint32_t*>(ba)[i] = 0u;
+        // every preparing warp: zeroed before any scale byte
+        if constexpr (kPrepWarps == 1) __syncwarp();
+        else asm volatile("bar.sync 2, 64;" ::: "memory");
+        prep_items(cur, slot, pt, kPrepThreads);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -517,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t b_desc0 = sdesc_sw64(smem_u32(bslots));
     const uint64_t atom_desc0 = sdesc_atom(smem_u32(stages + kCodeStage));
     const uint32_t idesc_k0 = idesc_mxf4((uint32_t)N, 0u), idesc_k1 = idesc_mxf4((uint32_t)N, 2u);
+    [[maybe_unused]] int nvis = 0, lead = 0;   // trees: of the group
     Cursor gc = c0;
     int cur = -1, gi = -1, stage = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
@@ -526,7 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (changed) {
         ++gi;
         cur = gc.g;
-        ok = mbar_wait(b_full + (gi & 1), (uint32_t)((gi >> 1) & 1), p.err, wl);
+        if constexpr (kTree) {
+          nvis = p.nvis[cur];
+          lead = lead_of(gc);
+        }
+        ok = mbar_wait(b_full + (gi & 1), (uint32_t)((gi >> 1) & 1), p.err, wl) &&
+             (!kTree || gi > 0 || mbar_wait(b_first, 0, p.err, wl));
         if (!ok) break;
         tc_fence_after();
         uint8_t* ba = bslots + (gi & 1) * kBSlotBytes + kBRows * (kIdxDim / 2);
@@ -536,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and its accumulator is free
       ok = mbar_wait(k_full + stage, ph, p.err, wl) &&
            (!sf_warp || mbar_wait(sf_full + stage, ph, p.err, wl)) &&
-           mbar_wait(acc_empty + acc, aph ^ 1, p.err, wl);
+           (kTree || mbar_wait(acc_empty + acc, aph ^ 1, p.err, wl));
       if (!ok) break;
       tc_fence_after();
       const uint32_t so = (uint32_t)(stage * kStageBytes) >> 4;   // stage offset, 16-byte units
@@ -551,22 +599,142 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bo = (uint32_t)((gi & 1) * kBSlotBytes) >> 4;
       const uint32_t sfb = tmem_base + kSfbCol + 4 * (gi & 1);
       for (int mg = 0; mg < mgroups; ++mg) {
-        const uint32_t d = tmem_base + (uint32_t)(acc * acc_cols + mg * N);
+        if constexpr (kTree) {
+          // an accumulator per M-group; those past the sequence are skipped
+          if (!unit_live(it - gc.lo, mg, lead, nvis)) continue;
+          ok = mbar_wait(acc_empty + acc, aph ^ 1, p.err, wl);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t d = tmem_base + (uint32_t)(acc * acc_cols + (kTree ? 0 : mg * N));
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
           umma_mxf4(d, a_desc0 + so + (uint32_t)(mg * a_mg + 2 * ks), b_desc0 + bo + (uint32_t)(2 * ks),
                     ks ? idesc_k1 : idesc_k0, sfa + 4 * mg, sfb, ks > 0 ? 1u : 0u);
+        if constexpr (kTree) {
+          umma_commit(acc_full + acc);
+          if (++acc == nacc) { acc = 0; aph ^= 1; }
+        }
       }
+      if (!ok) break;
       umma_commit(k_empty + stage);
-      umma_commit(acc_full + acc);
+      if constexpr (!kTree) umma_commit(acc_full + acc);
       const bool last_of_group = (it + 1 == end) || (gc.hi <= it + 1);
       if (last_of_group) umma_commit(b_empty + (gi & 1));
       if (++stage == kStages) { stage = 0; ph ^= 1; }
-      if (++acc == nacc) { acc = 0; aph ^= 1; }
+      if (!kTree && ++acc == nacc) { acc = 0; aph ^= 1; }
     }
     umma_commit(drain);
     mbar_wait(drain, 0, p.err, wl);
-  } else if (warp >= 2 && warp < 10) {
+  } else if (kTree && warp >= 2 && warp < R::kPrepWarp) {
+    // ------------------------------------------------ epilogue, trees of drafts
+    // Sixteen warps in two sets of eight, which take alternate M-groups, so
+    // that one set computes while the other waits; a warp has one TMEM lane
+    // quadrant and two of the group's four queries, and its loads of tensor
+    // memory run one half row (16 heads) ahead of the arithmetic.  Lane l of
+    // quadrant q holds key 4 l + q of the M-group.
+    if constexpr (kTree) {
+      const int quad = warp & 3, set = (warp - 2) >> 3, j0 = ((warp - 2) >> 2 & 1) * 2;
+      const int et = threadIdx.x - 64;
+      auto esync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); };
+      if (begin < end) {
+        // the first group's queries (every byte of its atom is written: four
+        // queries of 32 heads)
+        prep_items(g0, 0, et, kEpiThreads);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_first);
+      }
+      Cursor gc = c0;
+      int cur = -1, acc = 0, turn = 0;    // turn: which set takes the next M-group
+      uint32_t aph = 0;
+      int ncom = 0, nvis = 0, lead = 0;   // committed entries, and with the drafts'
+      int mine = 0;                       // this warp's queries of the group
+      uint64_t path[2] = {0, 0};
+      float* out[2] = {nullptr, nullptr};
+      bool ok = true;
+      for (int it = begin; it < end && ok; ++it) {
+        gc.advance(p, it);
+        const int g = gc.g;
+        if (g != cur) {
+          const int qg = q_begin(g), qe = q_end(g);
+          esync();
+          for (int i = et; i < kBRows; i += kEpiThreads) {
+            const int q = qg + (i >> 5);
+            wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          }
+          esync();
+          cur = g;
+          ncom = p.n_com[g];
+          nvis = p.nvis[g];
+          lead = lead_of(gc);
+          mine = max(0, min(2, qe - qg - j0));
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int q = min(qg + j0 + jj, p.nq - 1);
+            path[jj] = p.ents[q];
+            out[jj] = p.scores + (int64_t)q * p.ld;
+          }
+        }
+        const int t = it - gc.lo;
+        for (int mg = 0; mg < mgroups; ++mg) {
+          if (!unit_live(t, mg, lead, nvis)) continue;
+          const int a_me = acc;
+          const uint32_t ph_me = aph;
+          const bool take = turn == set;
+          turn ^= 1;
+          if (++acc == nacc) { acc = 0; aph ^= 1; }
+          if (!take) continue;
+          ok = mbar_wait_sleep(acc_full + a_me, ph_me, p.err, wl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) +
+                              (uint32_t)(a_me * acc_cols + j0 * 32);
+          auto release = [&]() {   // the accumulator is free once read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + a_me);
+          };
+          const int e0 = t * tile_e + mg * 128 - lead, e = e0 + 4 * lane + quad;
+          const bool inner = e0 >= 0 && e0 + 128 <= ncom;   // committed entries only
+          auto store = [&](int jj, float s) {
+            int col = e;
+            if (!inner) {
+              if (e < 0 || e >= nvis) return;
+              if (e >= ncom) {
+                // a draft's entry: the path's only, in the order of the path
+                const int bit = e - ncom;
+                if (!((path[jj] >> bit) & 1u)) return;
+                col = ncom + __popcll(path[jj] & ((1ull << bit) - 1ull));
+              }
+            }
+            if (CSA2_IN_BOUNDS(col < p.ld, p.err)) out[jj][col] = s;
+          };
+          uint32_t ra[16], rb[16];
+          if (mine > 0) {
+            tmem_ld16_issue(ta, ra);
+            tmem_ld16_wait(ra);
+          } else {
+            release();
+          }
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            if (jj >= mine) break;
+            const float* w = wbuf + (j0 + jj) * 32;
+            uint64_t a = 0, b = 0;
+            tmem_ld16_issue(ta + 32 * jj + 16, rb);
+            relu_dot_chains(w, ra, 16, a, b);
+            tmem_ld16_wait(rb);
+            if (jj + 1 < mine) tmem_ld16_issue(ta + 32 * (jj + 1), ra);
+            else release();
+            relu_dot_chains(w + 16, rb, 16, a, b);
+            if (jj + 1 < mine) tmem_ld16_wait(ra);
+            store(jj, relu_dot_sum(a, b));
+          }
+        }
+      }
+    }
+  } else if (!kTree && warp >= 2 && warp < 10) {
     // ------------------------------------------------ epilogue
     const int quad = warp & 3;                 // TMEM lane quadrant
     const int et = threadIdx.x - 64;           // 0..255
@@ -594,20 +762,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cur = -1, acc = 0, t_first = 0;
     uint32_t aph = 0;
     int nv[2] = {0, 0};   // visible entries of this thread's queries
-    uint64_t ents[2] = {0, 0};   // trees: the path's entries of this thread's queries
-    int ncom = 0;                // trees: committed entries of the sequence
-    int qg = 0, qe = 0;          // the group's queries [qg, qe)
     for (int it = begin; it < end; ++it) {
       gc.advance(p, it);
       const int g = gc.g;
       if (g != cur) {
         if (use_hist && cur >= 0) flush(cur);
         esync();
-        qg = q_begin(g);
-        qe = q_end(g);
         for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = qg + (i >> 5);
-          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+          const int q = g * p.qpg + (i >> 5);
+          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
         }
         if (pool) {
           // the block ids of this CTA's tiles of the group, loaded once
@@ -626,34 +789,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           nv[0] = group_nvis_query(p, g, 2 * half);
           nv[1] = group_nvis_query(p, g, 2 * half + 1);
         }
-        if constexpr (kTree) {
-          ncom = p.n_com[g];
-          const int q = qg + 2 * half;
-          ents[0] = q < qe ? p.ents[q] : 0u;
-          ents[1] = q + 1 < qe ? p.ents[q + 1] : 0u;
-        }
       }
       if (!mbar_wait_sleep(acc_full + acc, aph, p.err, wl)) break;
       tc_fence_after();
       const int t = it - gc.lo;
       const int lead = lead_of(gc);
       const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * acc_cols);
-      // score s of query q (trees: with the entries `path`) at slot `row` of the tile: entry e (pool mode: the
+      // score s of query q at slot `row` of the tile: entry e (pool mode: the
       // pool slot, whose block decides validity)
-      auto store = [&](int row, int q, int nvis, uint64_t path, float s) {
+      auto store = [&](int row, int q, int nvis, float s) {
         const int e = t * tile_e + slot_key(row) - lead;
-        if constexpr (kTree) {
-          if (q >= qe || e < 0 || e >= nvis) return;
-          int col = e;
-          if (e >= ncom) {
-            // a draft's entry: the path's only, in the order of the path
-            const int b = e - ncom;
-            if (!((path >> b) & 1u)) return;
-            col = ncom + __popcll(path & ((1ull << b) - 1ull));
-          }
-          if (CSA2_IN_BOUNDS(col < p.ld, p.err)) p.scores[(int64_t)q * p.ld + col] = s;
-          return;
-        }
         if (pool) {
           int32_t blk = -1;
           if (t * blocks_per_tile + (row >> 3) < p.pool_blocks)
@@ -681,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, g, nv[0], ents[0], relu_dot32(wbuf, r));
+        store(slot0, g, nv[0], relu_dot32(wbuf, r));
       } else if (p.qpg == 1) {
         // M-groups 2 half and 2 half + 1: columns N apart
         uint32_t ra[32], rb[32];
@@ -690,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, g, nv[0], ents[0], relu_dot32(wbuf, ra));
-        store(slot0 + 128, g, nv[0], ents[0], relu_dot32(wbuf, rb));
+        store(slot0, g, nv[0], relu_dot32(wbuf, ra));
+        store(slot0 + 128, g, nv[0], relu_dot32(wbuf, rb));
       } else {
         uint32_t ra[32], rb[32];
         const int j = 2 * half;
@@ -699,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty + acc);
-        store(slot0, qg + j, nv[0], ents[0], relu_dot32(wbuf + j * 32, ra));
-        store(slot0, qg + j + 1, nv[1], ents[1], relu_dot32(wbuf + (j + 1) * 32, rb));
+        store(slot0, g * p.qpg + j, nv[0], relu_dot32(wbuf + j * 32, ra));
+        store(slot0, g * p.qpg + j + 1, nv[1], relu_dot32(wbuf + (j + 1) * 32, rb));
       }
       if (++acc == nacc) { acc = 0; aph ^= 1; }
     }
@@ -729,7 +874,7 @@ cudaError_t launch_any(const P& p, const CUtensorMap& tm_kq, const CUtensorMap& 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Roles<P>::kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -747,7 +892,8 @@ cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
 
 cudaError_t launch_index_fp4_tree(const TreeIndexParams& p, const CUtensorMap& tm_kq, int grid,
                                   cudaStream_t s) {
-  if (p.qpg != kMaxQpg) return cudaErrorInvalidValue;
+  if (p.qpg != kMaxQpg || (p.tile_keys != 128 && p.tile_keys != 256 && p.tile_keys != kTileMax))
+    return cudaErrorInvalidValue;
   return launch_any(p, tm_kq, tm_kq, grid, s);
 }
 
