@@ -1519,8 +1519,15 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
   }
   // queries that share a tile of keys
   const int qpg = mx ? 4 : plan.max_draft <= 2 ? 2 : plan.max_draft <= 4 ? 4 : 8;
-  // keys of a tile
-  const int tile = mx ? 512 : 128;
+  // keys of a tile.  MXFP4: 512 (a stage's waits once in four M-groups: 4 x 29
+  // drafts over 128K 99 us, with 256 104, with 128 124), 256 when there would
+  // be fewer such tiles than SMs (29 drafts over 4096: 5.5 us, with 512 6.2)
+  int64_t tiles512 = 0;
+  for (int i = 0; mx && i < t->n_seqs; ++i) {
+    const int s = t->seq_ids ? t->seq_ids[i] : i;
+    tiles512 += (int64_t)((t->n_draft[i] + 3) / 4) * ((c->len[s] + 511) / 512);
+  }
+  const int tile = !mx ? 128 : tiles512 >= c->num_sms ? 512 : 256;
   const uint16_t* qb = static_cast<const uint16_t*>(q_idx);
   int64_t q0 = 0, done = 0;   // queries before this launch, queries of the sequence already taken
   int seq = 0;

@@ -383,9 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     return reinterpret_cast<uint4*>(kv + c * (kRows * 128) + e * 128 + ((k ^ (e & 7)) << 4));
   };
   auto scale_bf16x2 = [&](uint32_t byte) -> uint32_t {
-    const float sc = (p.layout == 0) ? ue8m0_value(byte) : fabsf(e4m3_value(byte));
-    const uint32_t s16 = float_to_bf16_bits(sc);
-    return s16 | (s16 << 16);
+    // E4M3 magnitude: its bits seven places up in a float have the value times
+    // 2^-120, subnormals too, and 4 bits of mantissa fit bf16 exactly
+    const uint32_t u = (p.layout == 0)
+                           ? __float_as_uint(ue8m0_value(byte))
+                           : __float_as_uint(__uint_as_float((byte & 0x7Fu) << 20) * 0x1p120f);
+    return (u >> 16) | (u & 0xFFFF0000u);
   };
   auto e2m1_piece = [&](uint32_t word, uint32_t s2) -> uint4 {
     uint32_t v[4];
