@@ -73,7 +73,9 @@ struct Small {
   float rope_c[32], rope_s[32];  // output RoPE(-i): cos, sin of each channel pair
   uint32_t tmem;
   uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2];   // [h]: channel half h
-  int32_t draft_row[64];         // trees: row of the j-th draft in the window
+  // trees: source of each window row (>= 0 a committed row, <= -2 draft row
+  // -2 - x, -1 none)
+  int32_t win_src[kRows];
 };
 constexpr int kSmemBytes = kSmallOff + (int)sizeof(Small) + 1024;
 
@@ -170,8 +172,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     swa_row0 = t.win_row;
     win_n = t.win_n;
     swa_count = win_n + __popcll(t.rows);
-    if (tid < 64 && ((t.rows >> tid) & 1u))
-      sm.draft_row[__popcll(t.rows & ((1ull << tid) - 1ull))] = t.draft0 + tid;
+    if (tid < 64) {
+      if ((t.rows >> tid) & 1u)
+        sm.win_src[win_n + __popcll(t.rows & ((1ull << tid) - 1ull))] = -2 - (t.draft0 + tid);
+    } else if (tid >= 128 && tid < 256) {
+      const int e = tid - 128;
+      if (e < win_n) sm.win_src[e] = swa_row0 + e;
+      else if (e >= swa_count) sm.win_src[e] = -1;
+    }
   } else if (p.prefill) {
     base = p.pre_base;
     len = p.pre_len;
@@ -220,6 +228,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  // Trees, FP8 window rows: requested here, long before they are written: a
+  // row of the tile to a warp in turn (row warp + 16 i), lanes 0-27 with 16
+  // codes each and their block's scale byte, and the RoPE channels of the
+  // warp's eight rows as 64 pieces of 16 bytes.  (Each fill worker loading its
+  // own 64 channels as 8-byte pieces when the tile is written took 8 us of a
+  // 44 us CTA.)
+  constexpr int kWinRows = kTree ? kRows / (kThreads / 32) : 1;
+  [[maybe_unused]] uint4 wraw[kWinRows], wrope[2];
+  [[maybe_unused]] uint32_t wscale[kWinRows];
+  const bool win_fp8 = kTree && ly.swa_codes && swa_first;
+  if constexpr (kTree) {
+    if (win_fp8) {
+      const TreeLayer& tl = p.tree[layer];
+#pragma unroll
+      for (int i = 0; i < kWinRows; ++i) {
+        const int32_t src = sm.win_src[warp + i * (kThreads / 32)];
+        const int64_t row = src >= 0 ? src : -2 - src;
+        wraw[i] = make_uint4(0u, 0u, 0u, 0u);
+        wscale[i] = 0u;
+        if (src != -1 && lane < 28) {
+          wraw[i] = ldg_now_v4((src >= 0 ? ly.swa_codes : tl.draft_codes) + row * 448 + 16 * lane);
+          wscale[i] = ldg_now_u8((src >= 0 ? ly.swa_scales : tl.draft_scales) + row * 8 + (lane >> 2));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pc = lane + 32 * u;   // piece pc % 8 of row pc / 8
+        const int32_t src = sm.win_src[warp + (pc >> 3) * (kThreads / 32)];
+        const int64_t row = src >= 0 ? src : -2 - src;
+        wrope[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (src != -1)
+          wrope[u] = ldg_now_v4((src >= 0 ? ly.swa_rope : tl.draft_rope) + row * 64 + 8 * (pc & 7));
+      }
+    }
+  }
   // S^T: two accumulators of 64 columns (even and odd K steps), summed by
   // the softmax; O^T: 4 d-tiles x 64 columns
   const uint32_t s_col = 0, o_col = 128;
@@ -416,17 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto window_piece = [&](int e, int c, int k) -> uint4 {
     const bool live = e < swa_count;
     if (!live) return make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (kTree) {
-      if (e >= win_n) {
-        const TreeLayer& tl = p.tree[layer];
-        const int64_t row = sm.draft_row[e - win_n];
-        if (c == 7) return __ldg(reinterpret_cast<const uint4*>(tl.draft_rope + row * 64) + k);
-        const float sc = ue8m0_value(__ldg(tl.draft_scales + row * 8 + c));
-        const uint2 cc =
-            __ldg(reinterpret_cast<const uint2*>(tl.draft_codes + row * 448 + 64 * c + 8 * k));
-        return e4m3_piece(cc.x, cc.y, sc);
-      }
-    }
     const int64_t row = (int64_t)swa_row0 + e;
     if (c == 7) return __ldg(reinterpret_cast<const uint4*>(ly.swa_rope + row * 64) + k);
     const float sc = ue8m0_value(__ldg(ly.swa_scales + row * 8 + c));
@@ -473,6 +505,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- first tile: rows -> KV buffer, then S^T
   int next_topk = next_topk_after(-1);
+  if constexpr (kTree) {
+    if (win_fp8) {
+#pragma unroll
+      for (int i = 0; i < kWinRows; ++i) {
+        const int e = warp + i * (kThreads / 32);
+        if (lane < 28) {
+          const float sc = ue8m0_value(wscale[i]);
+          const int c = lane >> 2, k = 2 * (lane & 3);
+          *piece_at(e, c, k) = e4m3_piece(wraw[i].x, wraw[i].y, sc);
+          *piece_at(e, c, k + 1) = e4m3_piece(wraw[i].z, wraw[i].w, sc);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pc = lane + 32 * u;
+        *piece_at(warp + (pc >> 3) * (kThreads / 32), 7, pc & 7) = wrope[u];
+      }
+    }
+  }
   if (n_tiles > 0) {
     const int tile = sm.my_list[0];
     if (next_topk < n_tiles) {
@@ -480,7 +531,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int after = next_topk_after(next_topk);
       if (after < n_tiles) prefetch_l2(sm.my_list[after]);
     }
-    if (tile < 0 && !ly.swa_codes) {
+    if (win_fp8) {
+      if (tid < kRows) sm.row_valid[tid] = tid < swa_count;
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) {
+        for (int h = 0; h < 2; ++h) {
+          ok = mbar_wait(&sm.bar_q[h], 0, p.err, wl) && ok;
+          tc_fence_after();
+          for (int k = 0; k < 16; ++k) mma_s(16 * h + k);
+        }
+        umma_commit(&sm.bar_mma);
+      }
+    } else if (tile < 0 && !ly.swa_codes) {
       // bf16 window rows: loaded by TMA at kernel entry
       if (tid < kRows) sm.row_valid[tid] = tid < swa_count;
       if constexpr (kTree) {
@@ -493,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int e = win_n + i / 64;
           if (e >= swa_count) return make_uint4(0u, 0u, 0u, 0u);
           return __ldg(reinterpret_cast<const uint4*>(
-                           draft + (int64_t)sm.draft_row[e - win_n] * kHeadDim) + (i & 63));
+                           draft + (int64_t)(-2 - sm.win_src[e]) * kHeadDim) + (i & 63));
         };
         // the first pieces are in flight while the box arrives
         const uint4 first = tid < n_pieces ? piece_of(tid) : make_uint4(0u, 0u, 0u, 0u);
