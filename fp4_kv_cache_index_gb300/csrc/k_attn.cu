@@ -526,11 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (n_tiles > 0) {
     const int tile = sm.my_list[0];
-    if (next_topk < n_tiles) {
-      prefetch_tile(sm.my_list[next_topk]);
-      const int after = next_topk_after(next_topk);
-      if (after < n_tiles) prefetch_l2(sm.my_list[after]);
-    }
+    auto request_next = [&]() {
+      if (next_topk < n_tiles) {
+        prefetch_tile(sm.my_list[next_topk]);
+        const int after = next_topk_after(next_topk);
+        if (after < n_tiles) prefetch_l2(sm.my_list[after]);
+      }
+    };
+    // a window tile of a tree: its rows are written, and its S^T issued,
+    // before the first top-k tile's loads are
+    const bool window_now = kTree && tile < 0;
+    if (!window_now) request_next();
     if (win_fp8) {
       if (tid < kRows) sm.row_valid[tid] = tid < swa_count;
       fence_proxy_async_smem();
@@ -543,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         umma_commit(&sm.bar_mma);
       }
+      request_next();
     } else if (tile < 0 && !ly.swa_codes) {
       // bf16 window rows: loaded by TMA at kernel entry
       if (tid < kRows) sm.row_valid[tid] = tid < swa_count;
@@ -572,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncthreads();
+        request_next();   // (warp 0, which issues the MMAs, loads nothing)
         if (tid == 0) {
           for (int h = 0; h < 2; ++h) {
             ok = mbar_wait(&sm.bar_q[h], 0, p.err, wl) && ok;
