@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // come in two channel halves so that S^T of half 0 can start before half 1
   // has arrived.
   const bool swa_first = swa_count > 0 && split == 0;
+  const bool win_box = swa_first && !ly.swa_codes && swa_box;
   if (tid == 0) {
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sm.bar_q[h], 1);
@@ -212,18 +213,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     for (int h = 0; h < 2; ++h) {
       mbar_arrive_expect_tx(&sm.bar_q[h], kHG * kHeadDim);
-      for (int c = 4 * h; c < 4 * h + 4; ++c)
-        tma_load_2d(qs + c * (kHG * 128), tm_q, 64 * c, q * p.n_heads + hg * kHG, &sm.bar_q[h]);
-      if (swa_first && !ly.swa_codes && swa_box) {
-        mbar_arrive_expect_tx(&sm.bar_kv[h], kRows * kHeadDim);
-        for (int c = 4 * h; c < 4 * h + 4; ++c)
-          tma_load_2d(kv + c * (kRows * 128), tm_swa, 64 * c, swa_row0, &sm.bar_kv[h]);
-      }
+      if (win_box) mbar_arrive_expect_tx(&sm.bar_kv[h], kRows * kHeadDim);
     }
+  }
+  if (warp == 0) {
+    // a box to a lane (one thread issuing all sixteen held the CTA back)
+    __syncwarp();
+    const int c = lane & 7, h = c >> 2;
+    if (lane < 8)
+      tma_load_2d(qs + c * (kHG * 128), tm_q, 64 * c, q * p.n_heads + hg * kHG, &sm.bar_q[h]);
+    else if (lane < 16 && win_box)
+      tma_load_2d(kv + c * (kRows * 128), tm_swa, 64 * c, swa_row0, &sm.bar_kv[h]);
+    __syncwarp();
   }
   if (tid < kMaxTiles) sm.tile_any[tid] = 0;
   if (tid < kHG) { sm.m[tid] = -INFINITY; sm.l[tid] = 0.0f; }
-  if (warp == 0) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
+  if (warp == 1) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -949,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
