@@ -18,8 +18,7 @@ LIB = os.path.join(PKG, "libcsa2.so")
 DEBUG_BUILD = os.path.join(ROOT, "_build_debug")
 DEBUG_LIB = os.path.join(PKG, "libcsa2_debug.so")
 SOURCES = ["csa2_api.cu", "k_append.cu", "k_index.cu", "k_index_fp4.cu", "k_topk.cu", "k_attn.cu",
-           "k_hsi.cu", "k_swa.cu", "k_tree.cu", "k_norm_rope.cu",
-           "k_index_pair.cu"]
+           "k_hsi.cu", "k_swa.cu", "k_tree.cu", "k_norm_rope.cu"]
 HEADERS = ["csa2_device.cuh", "csa2_kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1527,8 +1527,7 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
     const int s = t->seq_ids ? t->seq_ids[i] : i;
     tiles512 += (int64_t)((t->n_draft[i] + 3) / 4) * ((c->len[s] + 511) / 512);
   }
-  const bool pair = !mx && qpg == 8 && c->index_sms >= 2;
-  const int tile = pair ? 256 : !mx ? 128 : tiles512 >= c->num_sms ? 512 : 256;
+  const int tile = !mx ? 128 : tiles512 >= c->num_sms ? 512 : 256;
   const uint16_t* qb = static_cast<const uint16_t*>(q_idx);
   int64_t q0 = 0, done = 0;   // queries before this launch, queries of the sequence already taken
   int seq = 0;
@@ -1584,12 +1583,11 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
       e = launch_index_fp4_tree(*ip, c->tm_kq, grid, S(stream));
     } else {
       CUtensorMap tm_q;
-      if (!make_map(&tm_q, qn, (uint64_t)n * kIdxHeads, kIdxDim, 64, pair ? 128 : 32 * qpg)) {
+      if (!make_map(&tm_q, qn, (uint64_t)n * kIdxHeads, kIdxDim, 64, 32 * qpg)) {
         st = CSA2_ERR_CUDA;
         break;
       }
-      e = pair ? launch_index_pair(*ip, c->tm_k, tm_q, std::min(c->index_sms / 2, tiles), S(stream))
-               : launch_index_tree(*ip, c->tm_k, tm_q, grid, S(stream));
+      e = launch_index_tree(*ip, c->tm_k, tm_q, grid, S(stream));
     }
     if (e != cudaSuccess) st = CSA2_ERR_CUDA;
   }

@@ -108,12 +108,8 @@ struct TreeIndexParams : IndexParams {
   int32_t q_first[kMaxTreeQueries + 1];  // first query of each group
   int32_t n_com[kMaxTreeQueries];        // committed entries of the group's sequence
   uint64_t ents[kMaxTreeQueries];        // per query: its path's entries
-  int32_t tile_keys;                     // keys of a tile: 128 or (pairs) 256, MXFP4 keys 256 or 512
+  int32_t tile_keys;                     // keys of a tile: 128 (bf16 keys), 128 to 512 (MXFP4 keys)
 };
-// Groups of up to eight queries on pairs of CTAs (k_index_pair.cu): qpg 8,
-// tile_keys 256; tm_k as for launch_index, tm_q in boxes of 128 rows.
-cudaError_t launch_index_pair(const TreeIndexParams& p, const CUtensorMap& tm_k,
-                              const CUtensorMap& tm_q, int pairs, cudaStream_t s);
 int index_smem_bytes(int qpg);
 cudaError_t launch_index_tree(const TreeIndexParams& p, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_q, int grid, cudaStream_t s);

@@ -771,13 +771,3 @@ def test_refusals():
     C.csa2_cache_accept_tree(c, t, [2, -1])
     assert [c.length(i) for i in range(2)] == [42, 20]
     refused(lambda: C.csa2_cache_accept_tree(c, t, [2, -1]), 1)      # the step is over
-
-
-def test_the_readme_step_runs():
-    import os
-    import re
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    text = open(os.path.join(root, "README.md")).read()
-    code = re.findall(r"```python\n(.*?)```", text, re.S)[1]
-    assert "csa2_cache_accept_tree" in code
-    exec(compile(code, "README.md", "exec"), {})
