@@ -717,6 +717,26 @@ def test_no_drafts_at_all():
     C.csa2_cache_accept_tree(st.cache, none, [])
 
 
+@pytest.mark.parametrize("idx_layout", [0, 1])
+def test_a_wait_that_runs_out_is_reported(idx_layout):
+    """The indexer's key loads are withheld: its waits run out, the error word
+    says so, and the cache works afterwards."""
+    import fp4_kv_cache_index_gb300 as C
+    st = Setup([random_tree(9, 2), random_tree(6, 3)], [700, 300], idx_layout=idx_layout)
+    good = C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w)
+    scores = torch.full((st.nq, 768), -5.0, device="cuda")
+    st.cache.set_wait_limit(200_000)
+    st.cache.inject_fault(1)
+    C.csa2_index_scores_tree(st.cache, st.tree, st.q_idx, st.w, scores)
+    torch.cuda.synchronize()
+    assert torch.all(scores == -5.0)
+    assert st.cache.device_error() == 6
+    st.cache.inject_fault(0)
+    st.cache.set_wait_limit(0)
+    assert torch.equal(C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w), good)
+    assert st.cache.device_error() == 0
+
+
 def test_refusals():
     import fp4_kv_cache_index_gb300 as C
     st = Setup([[-1, 0, 0], [-1]], [40, 20])
@@ -771,3 +791,13 @@ def test_refusals():
     C.csa2_cache_accept_tree(c, t, [2, -1])
     assert [c.length(i) for i in range(2)] == [42, 20]
     refused(lambda: C.csa2_cache_accept_tree(c, t, [2, -1]), 1)      # the step is over
+
+
+def test_the_readme_step_runs():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code = re.findall(r"```python\n(.*?)```", text, re.S)[1]
+    assert "csa2_cache_accept_tree" in code
+    exec(compile(code, "README.md", "exec"), {})
