@@ -72,7 +72,7 @@ struct Small {
   int32_t n_tiles;
   float rope_c[32], rope_s[32];  // output RoPE(-i): cos, sin of each channel pair
   uint32_t tmem;
-  uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2];   // [h]: channel half h
+  uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2], bar_fill[2];   // [h]: channel half h
   // trees: source of each window row (>= 0 a committed row, <= -2 draft row
   // -2 - x, -1 none)
   int32_t win_src[kRows];
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.bar_q[h], 1);
       mbar_init(&sm.bar_kv[h], 1);
       mbar_init(&sm.bar_o[h], 1);
+      mbar_init(&sm.bar_fill[h], kThreads / 32 - 1);   // the filling warps
     }
     mbar_init(&sm.bar_mma, 1);
     fence_barrier_init();
@@ -739,20 +740,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The next tile (always a top-k tile: the window comes first) replaces
       // the KV buffer half by half: half 0 once O^T d-blocks 0-1 are done
       // (while blocks 2-3 run), half 1 once blocks 2-3 are done (while S^T of
-      // half 0 runs).
+      // half 0 runs).  The workers signal each half and run on to the next;
+      // warp 0 issues S^T of a half when all have.
       const int tile = sm.my_list[ti + 1];
+      if (warp == 0) {
+        sm.row_valid[lane] = idx_s[tile * kRows + lane] >= 0;
+        if (lane == 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        ok = mbar_wait(&sm.bar_o[h], ph_o, p.err, wl) && ok;
-        tc_fence_after();
-        fill_half(tile, h);
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
+          for (int h = 0; h < 2; ++h) {
+            ok = mbar_wait(&sm.bar_fill[h], ph_o, p.err, wl) && ok;
+            tc_fence_after();
+            for (int k = 0; k < 16; ++k) mma_s(16 * h + k);
+          }
+          umma_commit(&sm.bar_mma);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = mbar_wait(&sm.bar_o[h], ph_o, p.err, wl) && ok;
           tc_fence_after();
-          for (int k = 0; k < 16; ++k) mma_s(16 * h + k);
-          if (h == 1) umma_commit(&sm.bar_mma);
+          fill_half(tile, h);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.bar_fill[h]);
         }
       }
       next_topk = next_topk_after(next_topk);
