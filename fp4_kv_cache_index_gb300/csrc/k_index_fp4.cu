@@ -632,7 +632,16 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     // that one set computes while the other waits; a warp has one TMEM lane
     // quadrant and two of the group's four queries, and its loads of tensor
     // memory run one half row (16 heads) ahead of the arithmetic.  Lane l of
-    // quadrant q holds key 4 l + q of the M-group.
+    // quadrant q holds key 4 l + q of the M-group.  (A set that waits for an
+    // accumulator's phase must have seen the one before it: M-group u waits
+    // on accumulator u % 3 after M-group u - 2 was taken, whose products
+    // follow those of u - 3.  More sets than accumulators would misread the
+    // phase's parity.)  Measured, 4 x 29 drafts (104 in all, ragged) over
+    // 128K entries, 13 million scores: 100 us; 163 us with 128-key tiles, eight warps taking every tile and two warps preparing the first
+    // group's queries.  What bounds it now is the issuing thread's serial work
+    // (two MMAs, two to three waits and a commit an M-group, about 1000 cycles
+    // beside the epilogue): three sets of four warps take the same time, and
+    // so does coalescing the stores through shared memory or worse (122 us).
     if constexpr (kTree) {
       const int quad = warp & 3, set = (warp - 2) >> 3, j0 = ((warp - 2) >> 2 & 1) * 2;
       const int et = threadIdx.x - 64;

@@ -765,7 +765,9 @@ csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t
 /* Ends the step: of tree i the path of draft accepted[i] (-1: none) becomes
  * committed.  Its entries move up behind the committed ones, the other
  * drafts' entries are dropped and the sequence's length follows; a next
- * tree's pos0 is pos0[i] + the path's length.  accepted: host [n_seqs].     */
+ * tree's pos0 is pos0[i] + the path's length.  accepted: host [n_seqs].  Like
+ * the append calls it changes the host's lengths when it is called, so it does
+ * not belong into a captured graph that is replayed.                        */
 csa2_status_t csa2_cache_accept_tree(csa2_cache_t* cache, const csa2_tree_t* tree,
                                      const int32_t* accepted, csa2_stream_t stream);
 
