@@ -3,6 +3,7 @@
 // the kernels in k_append.cu, k_index.cu, k_topk.cu and k_attn.cu.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -1848,7 +1849,8 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
   CSA2_RANGE();
   if (n_parts < 0 || n_parts > CSA2_MAX_NORM_PARTS || (n_parts > 0 && !parts))
     return CSA2_ERR_INVALID_ARG;
-  if (!(eps >= 1e-30f) || !std::isfinite(eps) || !(rope_base >= 0.0) || !std::isfinite(rope_base))
+  if (!(eps >= 1e-30f && eps <= 1.0f) || !(rope_base == 0.0 || rope_base >= 1.0) ||
+      !std::isfinite(rope_base))
     return CSA2_ERR_INVALID_ARG;
   NormParams p;
   std::memset(&p, 0, sizeof(p));
@@ -1863,6 +1865,7 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
     if ((a.x_fp32 != 0 && a.x_fp32 != 1) || (a.out_fp32 != 0 && a.out_fp32 != 1))
       return CSA2_ERR_INVALID_ARG;
     if (a.n_tokens == 0) continue;
+    if (a.n_tokens > kNormMaxRows / a.n_heads) return CSA2_ERR_UNSUPPORTED;
     if (!a.x || !a.out || !aligned16(a.x) || !aligned16(a.out) ||
         (a.weight && !aligned16(a.weight)) || (a.rope_dim > 0 && !a.pos) ||
         (reinterpret_cast<uintptr_t>(a.pos) & 7u))
@@ -1871,6 +1874,11 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
     // the stride of an axis of one is not used
     if ((a.n_tokens > 1 && (a.x_token_stride % xa || a.out_token_stride % oa)) ||
         (a.n_heads > 1 && (a.x_head_stride % xa || a.out_head_stride % oa)))
+      return CSA2_ERR_INVALID_ARG;
+    // strides that lay two heads of the output over each other
+    const int64_t ot = std::llabs(a.out_token_stride), oh = std::llabs(a.out_head_stride);
+    if ((a.n_tokens > 1 && ot < a.dim) || (a.n_heads > 1 && oh < a.dim) ||
+        (a.n_tokens > 1 && a.n_heads > 1 && ot == oh))
       return CSA2_ERR_INVALID_ARG;
     NormPart& d = p.part[p.n_parts];
     d.x = a.x;
@@ -1894,10 +1902,9 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
     d.rope_table = row;
     if (row == p.n_parts)
       for (int t = 0; t < a.rope_dim / 2; ++t) {
-        // 2^64 * base^(-2t / rope_dim) / (2 pi); below one turn for any base
-        // >= 1, and only the fraction of a turn counts otherwise
+        // 2^64 * base^(-2t / rope_dim) / (2 pi), below one turn as base >= 1
         const double f = std::pow(base, -2.0 * t / a.rope_dim) * 0.15915494309189535;
-        p.turns[row][t] = (uint64_t)((f - std::floor(f)) * 18446744073709551616.0);
+        p.turns[row][t] = (uint64_t)(f * 18446744073709551616.0);
       }
     ++p.n_parts;
   }

@@ -168,6 +168,7 @@ cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
 // ---------------------------------------------------------------- norm + rotation
 constexpr int kNormMaxParts = 8;
 constexpr int kNormMaxPairs = 64;     // rotated channels / 2
+constexpr int64_t kNormMaxRows = (int64_t)1 << 31;   // heads of a tensor: 256 GB of the narrowest
 struct NormPart {
   const void* x;
   void* out;

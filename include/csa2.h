@@ -639,12 +639,14 @@ csa2_status_t csa2_sparse_attn_prefill_layers(const csa2_cache_t* cache, int32_t
  *     dim] with the given strides in elements (the channels of a head are
  *     contiguous); every head 16-byte aligned.  out may be x with the same
  *     type and strides; any other overlap is not allowed, nor may two heads
- *     of an output overlap.
+ *     of an output overlap (strides that make them are refused where one is
+ *     below dim or both are equal).
  *   weight: nullable dev fp32 [dim];  pos: dev int64 [n_tokens] (may be NULL
  *     without rotation), any value;  dim: 64, 128, 256 or 512 (else
  *     CSA2_ERR_UNSUPPORTED);  rope_dim: 0 (no rotation) up to dim, a multiple
  *     of 8, at most 128.
- *   eps: at least 1e-30 (finite);  rope_base: 0 means 10000.
+ *   n_tokens * n_heads: at most 2^31 (else CSA2_ERR_UNSUPPORTED);
+ *   eps: 1e-30 to 1;  rope_base: at least 1, or 0 for 10000.
  * A head that holds an infinity or a NaN gives what the formula gives.      */
 #define CSA2_MAX_NORM_PARTS 8
 typedef struct {

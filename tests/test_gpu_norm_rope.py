@@ -237,3 +237,24 @@ def test_refusals():
         C.csa2_norm_rope([rand((4, 2, 96))], pos)
     with pytest.raises(C.Csa2Error):
         C.csa2_norm_rope([x], pos, eps=0.0)
+    with pytest.raises(C.Csa2Error):      # every token of the output on one place
+        C.csa2_norm_rope([x], pos, outs=[rand((1, 2, 128)).expand(4, 2, 128)])
+    with pytest.raises(C.Csa2Error):
+        C.csa2_norm_rope([x], pos, eps=2.0)
+
+
+def test_the_ends_of_the_ranges():
+    """eps 1 beside squares beyond fp32 and beside zeros; the smallest eps; an
+    input that broadcasts one token."""
+    import fp4_kv_cache_index_gb300 as C
+    x = rand((4, 3, 256), torch.float32, 8)
+    x[1] *= 1e30
+    x[2] = 0
+    x[3] *= 1e-12
+    pos = positions(4)
+    for eps in (1.0, 1e-30):
+        y, = C.csa2_norm_rope([x], pos, eps=eps)
+        check(y, x, pos, None, 64, eps=eps)
+    one = rand((1, 3, 256)).expand(4, 3, 256)
+    y, = C.csa2_norm_rope([one], pos, outs=[torch.empty(4, 3, 256, dtype=torch.bfloat16, device="cuda")])
+    check(y, one, pos, None, 64)

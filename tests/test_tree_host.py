@@ -113,3 +113,23 @@ def test_norm_rope_scalar_checks():
     assert L.csa2_norm_rope(9, ctypes.byref(a), 1e-6, 0.0, None) == 1
     assert L.csa2_norm_rope(1, None, 1e-6, 0.0, None) == 1
     assert L.csa2_norm_rope(0, None, 1e-6, 0.0, None) == 0
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(out_token_stride=0), 1), (dict(out_token_stride=256), 1), (dict(out_token_stride=-256), 1),
+    (dict(n_heads=2, n_tokens=1, out_head_stride=0), 1), (dict(n_heads=2), 1),
+    (dict(n_tokens=(1 << 31) + 1), 2), (dict(n_tokens=1 << 62, n_heads=4, out_head_stride=1024), 2),
+    (dict(n_tokens=1 << 24, n_heads=129, out_token_stride=1 << 17), 2),
+])
+def test_norm_rope_refuses_heads_over_each_other_and_endless_tensors(kw, status):
+    assert L.csa2_norm_rope(1, ctypes.byref(part(**kw)), 1e-6, 0.0, None) == status
+
+
+def test_norm_rope_refuses_an_eps_or_a_base_outside_the_formula_s_range():
+    """An eps above 1 would count beside squares beyond fp32; a base below 1
+    turns a channel by more than a turn per position."""
+    a = part()
+    for eps in (1.5, 1e30, 3.4e38):
+        assert L.csa2_norm_rope(1, ctypes.byref(a), eps, 0.0, None) == 1
+    for base in (1e-300, 0.5, 0.999):
+        assert L.csa2_norm_rope(1, ctypes.byref(a), 1e-6, base, None) == 1
