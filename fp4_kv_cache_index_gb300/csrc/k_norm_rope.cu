@@ -50,6 +50,12 @@ __host__ __device__ constexpr int rows_per_block(int dim, bool fp32) {
   return kNormThreads / (dim / 16) * (fp32 ? iters_of<true>() : iters_of<false>());
 }
 
+// The sine table of a block stays below the 48 KB that a launch may ask for
+// without an attribute of the kernel (which calls from several threads would
+// set over each other): at most one token a row, dim / 2 pairs up to 64.
+static_assert(rows_per_block(64, false) * 32 * sizeof(float2) <= 48 * 1024, "sine table");
+static_assert(rows_per_block(128, false) * kNormMaxPairs * sizeof(float2) <= 48 * 1024, "sine table");
+
 // Eight channels as they are in memory.  Plain loads, not the read-only path:
 // the output may be the input.
 template <bool kF32>
@@ -248,9 +254,6 @@ cudaError_t launch_norm_rope(const NormParams& p_in, cudaStream_t s) {
   p.block0[p.n_parts] = blocks;
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_norm_rope, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kNormThreads);

@@ -258,3 +258,31 @@ def test_the_ends_of_the_ranges():
     one = rand((1, 3, 256)).expand(4, 3, 256)
     y, = C.csa2_norm_rope([one], pos, outs=[torch.empty(4, 3, 256, dtype=torch.bfloat16, device="cuda")])
     check(y, one, pos, None, 64)
+
+
+def test_calls_from_two_threads():
+    """Launches of different table sizes issued at once from two threads, each
+    on its own stream."""
+    import threading
+    import fp4_kv_cache_index_gb300 as C
+    xs = [rand((96, 1, 64), seed=1), rand((2, 64, 512), seed=2)]
+    ps = [positions(96, 3), positions(2, 4)]
+    torch.cuda.synchronize()
+    outs, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(300):
+                    outs[i] = C.csa2_norm_rope([xs[i]], ps[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001 - reported below
+            errors.append(e)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors
+    for i in range(2):
+        check(outs[i][0], xs[i], ps[i], None, 64)
