@@ -687,12 +687,12 @@ def _shaped(t: torch.Tensor, shape, dtype, what: str, dev: int):
     return t.data_ptr()
 
 
-def _scratch(nbytes: int, device, stream):
-    """A workspace that belongs to the stream the call runs on."""
+def _empty(shape, dtype, device, stream):
+    """An output, or a workspace, that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=None, norms=None,
@@ -710,7 +710,7 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
     if n > 8:
         raise ValueError("csa2_norm_rope: at most 8 tensors")
     if outs is None:
-        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+        outs = [_empty(x.shape, x.dtype, x.device, stream) for x in xs]
     one_pos, one_dim = isinstance(positions, torch.Tensor), isinstance(rope_dim, int)
     if (len(outs) != n or (weights is not None and len(weights) != n)
             or (norms is not None and len(norms) != n)
@@ -823,10 +823,12 @@ def csa2_index_topk_tree(cache: Cache, tree: Tree, q_idx: torch.Tensor, w: torch
     int32 [n_queries, topk] entries of the cache, ascending, -1 padded."""
     nq, c, dev = tree.n_queries, cache.cfg, torch.cuda.current_device()
     if topk_idx is None:
-        topk_idx = torch.empty(nq, c.topk, dtype=torch.int32, device=q_idx.device)
+        topk_idx = _empty((nq, c.topk), torch.int32, q_idx.device, stream)
     ws = workspace
     if ws is None:
-        ws = _scratch(csa2_index_workspace_bytes(cache, nq), q_idx.device, stream)
+        ws = _empty(max(16, csa2_index_workspace_bytes(cache, nq)), torch.uint8, q_idx.device, stream)
+    elif ws.get_device() != dev:
+        raise ValueError("workspace: expected on the current device")
     _check(lib.csa2_index_topk_tree(
         cache.handle, tree.ref,
         _shaped(q_idx, (nq, c.idx_heads, c.idx_dim), torch.bfloat16, "q_idx", dev),
@@ -883,7 +885,7 @@ def csa2_sparse_attn_tree_layers(cache: Cache, tree: Tree, qs: Sequence[torch.Te
     H, D, W, bf16 = c.n_heads, c.head_dim, c.swa, torch.bfloat16
     dev = torch.cuda.current_device()
     if outs is None:
-        outs = [torch.empty(q.shape, dtype=q.dtype, device=q.device) for q in qs]
+        outs = [_empty(q.shape, q.dtype, q.device, stream) for q in qs]
     for xs in (outs, lses, sinks, swa_kvs, draft_kvs, swa_fp8s, draft_fp8s):
         if xs is not None and len(xs) != L:
             raise ValueError("csa2_sparse_attn_tree_layers: one entry per layer expected")

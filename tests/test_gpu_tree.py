@@ -667,6 +667,31 @@ def test_graph_capture_and_another_stream():
     assert torch.equal(idx2, idx)
 
 
+def test_outputs_belong_to_the_stream_of_the_call():
+    """Memory that the current stream has just given back may still be read by
+    its pending work: a call on another stream must not return it."""
+    import fp4_kv_cache_index_gb300 as C
+    st = Setup([random_tree(20, 9), chain(5)], [2500, 60])
+    wd = window(st, 341)
+    q = rn(3, st.nq, 64, 512).bfloat16()
+    pos = st.tree.positions()
+    idx = C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w)
+    here = [lambda s: C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w, stream=s),
+            lambda s: run_readout(st, idx, q, wd, stream=s),
+            lambda s: C.csa2_norm_rope([q], pos, stream=s)[0]]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for call in here:
+        want = call(None)
+        freed = torch.empty_like(want)
+        place = freed.data_ptr()
+        del freed
+        got = call(s)
+        s.synchronize()
+        assert got.data_ptr() != place
+        assert torch.equal(got, want)
+
+
 def test_repeats_are_the_same_bits():
     import fp4_kv_cache_index_gb300 as C
     st = Setup([random_tree(64, 9), random_tree(64, 10)], [9000, 5000])
@@ -765,6 +790,7 @@ def test_refusals():
     mx = Setup([[-1, 0, 0], [-1]], [40, 20], idx_layout=1)
     hist = torch.zeros(4, 2048, dtype=torch.int32, device="cuda")
     refused(lambda: C.csa2_index_scores_tree(mx.cache, mx.tree, qi, w, scores, key_hist=hist), 2)
+    refused(lambda: C.csa2_index_topk_tree(c, t, qi, w, workspace=torch.empty(1 << 20, dtype=torch.uint8)))
     refused(lambda: C.csa2_index_topk_tree(c, t, qi, w, workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), 3)
     idx = C.csa2_index_topk_tree(c, t, qi, w)
     wd = window(st, 5)
