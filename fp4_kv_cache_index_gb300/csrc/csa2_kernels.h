@@ -108,7 +108,7 @@ struct TreeIndexParams : IndexParams {
   int32_t q_first[kMaxTreeQueries + 1];  // first query of each group
   int32_t n_com[kMaxTreeQueries];        // committed entries of the group's sequence
   uint64_t ents[kMaxTreeQueries];        // per query: its path's entries
-  int32_t tile_keys;                     // keys of a tile: 128 (bf16 keys), 128 to 512 (MXFP4 keys)
+  int32_t tile_keys;                     // keys of a tile: 128 (bf16 keys), 256 or 512 (MXFP4 keys)
 };
 int index_smem_bytes(int qpg);
 cudaError_t launch_index_tree(const TreeIndexParams& p, const CUtensorMap& tm_k,

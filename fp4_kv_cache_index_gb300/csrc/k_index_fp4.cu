@@ -637,11 +637,12 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     // on accumulator u % 3 after M-group u - 2 was taken, whose products
     // follow those of u - 3.  More sets than accumulators would misread the
     // phase's parity.)  Measured, 4 x 29 drafts (104 in all, ragged) over
-    // 128K entries, 13 million scores: 100 us; 163 us with 128-key tiles, eight warps taking every tile and two warps preparing the first
-    // group's queries.  What bounds it now is the issuing thread's serial work
-    // (two MMAs, two to three waits and a commit an M-group, about 1000 cycles
-    // beside the epilogue): three sets of four warps take the same time, and
-    // so does coalescing the stores through shared memory or worse (122 us).
+    // 128K entries, 13 million scores: 100 us; 163 us with 128-key tiles,
+    // eight warps taking every tile and two warps preparing the first group's
+    // queries.  What bounds it now is the issuing thread's serial work (two
+    // MMAs, two to three waits and a commit an M-group, about 1000 cycles
+    // beside the epilogue).  Not faster: three sets of four warps (the same),
+    // stores coalesced through shared memory (122 us).
     if constexpr (kTree) {
       const int quad = warp & 3, set = (warp - 2) >> 3, j0 = ((warp - 2) >> 2 & 1) * 2;
       const int et = threadIdx.x - 64;
@@ -901,7 +902,7 @@ cudaError_t launch_index_fp4(const IndexParams& p, const CUtensorMap& tm_kq,
 
 cudaError_t launch_index_fp4_tree(const TreeIndexParams& p, const CUtensorMap& tm_kq, int grid,
                                   cudaStream_t s) {
-  if (p.qpg != kMaxQpg || (p.tile_keys != 128 && p.tile_keys != 256 && p.tile_keys != kTileMax))
+  if (p.qpg != kMaxQpg || (p.tile_keys != 256 && p.tile_keys != kTileMax))
     return cudaErrorInvalidValue;
   return launch_any(p, tm_kq, tm_kq, grid, s);
 }
