@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 62);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = 32 * p.qpg;                      // MMA N
+  const int N = kTree ? kBRows : 32 * p.qpg;     // MMA N
   const bool pool = !kTree && p.pool != nullptr;
   // first query of group g, and one past its last
   auto q_begin = [&](int g) -> int {
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
   const int mgroups = tile_e / 128;
   // columns of an accumulator: a tile's (128, 64 or 128), trees: an M-group's
   const int acc_cols = kTree ? N : mgroups * N;
-  const int nacc = min(kNAcc, (int)kAccCols / acc_cols);   // 3, 4 or 3 accumulators
+  const int nacc = kTree ? (int)kAccCols / kBRows : min(kNAcc, (int)kAccCols / acc_cols);   // 3, 4 or 3 accumulators
   const int blocks_per_tile = tile_e / 8;
   // Contiguous keys: tiles are aligned chunks of tile_e key rows, so a
   // sequence starting inside a chunk begins `lead` keys into its first tile
@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
   // (elsewhere the epilogue bounds the pipeline and the MMA issuer copies
   // them itself)
   const bool sf_warp = kTree || (perm && p.qpg == 1);
-  // trees: whether M-group mg of tile t holds any entry of the sequence
-  auto unit_live = [&](int t, int mg, int lead, int nvis) -> bool {
-    const int e = t * tile_e + mg * 128 - lead;
-    return e < nvis && e + 128 > 0;
+  // trees: the M-groups [a, b) of the tile whose first key is entry e0 (below
+  // 0 in the sequence's first tile) that hold entries of the sequence
+  auto live_groups = [&](int e0, int nvis, int& a, int& b) {
+    a = e0 < 0 ? -e0 >> 7 : 0;
+    b = min(mgroups, (nvis - e0 + 127) >> 7);
   };
   auto slot_key = [&](int sl) -> int {
     return perm ? (sl & ~127) + 4 * (sl & 31) + ((sl >> 5) & 3) : sl;
@@ -598,10 +599,11 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       }
       const uint32_t bo = (uint32_t)((gi & 1) * kBSlotBytes) >> 4;
       const uint32_t sfb = tmem_base + kSfbCol + 4 * (gi & 1);
-      for (int mg = 0; mg < mgroups; ++mg) {
+      // trees: an accumulator per M-group; those past the sequence are skipped
+      int mg_a = 0, mg_b = mgroups;
+      if constexpr (kTree) live_groups((it - gc.lo) * tile_e - lead, nvis, mg_a, mg_b);
+      for (int mg = mg_a; mg < mg_b; ++mg) {
         if constexpr (kTree) {
-          // an accumulator per M-group; those past the sequence are skipped
-          if (!unit_live(it - gc.lo, mg, lead, nvis)) continue;
           ok = mbar_wait(acc_empty + acc, aph ^ 1, p.err, wl);
           if (!ok) break;
           tc_fence_after();
@@ -637,12 +639,18 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     // on accumulator u % 3 after M-group u - 2 was taken, whose products
     // follow those of u - 3.  More sets than accumulators would misread the
     // phase's parity.)  Measured, 4 x 29 drafts (104 in all, ragged) over
-    // 128K entries, 13 million scores: 100 us; 163 us with 128-key tiles,
+    // 128K entries, 13 million scores: 80 us; 163 us with 128-key tiles,
     // eight warps taking every tile and two warps preparing the first group's
-    // queries.  What bounds it now is the issuing thread's serial work (two
-    // MMAs, two to three waits and a commit an M-group, about 1000 cycles
-    // beside the epilogue).  Not faster: three sets of four warps (the same),
-    // stores coalesced through shared memory (122 us).
+    // queries; 99 us with each M-group of a tile tested for entries instead of
+    // counted (both sides' loops: instructions, few warps to hide them, are
+    // what this kernel spends its time on).  What bounds it now: an M-group
+    // takes 870 cycles, the issuing thread's serial work (550 with no epilogue
+    // beside it, whatever the MMAs' size) next to 1600 in each set, of which
+    // a fifth is the weights' loads.  Not faster: three sets of four warps
+    // (86 us), of eight (72 registers: 130), the next M-group's columns
+    // requested early (82), waits tried ahead in the issuer (82), the whole
+    // warp in the issuer's loop (no change), stores coalesced through shared
+    // memory (122 against 100 then).
     if constexpr (kTree) {
       const int quad = warp & 3, set = (warp - 2) >> 3, j0 = ((warp - 2) >> 2 & 1) * 2;
       const int et = threadIdx.x - 64;
@@ -656,12 +664,16 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
         if (lane == 0) mbar_arrive(b_first);
       }
       Cursor gc = c0;
-      int cur = -1, acc = 0, turn = 0;    // turn: which set takes the next M-group
+      // M-groups are counted through the CTA's tiles: `unit` is the first of
+      // the tile, `next` this set's next one, in accumulator `acc`
+      int cur = -1, unit = 0, next = set, acc = set;
       uint32_t aph = 0;
       int ncom = 0, nvis = 0, lead = 0;   // committed entries, and with the drafts'
       int mine = 0;                       // this warp's queries of the group
       uint64_t path[2] = {0, 0};
       float* out[2] = {nullptr, nullptr};
+      const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(j0 * 32);
+      const float* w = wbuf + j0 * 32;
       bool ok = true;
       for (int it = begin; it < end && ok; ++it) {
         gc.advance(p, it);
@@ -686,26 +698,21 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
             out[jj] = p.scores + (int64_t)q * p.ld;
           }
         }
-        const int t = it - gc.lo;
-        for (int mg = 0; mg < mgroups; ++mg) {
-          if (!unit_live(t, mg, lead, nvis)) continue;
-          const int a_me = acc;
-          const uint32_t ph_me = aph;
-          const bool take = turn == set;
-          turn ^= 1;
-          if (++acc == nacc) { acc = 0; aph ^= 1; }
-          if (!take) continue;
-          ok = mbar_wait_sleep(acc_full + a_me, ph_me, p.err, wl);
+        const int et0 = (it - gc.lo) * tile_e - lead;   // entry of the tile's first key
+        int mg_a, mg_b;
+        live_groups(et0, nvis, mg_a, mg_b);
+        const int n_units = mg_b - mg_a;
+        for (; next < unit + n_units; next += 2) {
+          ok = mbar_wait_sleep(acc_full + acc, aph, p.err, wl);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ta = tmem_base + ((uint32_t)(quad * 32) << 16) +
-                              (uint32_t)(a_me * acc_cols + j0 * 32);
+          const int e0 = et0 + (mg_a + next - unit) * 128, e = e0 + 4 * lane + quad;
+          const uint32_t ta = ta0 + (uint32_t)(acc * kBRows);
           auto release = [&]() {   // the accumulator is free once read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty + a_me);
+            if (lane == 0) mbar_arrive(acc_empty + acc);
           };
-          const int e0 = t * tile_e + mg * 128 - lead, e = e0 + 4 * lane + quad;
           const bool inner = e0 >= 0 && e0 + 128 <= ncom;   // committed entries only
           auto store = [&](int jj, float s) {
             int col = e;
@@ -723,25 +730,31 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
           uint32_t ra[16], rb[16];
           if (mine > 0) {
             tmem_ld16_issue(ta, ra);
+            tmem_ld16_issue(ta + 16, rb);
             tmem_ld16_wait(ra);
+            tmem_ld16_wait(rb);
+            uint64_t a = 0, b = 0;
+            relu_dot_chains(w, ra, 16, a, b);
+            if (mine > 1) tmem_ld16_issue(ta + 32, ra);
+            relu_dot_chains(w + 16, rb, 16, a, b);
+            if (mine > 1) tmem_ld16_issue(ta + 48, rb);
+            store(0, relu_dot_sum(a, b));
+          }
+          if (mine > 1) {
+            tmem_ld16_wait(ra);
+            tmem_ld16_wait(rb);
+            release();
+            uint64_t a = 0, b = 0;
+            relu_dot_chains(w + 32, ra, 16, a, b);
+            relu_dot_chains(w + 48, rb, 16, a, b);
+            store(1, relu_dot_sum(a, b));
           } else {
             release();
           }
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            if (jj >= mine) break;
-            const float* w = wbuf + (j0 + jj) * 32;
-            uint64_t a = 0, b = 0;
-            tmem_ld16_issue(ta + 32 * jj + 16, rb);
-            relu_dot_chains(w, ra, 16, a, b);
-            tmem_ld16_wait(rb);
-            if (jj + 1 < mine) tmem_ld16_issue(ta + 32 * (jj + 1), ra);
-            else release();
-            relu_dot_chains(w + 16, rb, 16, a, b);
-            if (jj + 1 < mine) tmem_ld16_wait(ra);
-            store(jj, relu_dot_sum(a, b));
-          }
+          acc += 2;
+          if (acc >= nacc) { acc -= nacc; aph ^= 1; }
         }
+        unit += n_units;
       }
     }
   } else if (!kTree && warp >= 2 && warp < 10) {
