@@ -679,7 +679,10 @@ cudaError_t launch_any(void (*kern)(P, CUtensorMap, CUtensorMap), int epi_warps,
                        const CUtensorMap& tm_k, const CUtensorMap& tm_q, int grid,
                        cudaStream_t s) {
   const int smem = index_smem_bytes(p.qpg);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the most that any launch of the kernel takes: calls from several threads,
+  // with groups of other sizes, must not set it below one another's need
+  const int most = p.qpg == 1 ? smem : index_smem_bytes(kMaxQpg);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);

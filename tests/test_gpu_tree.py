@@ -667,6 +667,35 @@ def test_graph_capture_and_another_stream():
     assert torch.equal(idx2, idx)
 
 
+def test_calls_from_two_threads():
+    """Trees of other widths (two and eight drafts a tile) scored at once from
+    two threads, each with its cache, stream and workspace."""
+    import threading
+    import fp4_kv_cache_index_gb300 as C
+    sts = [Setup([chain(2)], [700]), Setup([chain(16)], [900])]
+    want = [C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w) for st in sts]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            st = sts[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    got[i] = C.csa2_index_topk_tree(st.cache, st.tree, st.q_idx, st.w)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001 - reported below
+            errors.append(e)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors
+    for i in range(2):
+        assert torch.equal(got[i], want[i])
+
+
 def test_outputs_belong_to_the_stream_of_the_call():
     """Memory that the current stream has just given back may still be read by
     its pending work: a call on another stream must not return it."""
