@@ -38,8 +38,9 @@
 // brought there, so rows outside the window are never read by the MMAs.
 // Measured, 1024 drafts of 16 sequences x 64 heads x 640 candidates (86
 // GFLOP): 228 us, with FP8 windows 248 us.  What bounds it: one query has 64
-// heads, and an MMA of N = 64 takes 70-95 cycles, as long as one of N = 128
-// (a tile's 64 MMAs 5600 of its 8700 cycles); the softmax between S^T and O^T
+// heads, and an MMA of N = 64 takes 70-95 cycles, as long as one of N = 16 or
+// 128 (its 128-row operand, 4 KB, is read at 64 bytes a cycle; a tile's 64
+// MMAs 5600 of its 8700 cycles); the softmax between S^T and O^T
 // (1350); and a quarter of a CTA's 27 us is its prologue and epilogue.
 // Online softmax (base 2) runs across TMEM lanes: each thread holds one
 // candidate row; a head's running maximum moves (with a reduce-scatter over

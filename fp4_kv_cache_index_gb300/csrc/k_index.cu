@@ -413,13 +413,14 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     // queries (two at most).  Their loads of tensor memory run one half row (16
     // heads) ahead of the arithmetic, from one tile to the next too, and a tile
     // of committed entries, all but a sequence's last, is stored without any
-    // test.  Measured, 2 x 64 drafts over 131072 entries (139 GFLOP): 112 us,
-    // 64 % of the measured bf16 rate; the MMAs alone take 84 us (an MMA of N =
-    // 256 reads 12 KB of operands at about 64 bytes a cycle), the epilogue
-    // alone 90.  8 x 8 drafts over 128K entries: 61 us, 71 % of the copy
-    // bandwidth.  Not faster: two sets of warps on alternate tiles (126 us: a
-    // set's accumulator is released too late for the next MMAs), ReLUs on the
-    // FMA pipe (no change), suspended waits (no change).
+    // test.  Measured, 2 x 64 drafts over 131072 entries (139 GFLOP): 108 us,
+    // 67 % of the measured bf16 rate; the MMAs alone take 84 us, the epilogue
+    // alone 90 (with a quarter of its arithmetic the whole takes 99, with MMAs
+    // of N = 16 instead of 256 it takes 100).  8 x 8 drafts over 128K entries:
+    // 57 us, 76 % of the copy bandwidth.  Not faster: two sets of warps on
+    // alternate tiles (126 us: a set's accumulator is released too late for the
+    // next MMAs), two issuing threads on alternate tiles, ReLUs on the FMA pipe,
+    // weights not from shared memory, suspended waits (no change).
     if constexpr (kTree) {
       const int quad = warp & 3, row = quad * 32 + lane;
       const int et = threadIdx.x - 64;
