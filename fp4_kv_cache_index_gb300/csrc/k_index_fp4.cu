@@ -674,8 +674,12 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       float* out[2] = {nullptr, nullptr};
       const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(j0 * 32);
       const float* w = wbuf + j0 * 32;
+      // A warp whose wait ran out takes no more M-groups but walks on through
+      // the tiles, so that it joins every barrier of a group change: the sets
+      // wait on different accumulators, and the other set may already stand
+      // at that barrier.
       bool ok = true;
-      for (int it = begin; it < end && ok; ++it) {
+      for (int it = begin; it < end; ++it) {
         gc.advance(p, it);
         const int g = gc.g;
         if (g != cur) {
@@ -703,8 +707,8 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
         live_groups(et0, nvis, mg_a, mg_b);
         const int n_units = mg_b - mg_a;
         for (; next < unit + n_units; next += 2) {
-          ok = mbar_wait_sleep(acc_full + acc, aph, p.err, wl);
-          if (!ok) break;
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_sleep(acc_full + acc, aph, p.err, wl));
+          if (!ok) continue;
           tc_fence_after();
           const int e0 = et0 + (mg_a + next - unit) * 128, e = e0 + 4 * lane + quad;
           const uint32_t ta = ta0 + (uint32_t)(acc * kBRows);
