@@ -674,22 +674,23 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       float* out[2] = {nullptr, nullptr};
       const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(j0 * 32);
       const float* w = wbuf + j0 * 32;
-      // A warp whose wait ran out takes no more M-groups but walks on through
-      // the tiles, so that it joins every barrier of a group change: the sets
-      // wait on different accumulators, and the other set may already stand
-      // at that barrier.
+      // a group's weights, by all epilogue warps between two barriers
+      auto weights = [&](int qg, int qe) {
+        esync();
+        for (int i = et; i < kBRows; i += kEpiThreads) {
+          const int q = qg + (i >> 5);
+          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+        }
+        esync();
+      };
+      int it = begin;
       bool ok = true;
-      for (int it = begin; it < end; ++it) {
+      for (; it < end && ok; ++it) {
         gc.advance(p, it);
         const int g = gc.g;
         if (g != cur) {
           const int qg = q_begin(g), qe = q_end(g);
-          esync();
-          for (int i = et; i < kBRows; i += kEpiThreads) {
-            const int q = qg + (i >> 5);
-            wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
-          }
-          esync();
+          weights(qg, qe);
           cur = g;
           ncom = p.n_com[g];
           nvis = p.nvis[g];
@@ -707,8 +708,8 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
         live_groups(et0, nvis, mg_a, mg_b);
         const int n_units = mg_b - mg_a;
         for (; next < unit + n_units; next += 2) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_sleep(acc_full + acc, aph, p.err, wl));
-          if (!ok) continue;
+          ok = mbar_wait_sleep(acc_full + acc, aph, p.err, wl);
+          if (!ok) break;
           tc_fence_after();
           const int e0 = et0 + (mg_a + next - unit) * 128, e = e0 + 4 * lane + quad;
           const uint32_t ta = ta0 + (uint32_t)(acc * kBRows);
@@ -759,6 +760,15 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
           if (acc >= nacc) { acc -= nacc; aph ^= 1; }
         }
         unit += n_units;
+      }
+      // A warp whose wait ran out takes no more M-groups but still joins the
+      // barriers of every group change: the sets wait on different
+      // accumulators, and the other one may already stand there.
+      for (; it < end; ++it) {
+        gc.advance(p, it);
+        if (gc.g == cur) continue;
+        cur = gc.g;
+        weights(q_begin(cur), q_end(cur));
       }
     }
   } else if (!kTree && warp >= 2 && warp < 10) {
