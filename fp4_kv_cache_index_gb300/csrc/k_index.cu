@@ -451,7 +451,16 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       float* out[2] = {nullptr, nullptr};
       uint64_t ents[2] = {0, 0};
       uint32_t ra[16], rb[16];
-      const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
+      // First column of this warp's queries in an accumulator.  Warps that have
+      // none (two drafts a tile: the third and fourth part) load columns of the
+      // last part instead and drop them: theirs would lie past the group's 32
+      // qpg columns, in the accumulator that the MMAs write or past the
+      // allocation.
+      const int col0 = min(j0, p.qpg - jq) * 32;
+      auto tm_load = [&](uint32_t ta, int col, uint32_t (&r)[16]) {
+        if (CSA2_IN_BOUNDS(col0 + col + 16 <= acc_cols, p.err)) tmem_ld16_issue(ta + col, r);
+      };
+      const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
       bool ready = false;            // ra holds, or is receiving, the tile's first half row
       for (int it = begin; it < end; ++it) {
         gc.advance(p, it);
@@ -492,23 +501,14 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
           out[jj][col] = s;
           if (use_hist) atomicAdd(hs + (j0 + jj) * kKeyHistBins + (score_key(s) >> 21), 1u);
         };
-        // A half row (16 heads) of this warp's query jj from accumulator a.  A
-        // warp without queries loads none: its columns would lie past the
-        // group's (two drafts a tile have 64 columns an accumulator and four
-        // parts of warps), in the accumulator that the MMAs write or past the
-        // allocation.  With mine > 0, j0 + jj < qpg and they are the group's.
-        auto load = [&](int a, int jj, int half, uint32_t (&r)[16]) {
-          const int col = (j0 + jj) * 32 + 16 * half;
-          if (CSA2_IN_BOUNDS(col + 16 <= acc_cols, p.err))
-            tmem_ld16_issue(lane_base + (uint32_t)(a * acc_cols + col), r);
-        };
+        const uint32_t ta = ta0 + (uint32_t)(acc * acc_cols);
         if (!ready) {
           if (!mbar_wait(acc_full + acc, aph, p.err, wl)) break;
           tc_fence_after();
-          if (mine > 0) load(acc, 0, 0, ra);
+          tm_load(ta, 0, ra);
         }
-        if (ready || mine > 0) tmem_ld16_wait(ra);
         ready = false;
+        tmem_ld16_wait(ra);
         // the accumulator is free once this warp's last columns are read;
         // the next tile's first half row is requested if its MMAs are done
         const int nacc_ = acc ^ 1;
@@ -517,30 +517,28 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(acc_empty + acc);
-        };
-        auto look_ahead = [&]() {
           if (it + 1 < end) {
             ready = __all_sync(0xffffffffu, mbar_try_wait(acc_full + nacc_, naph));
-            if (ready) {
-              tc_fence_after();
-              load(nacc_, 0, 0, ra);
-            }
+            if (ready) tc_fence_after();
           }
         };
-        if (mine == 0) release();
+        if (mine == 0) {
+          release();
+          if (ready) tm_load(ta0 + (uint32_t)(nacc_ * acc_cols), 0, ra);
+        }
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {
           if (jj >= mine) break;
           const float* w = wbuf + (j0 + jj) * 32;
           uint64_t a = 0, b = 0;
-          load(acc, jj, 1, rb);
+          tm_load(ta, 32 * jj + 16, rb);
           relu_dot_chains(w, ra, 16, a, b);
           tmem_ld16_wait(rb);
           if (jj + 1 < mine) {
-            load(acc, jj + 1, 0, ra);
+            tm_load(ta, 32 * (jj + 1), ra);
           } else {
             release();
-            look_ahead();
+            if (ready) tm_load(ta0 + (uint32_t)(nacc_ * acc_cols), 0, ra);
           }
           relu_dot_chains(w + 16, rb, 16, a, b);
           if (jj + 1 < mine) tmem_ld16_wait(ra);
@@ -718,7 +716,8 @@ cudaError_t launch_index(const IndexParams& p, const CUtensorMap& tm_k, const CU
 
 cudaError_t launch_index_tree(const TreeIndexParams& p, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_q, int grid, cudaStream_t s) {
-  if (p.qpg < 2 || p.qpg > kMaxQpg) return cudaErrorInvalidValue;
+  // widths that the epilogue's parts share out evenly
+  if (p.qpg != 2 && p.qpg != 4 && p.qpg != kMaxQpg) return cudaErrorInvalidValue;
   return launch_any(k_index<16, TreeIndexParams>, 16, p, tm_k, tm_q, grid, s);
 }
 
