@@ -788,13 +788,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // has not waited for its query rows, one that gave up perhaps not for its
   // window rows either: the copies must have landed before the outputs are
   // staged in the Q buffer and before the CTA exits.
-  if (tid == 0 && (n_tiles == 0 || !ok)) {
-    for (int h = 0; h < 2; ++h) {
-      mbar_wait(&sm.bar_q[h], 0, p.err, wl);
-      if (win_box) mbar_wait(&sm.bar_kv[h], 0, p.err, wl);
-    }
+  if ((n_tiles == 0 || !ok) && tid < 2) {
+    mbar_wait(&sm.bar_q[tid], 0, p.err, wl);
+    bool box = n_tiles > 0 && sm.my_list[0] < 0 && !ly.swa_codes;   // window rows by TMA
+    if constexpr (kTree) box = box && p.tq[q].win_n > 0;
+    if (box) mbar_wait(&sm.bar_kv[tid], 0, p.err, wl);
   }
-
   // l of each head: the partial sums reduced over all rows
   {
     const float sum = warp_reduce_scatter16<false>(lsum, lane);
