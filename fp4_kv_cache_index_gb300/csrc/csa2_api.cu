@@ -1649,8 +1649,10 @@ csa2_status_t csa2_index_topk_tree(const csa2_cache_t* c, const csa2_tree_t* tre
   float* scores = static_cast<float*>(workspace);
   uint32_t* hist = reinterpret_cast<uint32_t*>(scores + nq * ld);
   uint32_t* seg_ws = hist + nq * kKeyHistBinsHost;
-  // the histograms come from the bf16 indexer's epilogue
-  uint32_t* key_hist = mx ? nullptr : hist;
+  // the histograms come from the bf16 indexer's epilogue, or, for trees of one
+  // draft, from the decode indexer of either key format (the MXFP4 indexer's
+  // shared memory has room for one query's, not for a group's four)
+  uint32_t* key_hist = mx && plan.max_draft > 1 ? nullptr : hist;
   st = run_index_tree(c, tree, plan, q_idx, w, scores, ld, key_hist, stream);
   if (st != CSA2_OK) return st;
   TopkParams* tp = new (std::nothrow) TopkParams();
