@@ -211,7 +211,9 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint6
 // code of x / scale, nearest, ties to even, saturating) -> 16 code bytes in
 // the B slot's swizzled row and the scale byte in its atom.
 // kCvt: the codes by the hardware's conversion (the same rounding; without it
-// a comparison per grid point).
+// a comparison per grid point).  Both give a NaN the code of +6: a product
+// with a NaN is the one positive NaN of fp32 arithmetic here, so its sign is
+// gone before either sees it.
 template <bool kCvt>
 __device__ __forceinline__ void prep_query_block(const uint16_t* src, bool live, uint8_t* bcodes,
                                                  uint8_t* batom, int n, int b) {
