@@ -215,8 +215,11 @@ class Cache:
         if nbytes == 0:
             raise Csa2Error(1, "csa2_cache_bytes")
         device = torch.device("cuda") if device is None else torch.device(device)
-        self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        # the cache at a 256-byte boundary, and behind it 16 bytes: the token
+        # workspace of readouts that are given none
+        self.buffer = torch.empty(nbytes + 256 + 32, dtype=torch.uint8, device=device)
         self._off = (-self.buffer.data_ptr()) % 256
+        self._token = self.buffer.data_ptr() + self._off + (nbytes + 15) // 16 * 16
         self.handle = ctypes.c_void_p()
         _check(lib.csa2_cache_create(ctypes.byref(cfg), self.batch, caps,
                                      ctypes.c_void_p(self.buffer.data_ptr() + self._off),
@@ -918,8 +921,7 @@ def csa2_sparse_attn_tree_layers(cache: Cache, tree: Tree, qs: Sequence[torch.Te
             _shaped(outs[l], (nq, H, D), bf16, "out", dev),
             0 if lse is None else _shaped(lse, (nq, H), torch.float32, "lse", dev),
             0 if sink is None else _shaped(sink, (H,), torch.float32, "sink", dev), *f8))
-    # the two-CTA split only asks for a token workspace; its memory is not written
-    ws, nbytes = (topk_idx.data_ptr(), 16) if workspace is None else (
+    ws, nbytes = (cache._token, 16) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib.csa2_sparse_attn_tree(
         cache.handle, tree.ref, L, b"".join(layers), _i32_array(swa_len),
