@@ -713,12 +713,13 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
     if n > 8:
         raise ValueError("csa2_norm_rope: at most 8 tensors")
     if outs is None:
-        outs = [_empty(x.shape, x.dtype, x.device, stream) for x in xs]
+        outs = [None] * n
     one_pos, one_dim = isinstance(positions, torch.Tensor), isinstance(rope_dim, int)
     if (len(outs) != n or (weights is not None and len(weights) != n)
             or (norms is not None and len(norms) != n)
             or (not one_pos and len(positions) != n) or (not one_dim and len(rope_dim) != n)):
         raise ValueError("csa2_norm_rope: one entry per tensor expected")
+    outs = [_empty(x.shape, x.dtype, x.device, stream) if y is None else y for x, y in zip(xs, outs)]
     dev = torch.cuda.current_device()
     bf16, f32 = torch.bfloat16, torch.float32
     parts, pos, pos_at, n_pos = [], None, 0, -1
@@ -751,7 +752,7 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
                                      1 if norms is None or norms[i] else 0, xt == f32, yt == f32))
     _check(lib.csa2_norm_rope(n, b"".join(parts), eps, rope_base, _stream(stream, dev)),
            "csa2_norm_rope")
-    return list(outs)
+    return outs
 
 
 # ------------------------------------------------------------------ trees of drafted tokens
