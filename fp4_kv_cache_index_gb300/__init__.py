@@ -705,8 +705,9 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
 
     xs: bf16 or fp32 tensors [n, heads, dim] or [n, dim], channels contiguous
     (slices of a wider projection are taken as they are); positions: int64
-    [n], or one per tensor; weights: per tensor None or fp32 [dim]; outs: per
-    tensor the output, bf16 or fp32 (None: like x; x itself: in place);
+    [n], or one per tensor (None where nothing is rotated); weights: per tensor
+    None or fp32 [dim]; outs: per tensor the output, bf16 or fp32 (None: like
+    x; x itself: in place);
     norms: per tensor whether to norm (default: all); rope_dim: one number or
     one per tensor, 0 for no rotation.  Returns the outputs."""
     n = len(xs)
@@ -714,7 +715,8 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
         raise ValueError("csa2_norm_rope: at most 8 tensors")
     if outs is None:
         outs = [None] * n
-    one_pos, one_dim = isinstance(positions, torch.Tensor), isinstance(rope_dim, int)
+    one_pos = positions is None or isinstance(positions, torch.Tensor)
+    one_dim = isinstance(rope_dim, int)
     if (len(outs) != n or (weights is not None and len(weights) != n)
             or (norms is not None and len(norms) != n)
             or (not one_pos and len(positions) != n) or (not one_dim and len(rope_dim) != n)):
@@ -737,6 +739,8 @@ def csa2_norm_rope(xs: Sequence[torch.Tensor], positions, weights=None, outs=Non
         if r:
             p = positions if one_pos else positions[i]
             if p is not pos or tokens != n_pos:   # once for tensors that share them
+                if p is None:
+                    raise ValueError("csa2_norm_rope: positions expected where rope_dim is not 0")
                 pos, n_pos = p, tokens
                 pos_at = _shaped(p, (tokens,), torch.int64, "positions", dev)
         if weights is not None and weights[i] is not None:

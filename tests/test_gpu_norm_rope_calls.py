@@ -1,5 +1,5 @@
 """Calls of csa2_norm_rope that its documentation allows: single outputs left
-to the call."""
+to the call, and no positions where nothing is rotated."""
 import pytest
 import torch
 
@@ -28,3 +28,15 @@ def test_single_outputs_left_to_the_call():
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(other, alone))
 
+
+def test_no_positions_where_nothing_is_rotated():
+    import fp4_kv_cache_index_gb300 as C
+    x, z, pos = rand((7, 3, 256), seed=4), rand((7, 128), seed=5), positions(7)
+    y, = C.csa2_norm_rope([x], None, rope_dim=0)
+    check(y, x, None, None, 0)
+    a, b = C.csa2_norm_rope([x, z], [None, pos], rope_dim=[0, 64])
+    check(a, x, None, None, 0)
+    check(b, z, pos, None, 64)
+    for bad in (lambda: C.csa2_norm_rope([x], None), lambda: C.csa2_norm_rope([x, z], [pos, None])):
+        with pytest.raises(ValueError):
+            bad()
