@@ -1520,8 +1520,8 @@ csa2_status_t run_index_tree(const csa2_cache* c, const csa2_tree_t* t, const Tr
   }
   // queries that share a tile of keys
   const int qpg = mx ? 4 : plan.max_draft <= 2 ? 2 : plan.max_draft <= 4 ? 4 : 8;
-  // keys of a tile.  MXFP4: 512 (a stage's waits once in four M-groups: 4 x 29
-  // drafts over 128K 80 us, with 256 96), 256 when there would be fewer such
+  // keys of a tile.  MXFP4: 512 (a stage's waits once in four M-groups: 101
+  // drafts of 4 trees over 128K 80 us, with 256 96), 256 when there would be fewer such
   // tiles than SMs (29 drafts over 4096: 5.2 us, with 512 5.8)
   int64_t tiles512 = 0;
   for (int i = 0; mx && i < t->n_seqs; ++i) {

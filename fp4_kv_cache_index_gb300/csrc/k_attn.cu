@@ -37,8 +37,9 @@
 // zeros up to the tile's end) are written by the workers over what the box
 // brought there, so rows outside the window are never read by the MMAs.
 // Measured, 1024 drafts of 16 sequences x 64 heads x 640 candidates (86
-// GFLOP): 228 us, with FP8 windows 248 us.  What bounds it: one query has 64
-// heads, and an MMA of N = 64 takes 70-95 cycles, as long as one of N = 16 or
+// GFLOP): 228 us, with FP8 windows 248 us.  What bounds it: a CTA has 64
+// heads of one query (128 heads are two CTAs, which gather the same entries
+// each), and an MMA of N = 64 takes 70-95 cycles, as long as one of N = 16 or
 // 128 (its 128-row operand, 4 KB, is read at 64 bytes a cycle; a tile's 64
 // MMAs 5600 of its 8700 cycles); the softmax between S^T and O^T
 // (1350); and a quarter of a CTA's 27 us is its prologue and epilogue.

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     // 67 % of the measured bf16 rate; the MMAs alone take 84 us, the epilogue
     // alone 90 (with a quarter of its arithmetic the whole takes 99, with MMAs
     // of N = 16 instead of 256 it takes 100).  8 x 8 drafts over 128K entries:
-    // 57 us, 76 % of the copy bandwidth.  Not faster: two sets of warps on
+    // 57 us, 76 % of the copy bandwidth (as a graph; 62 us among other calls).  Not faster: two sets of warps on
     // alternate tiles (126 us: a set's accumulator is released too late for the
     // next MMAs), two issuing threads on alternate tiles, ReLUs on the FMA pipe,
     // weights not from shared memory, suspended waits (no change).

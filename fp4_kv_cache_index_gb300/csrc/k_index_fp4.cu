@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     // accumulator's phase must have seen the one before it: M-group u waits
     // on accumulator u % 3 after M-group u - 2 was taken, whose products
     // follow those of u - 3.  More sets than accumulators would misread the
-    // phase's parity.)  Measured, 4 x 29 drafts (104 in all, ragged) over
+    // phase's parity.)  Measured, 4 ragged trees of 101 drafts over
     // 128K entries, 13 million scores: 80 us; 163 us with 128-key tiles,
     // eight warps taking every tile and two warps preparing the first group's
     // queries; 99 us with each M-group of a tile tested for entries instead of

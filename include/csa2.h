@@ -642,9 +642,10 @@ csa2_status_t csa2_sparse_attn_prefill_layers(const csa2_cache_t* cache, int32_t
  *     of an output overlap (strides that make them are refused where one is
  *     below dim or both are equal).
  *   weight: nullable dev fp32 [dim];  pos: dev int64 [n_tokens] (may be NULL
- *     without rotation), any value;  dim: 64, 128, 256 or 512 (else
- *     CSA2_ERR_UNSUPPORTED);  rope_dim: 0 (no rotation) up to dim, a multiple
- *     of 8, at most 128.
+ *     without rotation), of either sign: an angle is off by up to |pos| *
+ *     2^-51 radians, the rounding of its frequency to 53 bits;
+ *   dim: 64, 128, 256 or 512 (else CSA2_ERR_UNSUPPORTED);  rope_dim: 0 (no
+ *     rotation) up to dim, a multiple of 8, at most 128.
  *   n_tokens * n_heads: at most 2^31 (else CSA2_ERR_UNSUPPORTED);
  *   eps: 1e-30 to 1;  rope_base: at least 1, or 0 for 10000.
  * A head that holds an infinity or a NaN gives what the formula gives.      */
