@@ -20,6 +20,13 @@
 // Emission writes, in increasing index order, every key > T and the first
 // (k - count above T) keys == T: ties go to the lower index.  Integer
 // atomics only, so the result is the same on every run.
+//
+// A score-key histogram may disagree with its row: an indexer whose wait ran
+// out leaves scores unwritten and counts missing.  The selection then means
+// nothing, but every access stays inside its buffer and the result holds
+// indices of the row and -1: a digit whose counts do not reach k selects bin
+// 0, the candidates are no more than were found, and what is emitted ends at
+// k and is padded up to it.
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
@@ -133,7 +140,7 @@ struct BinTest {
 
 // Bin holding the rem-th largest key counted in hist (nbins = 1024 or 2048,
 // a multiple of kT: thread t holds bins [nb t, nb t + nb)); records it and
-// the count strictly above it.
+// the count strictly above it (bin 0 if hist counts fewer than rem keys).
 template <int kT>
 __device__ __forceinline__ void select_bin(Shared<kT>& sh, int nbins, uint32_t rem) {
   constexpr int kMaxB = kBins / kT;
@@ -144,6 +151,7 @@ __device__ __forceinline__ void select_bin(Shared<kT>& sh, int nbins, uint32_t r
     h[j] = j < nb ? sh.hist[nb * t + j] : 0u;
     mine += h[j];
   }
+  if (t == 0) { sh.sel_bin = 0u; sh.sel_above = 0u; }
   const uint32_t suf = block_suffix_sum<kT>(mine, sh);   // bins >= nb t
   uint32_t above = suf - mine;                             // bins >= nb t + nb
 #pragma unroll
@@ -287,6 +295,7 @@ __global__ void __launch_bounds__(kSegThreads, 8) k_topk_seg(const __grid_consta
     if (lane + o < 32) suf += t;
   }
   if (lane == 0) sh.warp_sum[warp] = suf;
+  if (tid == 0) { sh.sel_bin = 0u; sh.sel_above = 0u; sh.sel_count = 0u; }   // too few counts
   __syncthreads();
   for (int w = warp + 1; w < kSegWarps; ++w) suf += sh.warp_sum[w];   // bins >= 8 tid
   const uint32_t k = (uint32_t)p.k;
@@ -302,7 +311,10 @@ __global__ void __launch_bounds__(kSegThreads, 8) k_topk_seg(const __grid_consta
   }
   __syncthreads();
   const uint32_t b1 = sh.sel_bin;
-  if (sh.sel_above + sh.sel_count > (uint32_t)kCandCap) return;  // the row falls back
+  if (sh.sel_above + sh.sel_count > (uint32_t)kCandCap) {   // the row falls back
+    if (tid == 0) out[0] = 0u;
+    return;
+  }
   // pass 1: which of the 32 scores are candidates
   const BinTest in_bins(b1);
   const int lim = (int)(n - e0 > kSegPer ? kSegPer : n - e0);   // e0 < n here or lim <= 0
@@ -377,6 +389,13 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
   }
   const bool vec = srow.aligned16();
   const int64_t chunk = (int64_t)kThreads * kPer;
+  // -1 behind gt keys above T and eq keys equal to it, of which need_eq count
+  auto pad = [&](uint32_t gt, uint32_t eq, uint32_t need_eq) {
+    for (uint32_t i = gt + (eq < need_eq ? eq : need_eq) + tid; i < (uint32_t)k; i += kThreads) {
+      orow[i] = -1;
+      if (osc) osc[i] = 0.0f;
+    }
+  };
 
   // ---- digit 1: keys [31:21]
   if (p.key_hist) {
@@ -406,7 +425,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
   select_bin<kT>(sh, kBins, (uint32_t)k);
   const uint32_t b1 = sh.sel_bin;
   uint32_t above = sh.sel_above;
-  const uint32_t n_cand = above + sh.hist[b1];
+  uint32_t n_cand = above + sh.hist[b1];
   __syncthreads();
 
   uint32_t T;
@@ -433,6 +452,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
       sh.u.cand.key[pos] = src[4 + i];
       sh.u.cand.idx[pos] = (int32_t)src[4 + kCandCap + i];
     }
+    if (tot < n_cand) n_cand = tot;   // the histogram counts more than the row holds
     __syncthreads();
   } else if (n_cand <= (uint32_t)kCandCap) {
     // ---- ordered compaction of every key in bins >= b1: two runs of kPer
@@ -486,6 +506,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
         }
       }
     }
+    if (base < n_cand) n_cand = base;   // the histogram counts more than the row holds
   }
   if (n_cand <= (uint32_t)kCandCap) {
     // ---- digit 2 (bits [20:10]) and digit 3 (bits [9:0]) on the candidates
@@ -527,7 +548,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
       const bool is_gt = key > T, is_eq = key == T;
       if (is_gt || (is_eq && q_before < need_eq)) {
         const uint32_t pos = g_before + (q_before < need_eq ? q_before : need_eq);
-        if (CSA2_IN_BOUNDS(pos >= 0 && pos < k, p.err)) {
+        if (pos < (uint32_t)k) {
           orow[pos] = sh.u.cand.idx[i];
           if (osc) osc[pos] = key_score(key);
         }
@@ -535,6 +556,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
       g_before += is_gt;
       q_before += is_eq;
     }
+    pad(tot & 0xFFFFu, tot >> 16, need_eq);
     return;
   }
 
@@ -600,7 +622,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
       const bool is_gt = key[i] > T, is_eq = key[i] == T;
       if (is_gt || (is_eq && q_before < need_eq)) {
         const uint32_t pos = g_before + (q_before < need_eq ? q_before : need_eq);
-        if (CSA2_IN_BOUNDS(pos >= 0 && pos < k && e + i < n, p.err)) {
+        if (pos < (uint32_t)k) {
           orow[pos] = (int32_t)(e + i);
           if (osc) osc[pos] = key_score(key[i]);
         }
@@ -612,6 +634,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) k_topk(const __grid_constant__ 
     base_eq += tot >> 16;
     if (base_gt + (base_eq < need_eq ? base_eq : need_eq) >= (uint32_t)k) break;
   }
+  pad(base_gt, base_eq, need_eq);
 }
 
 }  // namespace

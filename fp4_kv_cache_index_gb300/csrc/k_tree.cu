@@ -20,6 +20,10 @@ __global__ void __launch_bounds__(256) k_tree_map(const __grid_constant__ TreeMa
   for (int i = lane; i < p.k; i += 32) {
     const int32_t c = idx[i];
     if (c < n_com) continue;
+    if (c - n_com >= __popcll(ents)) {   // no column of the row
+      idx[i] = -1;
+      continue;
+    }
     // position of the (c - n_com)-th set bit
     uint64_t m = ents;
     for (int j = c - n_com; j > 0; --j) m &= m - 1;

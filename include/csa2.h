@@ -415,7 +415,8 @@ size_t csa2_topk_workspace_bytes(int32_t n_rows, int64_t max_valid);
  * allowed.
  *   scores: dev fp32;  n_valid: host int64 [n_rows];  key_hist: nullable
  *   dev uint32 [n_rows, 2048], the score-key histogram of each row if the
- *   caller has it (see above), which saves one pass over the scores;
+ *   caller has it (see above), which saves one pass over the scores (with
+ *   other counts the result is some indices of the row, or -1);
  *   idx_out: dev int32 [n_rows, k];  score_out: nullable dev fp32
  *   [n_rows, k].  k <= 4096.                                                */
 csa2_status_t csa2_topk(int32_t n_rows, const float* scores, int64_t ld,
