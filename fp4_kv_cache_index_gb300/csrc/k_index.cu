@@ -344,7 +344,16 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       blk_nxt[0] = pool_blk(begin + gsel, c0, row >> 3);
       blk_nxt[1] = pool_blk(begin + gsel, c0, 16 + (row >> 3));
     }
-    for (int it = begin + gsel; it < end; it += 2) {
+    // group g's weights, behind the flush of the group before
+    auto enter = [&](int g) {
+      if (use_hist && cur >= 0) flush(cur);
+      gsync();
+      if (et < 32) wg[et] = (g < p.nq) ? __ldg(p.w + (int64_t)g * kIdxHeads + et) : 0.0f;
+      gsync();
+      cur = g;
+    };
+    int it = begin + gsel;
+    for (; it < end; it += 2) {
       gc.advance(p, it);
       const int g = gc.g;
       const int32_t blk[2] = {blk_nxt[0], blk_nxt[1]};
@@ -353,11 +362,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
         blk_nxt[1] = pool_blk(it + 2, gc, 16 + (row >> 3));
       }
       if (g != cur) {
-        if (use_hist && cur >= 0) flush(cur);
-        gsync();
-        if (et < 32) wg[et] = (g < p.nq) ? __ldg(p.w + (int64_t)g * kIdxHeads + et) : 0.0f;
-        gsync();
-        cur = g;
+        enter(g);
         nvis = group_nvis_query(p, g, 0);
       }
       const int jt = it - begin;
@@ -405,6 +410,12 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
         mbar_arrive(acc_empty + a);
         store(0, relu_dot32(wg, r));
       }
+    }
+    // a warp whose wait ran out still joins every barrier: the others of its
+    // set may have got their tile at the last moment and go on
+    for (; it < end; it += 2) {
+      gc.advance(p, it);
+      if (gc.g != cur) enter(gc.g);
     }
     if (use_hist && cur >= 0) flush(cur);
   } else if (kTree && warp >= 2) {
@@ -462,19 +473,24 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       };
       const uint32_t ta0 = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)col0;
       bool ready = false;            // ra holds, or is receiving, the tile's first half row
-      for (int it = begin; it < end; ++it) {
+      // group g's weights, behind the flush of the group before
+      auto enter = [&](int g, int qg, int qe) {
+        if (use_hist && cur >= 0) flush(cur);
+        esync();
+        for (int i = et; i < qrows; i += kEpiThreads) {
+          const int q = qg + (i >> 5);
+          wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+        }
+        esync();
+        cur = g;
+      };
+      int it = begin;
+      for (; it < end; ++it) {
         gc.advance(p, it);
         const int g = gc.g;
         if (g != cur) {
-          if (use_hist && cur >= 0) flush(cur);
-          esync();
           const int qg = p.q_first[g], qe = p.q_first[g + 1];
-          for (int i = et; i < qrows; i += kEpiThreads) {
-            const int q = qg + (i >> 5);
-            wbuf[i] = (q < qe) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
-          }
-          esync();
-          cur = g;
+          enter(g, qg, qe);
           ncom = p.n_com[g];
           nvis = p.nvis[g];
           mine = max(0, min(jq, qe - qg - j0));
@@ -548,6 +564,12 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
         aph = naph;
       }
       if (ready) tmem_ld16_wait(ra);
+      // a warp whose wait ran out still joins every barrier: the others may
+      // have got their tile at the last moment and go on
+      for (; it < end; ++it) {
+        gc.advance(p, it);
+        if (gc.g != cur) enter(gc.g, p.q_first[gc.g], p.q_first[gc.g + 1]);
+      }
       if (use_hist && cur >= 0) flush(cur);
     }
   } else if (warp >= 2) {
@@ -582,20 +604,25 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     uint32_t aph = 0;
     int nvis[kMaxQ];   // visible entries of this thread's queries in the current group
     int32_t blk_nxt = (p.pool && begin < end) ? pool_blk(begin, c0, row >> 3) : -1;
-    for (int it = begin; it < end; ++it) {
+    // group g's weights, behind the flush of the group before
+    auto enter = [&](int g) {
+      if (use_hist && cur >= 0) flush(cur);
+      esync();
+      for (int i = et; i < qrows; i += kEpiThreads) {
+        const int q = g * p.qpg + (i >> 5);
+        wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+      }
+      esync();
+      cur = g;
+    };
+    int it = begin;
+    for (; it < end; ++it) {
       gc.advance(p, it);
       const int g = gc.g;
       const int32_t blk = blk_nxt;
       if (p.pool && it + 1 < end) blk_nxt = pool_blk(it + 1, gc, row >> 3);
       if (g != cur) {
-        if (use_hist && cur >= 0) flush(cur);
-        esync();
-        for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = g * p.qpg + (i >> 5);
-          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
-        }
-        esync();
-        cur = g;
+        enter(g);
 #pragma unroll
         for (int jj = 0; jj < kMaxQ; ++jj)
           nvis[jj] = (j0 + jj < j1) ? group_nvis_query(p, g, j0 + jj) : 0;
@@ -667,6 +694,12 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
         release();
       }
       if (++acc == 2) { acc = 0; aph ^= 1; }
+    }
+    // a warp whose wait ran out still joins every barrier: the others may have
+    // got their tile at the last moment and go on
+    for (; it < end; ++it) {
+      gc.advance(p, it);
+      if (gc.g != cur) enter(gc.g);
     }
     if (use_hist && cur >= 0) flush(cur);
   }

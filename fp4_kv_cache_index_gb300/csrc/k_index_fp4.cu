@@ -511,13 +511,14 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     Cursor gc = c0;
     int cur = -1, gi = 0;
     bool ok = true;
-    for (int it = begin; it < end && ok; ++it) {
+    int it = begin;
+    for (; it < end; ++it) {
       gc.advance(p, it);
       if (gc.g == cur) continue;
-      cur = gc.g;
       const int slot = gi & 1;
       ok = mbar_wait_sleep(b_empty + slot, (uint32_t)(((gi >> 1) & 1) ^ 1), p.err, wl);
       if (!ok) break;
+      cur = gc.g;
       // trees: the epilogue warps, idle until then, prepare the first group
       if (!kTree || gi > 0) {
         uint8_t* ba = bslots + slot * kBSlotBytes + kBRows * (kIdxDim / 2);
@@ -531,6 +532,16 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(b_full + slot);
       ++gi;
+    }
+    // two warps: one whose wait ran out still joins the barrier of this and
+    // every further group, where the other may go on to
+    if constexpr (kPrepWarps == 2) {
+      for (; it < end; ++it) {
+        gc.advance(p, it);
+        if (gc.g == cur) continue;
+        cur = gc.g;
+        asm volatile("bar.sync 2, 64;" ::: "memory");
+      }
     }
   } else if (warp == kSfWarp && lane == 0 && sf_warp && begin < end) {
     // ------------------------------------------------ scale copies
@@ -801,27 +812,32 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     int cur = -1, acc = 0, t_first = 0;
     uint32_t aph = 0;
     int nv[2] = {0, 0};   // visible entries of this thread's queries
-    for (int it = begin; it < end; ++it) {
+    // group g's weights and pool ids, behind the flush of the group before
+    auto enter = [&](int g) {
+      if (use_hist && cur >= 0) flush(cur);
+      esync();
+      for (int i = et; i < qrows; i += kEpiThreads) {
+        const int q = g * p.qpg + (i >> 5);
+        wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
+      }
+      if (pool) {
+        // the block ids of this CTA's tiles of the group, loaded once
+        t_first = (begin > gc.lo ? begin : gc.lo) - gc.lo;
+        const int t_last = (end < gc.hi ? end : gc.hi) - gc.lo;
+        const int i0 = t_first * blocks_per_tile;
+        const int i1 = min(t_last * blocks_per_tile, p.pool_blocks);
+        const int32_t* src = p.pool + (int64_t)g * p.pool_blocks;
+        for (int i = i0 + et; i < i1; i += kEpiThreads) ids_s[i - i0] = __ldg(src + i);
+      }
+      esync();
+      cur = g;
+    };
+    int it = begin;
+    for (; it < end; ++it) {
       gc.advance(p, it);
       const int g = gc.g;
       if (g != cur) {
-        if (use_hist && cur >= 0) flush(cur);
-        esync();
-        for (int i = et; i < qrows; i += kEpiThreads) {
-          const int q = g * p.qpg + (i >> 5);
-          wbuf[i] = (q < p.nq) ? __ldg(p.w + (int64_t)q * kIdxHeads + (i & 31)) : 0.0f;
-        }
-        if (pool) {
-          // the block ids of this CTA's tiles of the group, loaded once
-          t_first = (begin > gc.lo ? begin : gc.lo) - gc.lo;
-          const int t_last = (end < gc.hi ? end : gc.hi) - gc.lo;
-          const int i0 = t_first * blocks_per_tile;
-          const int i1 = min(t_last * blocks_per_tile, p.pool_blocks);
-          const int32_t* src = p.pool + (int64_t)g * p.pool_blocks;
-          for (int i = i0 + et; i < i1; i += kEpiThreads) ids_s[i - i0] = __ldg(src + i);
-        }
-        esync();
-        cur = g;
+        enter(g);
         if (p.qpg == 1) {
           nv[0] = group_nvis_query(p, g, 0);
         } else {
@@ -887,6 +903,12 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
         store(slot0, g * p.qpg + j + 1, nv[1], relu_dot32(wbuf + (j + 1) * 32, rb));
       }
       if (++acc == nacc) { acc = 0; aph ^= 1; }
+    }
+    // a warp whose wait ran out still joins every barrier: the others may have
+    // got their tile at the last moment and go on
+    for (; it < end; ++it) {
+      gc.advance(p, it);
+      if (gc.g != cur) enter(gc.g);
     }
     if (use_hist && cur >= 0) flush(cur);
   }
