@@ -40,6 +40,12 @@ constexpr long long kWaitCycles = 1ll << 31;
 __device__ __forceinline__ long long wait_limit(long long cycles) {
   return cycles > 0 ? cycles : kWaitCycles;
 }
+// Limit of a CTA's last waits, for copies and MMAs that it has in flight: at
+// least a millisecond, however short the launch's own limit is (they end by
+// themselves within microseconds, and must not outlive the CTA).
+__device__ __forceinline__ long long drain_limit(long long limit) {
+  return limit > (1ll << 21) ? limit : (1ll << 21);
+}
 
 // ---------------------------------------------------------------- smem / mbarrier
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -79,7 +79,7 @@ struct Small {
   int32_t n_tiles;
   float rope_c[32], rope_s[32];  // output RoPE(-i): cos, sin of each channel pair
   uint32_t tmem;
-  uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2], bar_fill[2];   // [h]: channel half h
+  uint64_t bar_q[2], bar_kv[2], bar_mma, bar_o[2], bar_fill[2], bar_end;   // [h]: channel half h
   // trees: source of each window row (>= 0 a committed row, <= -2 draft row
   // -2 - x, -1 none)
   int32_t win_src[kRows];
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.bar_fill[h], kThreads / 32 - 1);   // the filling warps
     }
     mbar_init(&sm.bar_mma, 1);
+    mbar_init(&sm.bar_end, 1);
     fence_barrier_init();
     for (int h = 0; h < 2; ++h) {
       mbar_arrive_expect_tx(&sm.bar_q[h], kHG * kHeadDim);
@@ -790,10 +791,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // window rows either: the copies must have landed before the outputs are
   // staged in the Q buffer and before the CTA exits.
   if ((n_tiles == 0 || !ok) && tid < 2) {
-    mbar_wait(&sm.bar_q[tid], 0, p.err, wl);
+    mbar_wait(&sm.bar_q[tid], 0, p.err, drain_limit(wl));
     bool box = n_tiles > 0 && sm.my_list[0] < 0 && !ly.swa_codes;   // window rows by TMA
     if constexpr (kTree) box = box && p.tq[q].win_n > 0;
-    if (box) mbar_wait(&sm.bar_kv[tid], 0, p.err, wl);
+    if (box) mbar_wait(&sm.bar_kv[tid], 0, p.err, drain_limit(wl));
+    if (tid == 0 && !ok) {   // and the MMAs that this thread has issued
+      umma_commit(&sm.bar_end);
+      mbar_wait(&sm.bar_end, 0, p.err, drain_limit(wl));
+    }
   }
   // l of each head: the partial sums reduced over all rows
   {

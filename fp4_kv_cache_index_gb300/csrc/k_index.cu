@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
     // make sure no bulk copy is still writing into this CTA's shared memory
     if (lane == 0) {
       for (int s = 0; s < n_stages; ++s)
-        if (armed & (1u << s)) mbar_wait(k_full + s, (armed_ph >> s) & 1u, p.err, wl);
-      if (cur >= 0) mbar_wait(q_full, qph ^ 1, p.err, wl);
+        if (armed & (1u << s)) mbar_wait(k_full + s, (armed_ph >> s) & 1u, p.err, drain_limit(wl));
+      if (cur >= 0) mbar_wait(q_full, qph ^ 1, p.err, drain_limit(wl));
     }
     __syncwarp();
   } else if (warp == 1 && lane == 0 && begin < end) {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(64 + 32 * kEpiW, 1)
       if (++acc == nacc) { acc = 0; aph ^= 1; }
     }
     umma_commit(drain);
-    mbar_wait(drain, 0, p.err, wl);
+    mbar_wait(drain, 0, p.err, drain_limit(wl));
   } else if (kEpiW == 8 && warp >= 2 && p.qpg == 1) {
     // ------------------------------------------------ epilogue, one query per tile
     // Two groups of four warps take alternate tiles (group gsel the tiles

@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
     // no bulk copy may still be writing into this CTA's shared memory
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s)
-        if (armed & (1u << s)) mbar_wait(k_full + s, (armed_ph >> s) & 1u, p.err, wl);
+        if (armed & (1u << s)) mbar_wait(k_full + s, (armed_ph >> s) & 1u, p.err, drain_limit(wl));
     }
     __syncwarp();
   } else if (warp >= R::kPrepWarp && warp < kSfWarp && begin < end) {
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       if (++stage == kStages) { stage = 0; ph ^= 1; }
     }
     umma_commit(sf_drain);
-    mbar_wait(sf_drain, 0, p.err, wl);
+    mbar_wait(sf_drain, 0, p.err, drain_limit(wl));
   } else if (warp == 1 && lane == 0 && begin < end) {
     // ------------------------------------------------ MMA issuer
     // Shared-memory descriptors built once; a tile's offsets go into the
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(Roles<P>::kThreads, 1)
       if (!kTree && ++acc == nacc) { acc = 0; aph ^= 1; }
     }
     umma_commit(drain);
-    mbar_wait(drain, 0, p.err, wl);
+    mbar_wait(drain, 0, p.err, drain_limit(wl));
   } else if (kTree && warp >= 2 && warp < R::kPrepWarp) {
     // ------------------------------------------------ epilogue, trees of drafts
     // Sixteen warps in two sets of eight, which take alternate M-groups, so

@@ -153,8 +153,10 @@ csa2_status_t csa2_cache_set_index_sms(csa2_cache_t* cache, int32_t n_sms);
  * indexer and readout kernels launched for this cache after the call
  * (cycles = 0 restores the default of 2^31, about one second).  A wait that
  * runs out records CSA2_ERR_TIMEOUT in the device error word, waits (within
- * the same bound) for the copies its CTA has in flight, frees its tensor
- * memory and ends the kernel, so the context stays usable.
+ * the same bound, or 2^21 cycles if that is more) for the copies and MMAs its
+ * CTA has in flight, frees its tensor memory and ends the kernel, so the
+ * context stays usable.  A selection behind it holds entries of its row or
+ * -1, not the top-k.
  * CSA2_ERR_INVALID_ARG for a NULL cache or cycles < 0.  The pages have no
  * counterpart: this is a watchdog of this implementation.                 */
 csa2_status_t csa2_cache_set_wait_limit(csa2_cache_t* cache, int64_t cycles);
