@@ -95,6 +95,29 @@ class NormPart(ctypes.Structure):
                                                "out_fp32")])
 
 
+class WindowStruct(ctypes.Structure):
+    """csa2_window_t."""
+    _fields_ = ([(f, ctypes.c_int32) for f in ("n_seqs", "swa", "n_first", "fp8")] +
+                [(f, ctypes.c_void_p) for f in ("rows", "codes", "rope", "scales", "pos", "error")])
+
+
+class WindowOpts(ctypes.Structure):
+    """csa2_window_opts_t."""
+    _fields_ = [("sink", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("rope_out", ctypes.c_int32),
+                ("rope_base", ctypes.c_double), ("error", ctypes.c_void_p)]
+
+
+class VerifyStruct(ctypes.Structure):
+    """csa2_verify_t."""
+    _fields_ = ([(f, ctypes.c_int32) for f in ("vocab", "fp32")] +
+                [(f, ctypes.c_void_p) for f in ("token", "target", "target_root", "draft",
+                                                "draft_root")] +
+                [("ld", ctypes.c_int64)] +
+                [(f, ctypes.c_void_p) for f in ("temperature", "uniform", "noise")] +
+                [("noise_ld", ctypes.c_int64)] +
+                [(f, ctypes.c_void_p) for f in ("accepted", "next_token")])
+
+
 _NORM_PART = struct.Struct("@4P5q6i")
 _TREE_LAYER = struct.Struct("@12P")
 assert _NORM_PART.size == ctypes.sizeof(NormPart)
@@ -161,6 +184,16 @@ def _load():
         "csa2_sparse_attn_tree": ([P, P, i32, P, P, P, ctypes.c_float, i32, ctypes.c_double, P,
                                    sz, P], i32),
         "csa2_cache_accept_tree": ([P, P, P, P], i32),
+        "csa2_window_reset": ([P, i32, P], i32),
+        "csa2_window_append": ([P, i32, P, P, P, P, P, P], i32),
+        "csa2_window_read": ([P, i32, P, P, i32, P, P, P, P, P, P], i32),
+        "csa2_window_attn_decode": ([P, i32, i32, P, P, P, ctypes.c_float, P, P, P], i32),
+        "csa2_window_attn_tree": ([P, P, i32, P, P, P, P, P, ctypes.c_float, P, P, P], i32),
+        "csa2_window_accept_tree": ([P, P, P, P, P, P, P, P], i32),
+        "csa2_window_attn_prefill": ([i32, i32, i64, P, P, i64, i64, i32, P, i32, ctypes.c_float, P,
+                                      P, P], i32),
+        "csa2_window_device_error": ([P, P, ctypes.POINTER(i32)], i32),
+        "csa2_verify_tree": ([P, P, P], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -942,3 +975,310 @@ def csa2_cache_accept_tree(cache: Cache, tree: Tree, accepted: Sequence[int], st
         raise ValueError("csa2_cache_accept_tree: one accepted draft (or -1) per tree expected")
     _check(lib.csa2_cache_accept_tree(cache.handle, tree.ref, _i32_array(accepted),
                                       _stream(stream)), "csa2_cache_accept_tree")
+
+
+# ------------------------------------------------------------------ window rows in a cache
+class Window:
+    """The newest `swa` rows of every sequence of one layer, and those of its
+    first n_first tokens, in torch-owned memory (csa2_window_t): in 8 bits, or
+    as bf16 (fp8=False).  `swa_kv` and `swa_fp8` are the rows as
+    csa2_sparse_attn_decode takes them, without a copy."""
+
+    def __init__(self, n_seqs: int, swa: int = 128, n_first: int = 0, fp8: bool = True, device=None,
+                 stream=None):
+        if n_seqs < 0 or not 1 <= swa <= 128 or not 0 <= n_first <= 8:
+            raise ValueError("Window: n_seqs of at least 0, swa of 1 to 128 and n_first of 0 to 8 "
+                             "expected")
+        self.n_seqs, self.swa, self.n_first, self.fp8 = n_seqs, swa, n_first, bool(fp8)
+        device = torch.device("cuda") if device is None else torch.device(device)
+        n = max(1, n_seqs * (swa + n_first))
+
+        def empty(shape, dtype):
+            return _empty(shape, dtype, device, stream)
+
+        self.rows = self.codes = self.rope = self.scales = None
+        if self.fp8:
+            self.codes, self.rope = empty((n, 448), torch.uint8), empty((n, 64), torch.bfloat16)
+            self.scales = empty((n, 8), torch.uint8)
+        else:
+            self.rows = empty((n, 512), torch.bfloat16)
+        self.pos = empty((n,), torch.int64)
+        self.error = empty((4,), torch.int32)
+        self.device = self.pos.get_device()
+
+        def at(t):
+            return None if t is None else t.data_ptr()
+
+        self.struct = WindowStruct(n_seqs, swa, n_first, int(self.fp8), at(self.rows),
+                                   at(self.codes), at(self.rope), at(self.scales), at(self.pos),
+                                   at(self.error))
+        self.ref = ctypes.byref(self.struct)
+        self.reset(stream=stream)
+
+    def _here(self, what: str) -> int:
+        """The current device, which has to be the cache's."""
+        dev = torch.cuda.current_device()
+        if dev != self.device:
+            raise ValueError(f"{what}: the cache is on device {self.device}, the current one is {dev}")
+        return dev
+
+    def reset(self, seq: Optional[int] = None, stream=None):
+        """Forgets the rows of sequence seq (None: of all)."""
+        dev = self._here("csa2_window_reset")
+        _check(lib.csa2_window_reset(self.ref, -1 if seq is None else seq, _stream(stream, dev)),
+               "csa2_window_reset")
+
+    @property
+    def swa_kv(self) -> Optional[torch.Tensor]:
+        """bf16 [n_seqs, swa, 512], the window rows (None in 8 bits)."""
+        if self.fp8:
+            return None
+        return self.rows[:self.n_seqs * self.swa].view(self.n_seqs, self.swa, 512)
+
+    @property
+    def swa_fp8(self):
+        """The window rows in 8 bits (codes, rope, scales); None as bf16."""
+        if not self.fp8:
+            return None
+        n = self.n_seqs * self.swa
+        return self.codes[:n], self.rope[:n], self.scales[:n]
+
+    def device_error(self, stream=None) -> int:
+        st = ctypes.c_int32()
+        dev = self._here("csa2_window_device_error")
+        _check(lib.csa2_window_device_error(self.ref, _stream(stream, dev), ctypes.byref(st)),
+               "csa2_window_device_error")
+        return st.value
+
+
+def _one_each(what: str, n: int, *lists):
+    for xs in lists:
+        if xs is not None and len(xs) != n:
+            raise ValueError(f"{what}: one entry per segment expected")
+
+
+def csa2_window_append(win: Window, rows: torch.Tensor, pos: torch.Tensor,
+                       n_rows: Optional[Sequence[int]] = None,
+                       seq_ids: Optional[Sequence[int]] = None,
+                       rounded: Optional[torch.Tensor] = None, stream=None):
+    """Writes rows at the end of sequences: rows bf16 [sum n_rows, 512], n_rows[i]
+    of them (default: one) for sequence seq_ids[i] (default: i, each at most
+    once) at positions pos[i], pos[i] + 1, ...; pos: int64 [segments], negative:
+    not stored.  rounded: bf16 like rows, the rows as the cache holds them."""
+    dev, n = win._here("csa2_window_append"), pos.numel()
+    _one_each("csa2_window_append", n, n_rows, seq_ids)
+    total = n if n_rows is None else sum(n_rows)
+    _check(lib.csa2_window_append(
+        win.ref, n, _i32_array(seq_ids), _i32_array(n_rows),
+        _shaped(pos, (n,), torch.int64, "pos", dev),
+        _shaped(rows, (total, 512), torch.bfloat16, "rows", dev),
+        None if rounded is None else _shaped(rounded, (total, 512), torch.bfloat16, "rounded", dev),
+        _stream(stream, dev)), "csa2_window_append")
+
+
+def csa2_window_read(win: Window, end: torch.Tensor, n_rows: Optional[int] = None,
+                     seq_ids: Optional[Sequence[int]] = None, out: Optional[torch.Tensor] = None,
+                     first: Optional[torch.Tensor] = None, fp8: bool = False, stream=None):
+    """The windows in position order, bf16 [segments, n_rows, 512]: row j of
+    segment i is that of position max(0, end[i] - n_rows) + j, zero where it is
+    not held or not below end[i].  end: int64 [segments]; n_rows: default swa;
+    first: bf16 [segments, n_first, 512], filled with the first tokens' rows;
+    fp8: the rows as they are held in 8 bits (codes, rope, scales) instead (out:
+    such a triple)."""
+    dev, n = win._here("csa2_window_read"), end.numel()
+    _one_each("csa2_window_read", n, seq_ids)
+    w = win.swa if n_rows is None else n_rows
+    where = end.device
+    o = [None] * 4
+    if fp8:
+        if out is None:
+            out = (_empty((n * w, 448), torch.uint8, where, stream),
+                   _empty((n * w, 64), torch.bfloat16, where, stream),
+                   _empty((n * w, 8), torch.uint8, where, stream))
+        o[1:] = [_shaped(t, (n * w, d), ty, "out", dev) for t, d, ty in
+                 zip(out, (448, 64, 8), (torch.uint8, torch.bfloat16, torch.uint8))]
+    else:
+        if out is None:
+            out = _empty((n, w, 512), torch.bfloat16, where, stream)
+        o[0] = _shaped(out, (n, w, 512), torch.bfloat16, "out", dev)
+    _check(lib.csa2_window_read(
+        win.ref, n, _i32_array(seq_ids), _shaped(end, (n,), torch.int64, "end", dev), w, *o,
+        None if first is None else _shaped(first, (n, win.n_first, 512), torch.bfloat16, "first",
+                                           dev),
+        _stream(stream, dev)), "csa2_window_read")
+    return out
+
+
+def _window_opts(what, nq, heads, lse, sink, rope_out, rope_base, dev, error=None):
+    if lse is None and sink is None and not rope_out and error is None:
+        return None
+    return ctypes.byref(WindowOpts(
+        None if sink is None else _shaped(sink, (heads,), torch.float32, "sink", dev),
+        None if lse is None else _shaped(lse, (nq, heads), torch.float32, "lse", dev),
+        1 if rope_out else 0, float(rope_base),
+        None if error is None else _shaped(error, error.shape, torch.int32, "error", dev)))
+
+
+def _window_queries(what: str, q: torch.Tensor, nq: int, out, stream, dev: int):
+    """(output, pointers of q and output)"""
+    if q.dim() != 3 or q.shape[1] not in (64, 128):
+        raise ValueError(f"{what}: q of shape [n_queries, 64 or 128, 512] expected")
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    shape = (nq, q.shape[1], 512)
+    return out, _shaped(q, shape, torch.bfloat16, "q", dev), _shaped(out, shape, torch.bfloat16,
+                                                                     "out", dev)
+
+
+def _draft_rows(win: Window, draft_kv, nq: int, dev: int):
+    """Pointers of drafts' rows in the cache's form: bf16, or a triple."""
+    if not win.fp8:
+        return _shaped(draft_kv, (nq, 512), torch.bfloat16, "draft_kv", dev), None, None, None
+    if not isinstance(draft_kv, (tuple, list)) or len(draft_kv) != 3:
+        raise ValueError("draft_kv: the triple of csa2_swa_fp8_quantise expected, as the cache is in "
+                         "8 bits")
+    return (None, *[_shaped(t, (nq, d), ty, "draft_kv", dev) for t, d, ty in
+                    zip(draft_kv, (448, 64, 8), (torch.uint8, torch.bfloat16, torch.uint8))])
+
+
+def csa2_window_attn_decode(win: Window, q: torch.Tensor, pos: torch.Tensor, scale: float,
+                            seq_ids: Optional[Sequence[int]] = None,
+                            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            sink: Optional[torch.Tensor] = None, rope_out: bool = False,
+                            rope_base: float = 0.0, stream=None) -> torch.Tensor:
+    """Attention of a window layer, one token a sequence: q bf16 [n_queries, 64
+    or 128, 512] at positions pos (int64 [n_queries]; negative: sees nothing)
+    of sequences seq_ids (default: 0, 1, ...) over the rows that the cache
+    holds, the query's own among them (csa2_window_append comes first).  lse,
+    sink and rope_out as for csa2_sparse_attn_decode."""
+    dev, nq = win._here("csa2_window_attn_decode"), q.shape[0]
+    _one_each("csa2_window_attn_decode", nq, seq_ids)
+    out, q_at, out_at = _window_queries("csa2_window_attn_decode", q, nq, out, stream, dev)
+    _check(lib.csa2_window_attn_decode(
+        win.ref, q.shape[1], nq, _i32_array(seq_ids), q_at,
+        _shaped(pos, (nq,), torch.int64, "pos", dev), scale, out_at,
+        _window_opts("csa2_window_attn_decode", nq, q.shape[1], lse, sink, rope_out, rope_base, dev),
+        _stream(stream, dev)), "csa2_window_attn_decode")
+    return out
+
+
+def csa2_window_attn_tree(win: Window, tree: Tree, q: torch.Tensor, draft_kv, scale: float,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          sink: Optional[torch.Tensor] = None, rope_out: bool = False,
+                          rope_base: float = 0.0, stream=None) -> torch.Tensor:
+    """The same for the drafts of a tree: q bf16 [n_queries, heads, 512];
+    draft_kv: the drafts' rows in the cache's form, bf16 [n_queries, 512] or
+    the triple of csa2_swa_fp8_quantise."""
+    dev, nq = win._here("csa2_window_attn_tree"), tree.n_queries
+    out, q_at, out_at = _window_queries("csa2_window_attn_tree", q, nq, out, stream, dev)
+    _check(lib.csa2_window_attn_tree(
+        win.ref, tree.ref, q.shape[1], q_at, *_draft_rows(win, draft_kv, nq, dev), scale, out_at,
+        _window_opts("csa2_window_attn_tree", nq, q.shape[1], lse, sink, rope_out, rope_base, dev),
+        _stream(stream, dev)), "csa2_window_attn_tree")
+    return out
+
+
+def csa2_window_accept_tree(win: Window, tree: Tree, draft_kv, accepted: torch.Tensor, stream=None):
+    """Writes the rows of each tree's accepted path (accepted: int32 [n_seqs]
+    on the device, as csa2_verify_tree gives it; -1: none)."""
+    dev = win._here("csa2_window_accept_tree")
+    _check(lib.csa2_window_accept_tree(
+        win.ref, tree.ref, _shaped(accepted, (tree.n_seqs,), torch.int32, "accepted", dev),
+        *_draft_rows(win, draft_kv, tree.n_queries, dev), _stream(stream, dev)),
+        "csa2_window_accept_tree")
+
+
+def csa2_window_attn_prefill(q: torch.Tensor, pos0: int, rows: torch.Tensor, rows_pos0: int,
+                             scale: float, swa: int = 128, n_first: int = 0,
+                             first: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None,
+                             sink: Optional[torch.Tensor] = None, rope_out: bool = False,
+                             rope_base: float = 0.0, error: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """The same for a chunk of one sequence: query i at position pos0 + i; row r
+    of rows (bf16 [n, 512]) is that of position rows_pos0 + r, the chunk's rows
+    and those before it (csa2_window_read); first: bf16 [n_first, 512], the
+    first tokens' rows where rows_pos0 is not 0; error: int32, the sticky error
+    word of the call (Window.error)."""
+    what, dev, nq = "csa2_window_attn_prefill", torch.cuda.current_device(), q.shape[0]
+    out, q_at, out_at = _window_queries(what, q, nq, out, stream, dev)
+    n = rows.shape[0]
+    _check(lib.csa2_window_attn_prefill(
+        q.shape[1], nq, pos0, q_at, _shaped(rows, (n, 512), torch.bfloat16, "rows", dev), rows_pos0,
+        n, swa, None if first is None else _shaped(first, (n_first, 512), torch.bfloat16, "first", dev),
+        n_first, scale, out_at,
+        _window_opts(what, nq, q.shape[1], lse, sink, rope_out, rope_base, dev, error),
+        _stream(stream, dev)), what)
+    return out
+
+
+# ------------------------------------------------------------------ verification of drafts
+def csa2_verify_tree(tree: Tree, tokens: torch.Tensor, logits: torch.Tensor,
+                     temperature: Optional[torch.Tensor] = None,
+                     uniform: Optional[torch.Tensor] = None, noise: Optional[torch.Tensor] = None,
+                     root_logits: Optional[torch.Tensor] = None,
+                     draft_logits: Optional[torch.Tensor] = None,
+                     draft_root: Optional[torch.Tensor] = None,
+                     accepted: Optional[torch.Tensor] = None,
+                     next_token: Optional[torch.Tensor] = None, stream=None):
+    """Which drafts are kept, by rejection sampling against the target's
+    probabilities, and the token that follows them: (accepted, next_token),
+    int32 [n_seqs] on the device; accepted is the last accepted draft of each
+    tree (-1: none), as csa2_window_accept_tree takes it (csa2_cache_accept_tree
+    wants it on the host).
+
+    tokens: int32 [n_queries], the drafts'; logits: bf16 or fp32 [n_queries,
+    vocab], the target's after each draft, root_logits [n_seqs, vocab] those
+    after the last committed token (None: the first draft of each tree is the
+    token that the step before has drawn, and is kept); draft_logits and
+    draft_root: likewise those of the model that drafted (None: drafts count as
+    certain); temperature: fp32 [n_seqs] (None: 0), 0 takes the largest logit;
+    uniform: fp32 [n_queries] in [0, 1); noise: fp32 [n_seqs, vocab],
+    exponential variates.  Rows may be further apart than vocab (the same for
+    all logits); rows at 16-byte boundaries are read faster."""
+    what, dev, nq, S = "csa2_verify_tree", torch.cuda.current_device(), tree.n_queries, tree.n_seqs
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what}: logits bf16 or fp32 [n_queries, vocab] expected")
+    vocab, dtype = logits.shape[1], logits.dtype
+    ld = None
+
+    def rows(t, n, ty, name):
+        if (t.dim() != 2 or t.shape != (n, vocab) or t.dtype != ty or t.get_device() != dev
+                or (vocab > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{name}: expected {ty} [{n}, {vocab}] on the current device, with the "
+                             f"values of a row next to each other")
+        return t.data_ptr()
+
+    def lrows(t, n, name):
+        nonlocal ld
+        if t is None:
+            return None
+        at = rows(t, n, dtype, name)
+        if n > 1:   # a single row has no distance to the next
+            if ld is not None and t.stride(0) != ld:
+                raise ValueError(f"{name}: the rows of all logits have to be equally far apart")
+            ld = t.stride(0)
+        return at
+
+    if accepted is None:
+        accepted = _empty((S,), torch.int32, logits.device, stream)
+    if next_token is None:
+        next_token = _empty((S,), torch.int32, logits.device, stream)
+    f32 = torch.float32
+    at = [lrows(logits, nq, "logits"), lrows(root_logits, S, "root_logits"),
+          lrows(draft_logits, nq, "draft_logits"), lrows(draft_root, S, "draft_root")]
+    noise_ld = 0
+    if noise is not None:
+        noise_at = rows(noise, S, f32, "noise")
+        noise_ld = noise.stride(0) if S > 1 else (vocab + 3) // 4 * 4
+    v = VerifyStruct(
+        vocab, int(dtype == f32), _shaped(tokens, (nq,), torch.int32, "tokens", dev), *at,
+        (vocab + 7) // 8 * 8 if ld is None else ld,
+        None if temperature is None else _shaped(temperature, (S,), f32, "temperature", dev),
+        None if uniform is None else _shaped(uniform, (nq,), f32, "uniform", dev),
+        None if noise is None else noise_at, noise_ld,
+        _shaped(accepted, (S,), torch.int32, "accepted", dev),
+        _shaped(next_token, (S,), torch.int32, "next_token", dev))
+    _check(lib.csa2_verify_tree(tree.ref, ctypes.byref(v), _stream(stream, dev)), what)
+    return accepted, next_token

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -1916,6 +1917,23 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
 
 }  // extern "C"
 
+namespace {
+// Reads and clears a sticky error word (synchronises the stream).
+csa2_status_t read_error_word(uint32_t* d_err, csa2_stream_t stream, int32_t* device_status) {
+  uint32_t word = 0;
+  if (cudaMemcpyAsync(&word, d_err, sizeof(word), cudaMemcpyDeviceToHost, S(stream)) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(S(stream)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  if (word && cudaMemsetAsync(d_err, 0, sizeof(uint32_t), S(stream)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  *device_status = (word & kErrTimeoutBit) ? CSA2_ERR_TIMEOUT
+                   : (word & kErrIndexBit) ? CSA2_ERR_DEVICE
+                                           : CSA2_OK;
+  return CSA2_OK;
+}
+}  // namespace
+
 extern "C" {
 
 csa2_status_t csa2_swa_fp8_quantise(int64_t n_rows, const void* rows, uint8_t* codes, void* rope,
@@ -1934,17 +1952,539 @@ csa2_status_t csa2_get_device_error(const csa2_cache_t* c, csa2_stream_t stream,
                                     int32_t* device_status) {
   CSA2_RANGE();
   if (!c || !device_status) return CSA2_ERR_INVALID_ARG;
-  uint32_t word = 0;
-  if (cudaMemcpyAsync(&word, c->d_err, sizeof(word), cudaMemcpyDeviceToHost, S(stream)) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(S(stream)) != cudaSuccess)
-    return CSA2_ERR_CUDA;
-  if (word && cudaMemsetAsync(c->d_err, 0, sizeof(uint32_t), S(stream)) != cudaSuccess)
-    return CSA2_ERR_CUDA;
-  *device_status = (word & kErrTimeoutBit) ? CSA2_ERR_TIMEOUT
-                   : (word & kErrIndexBit) ? CSA2_ERR_DEVICE
-                                           : CSA2_OK;
+  return read_error_word(c->d_err, stream, device_status);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- window rows in a cache
+namespace {
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// The arrays of a cache, checked.
+csa2_status_t window_rows(const csa2_window_t* w, WinRows* r) {
+  if (!w || w->n_seqs < 0 || w->swa < 1 || w->n_first < 0 || (w->fp8 != 0 && w->fp8 != 1))
+    return CSA2_ERR_INVALID_ARG;
+  if (w->swa > 128 || w->n_first > CSA2_MAX_FIRST ||
+      (int64_t)w->n_seqs * (w->swa + w->n_first) > (int64_t)1 << 31)
+    return CSA2_ERR_UNSUPPORTED;
+  std::memset(r, 0, sizeof(*r));
+  r->n_seqs = w->n_seqs;
+  r->swa = w->swa;
+  r->n_first = w->n_first;
+  r->fp8 = w->fp8;
+  r->pos = w->pos;
+  r->err = w->error;
+  if (w->fp8) {
+    r->codes = w->codes;
+    r->rope = static_cast<uint16_t*>(w->rope);
+    r->scales = w->scales;
+  } else {
+    r->rows = static_cast<uint16_t*>(w->rows);
+  }
+  if (w->n_seqs == 0) return CSA2_OK;
+  if (!w->pos || !aligned16(w->pos) || (reinterpret_cast<uintptr_t>(w->error) & 3u))
+    return CSA2_ERR_INVALID_ARG;
+  const bool ok = w->fp8 ? r->codes && r->rope && r->scales && aligned16(r->codes) &&
+                               aligned16(r->rope) && aligned8(r->scales)
+                         : r->rows && aligned16(r->rows);
+  return ok ? CSA2_OK : CSA2_ERR_INVALID_ARG;
+}
+
+// Sequences of a call's segments: in range, and (once) no two alike.
+csa2_status_t check_sequences(const csa2_window_t* w, int32_t n, const int32_t* ids, bool once) {
+  if (!ids) return n <= w->n_seqs ? CSA2_OK : CSA2_ERR_INVALID_ARG;
+  if (once && n > w->n_seqs) return CSA2_ERR_INVALID_ARG;
+  std::unique_ptr<uint8_t[]> seen;
+  if (once) {
+    seen.reset(new (std::nothrow) uint8_t[(size_t)w->n_seqs / 8 + 1]());
+    if (!seen) return CSA2_ERR_OOM;
+  }
+  for (int32_t i = 0; i < n; ++i) {
+    const int32_t s = ids[i];
+    if (s < 0 || s >= w->n_seqs) return CSA2_ERR_INVALID_ARG;
+    if (!once) continue;
+    if ((seen[s >> 3] >> (s & 7)) & 1u) return CSA2_ERR_INVALID_ARG;
+    seen[s >> 3] |= (uint8_t)(1u << (s & 7));
+  }
   return CSA2_OK;
+}
+
+// Rows of drafts in the cache's form.
+csa2_status_t draft_rows(const csa2_window_t* w, const void* kv, const uint8_t* codes,
+                         const void* rope, const uint8_t* scales, WinDrafts* d) {
+  *d = {};
+  if (w->fp8) {
+    if (!codes || !rope || !scales || !aligned16(codes) || !aligned16(rope) || !aligned8(scales))
+      return CSA2_ERR_INVALID_ARG;
+    d->codes = codes;
+    d->rope = static_cast<const uint16_t*>(rope);
+    d->scales = scales;
+  } else {
+    if (!kv || !aligned16(kv)) return CSA2_ERR_INVALID_ARG;
+    d->rows = static_cast<const uint16_t*>(kv);
+  }
+  return CSA2_OK;
+}
+WinDrafts drafts_from(WinDrafts d, int64_t row) {
+  if (d.rows) d.rows += row * kHeadDim;
+  if (d.codes) d.codes += row * 448;
+  if (d.rope) d.rope += row * 64;
+  if (d.scales) d.scales += row * 8;
+  return d;
+}
+
+// Checks a tree's own numbers; `w`: against the sequences of a cache, too.
+// *n_queries: its drafts; their paths into *paths.
+csa2_status_t check_tree(const csa2_tree_t* t, const csa2_window_t* w, int64_t* n_queries,
+                         std::unique_ptr<uint64_t[]>* paths) {
+  if (!t || t->n_seqs < 0) return CSA2_ERR_INVALID_ARG;
+  *n_queries = 0;
+  if (t->n_seqs == 0) return CSA2_OK;
+  if (!t->n_draft || (w && !t->pos0)) return CSA2_ERR_INVALID_ARG;
+  if (w) {
+    const csa2_status_t st = check_sequences(w, t->n_seqs, t->seq_ids, true);
+    if (st != CSA2_OK) return st;
+  }
+  for (int i = 0; i < t->n_seqs; ++i) {
+    if (t->n_draft[i] < 0) return CSA2_ERR_INVALID_ARG;
+    if (w && (t->pos0[i] < 0 || t->pos0[i] > INT64_MAX - CSA2_MAX_DRAFT))
+      return CSA2_ERR_INVALID_ARG;
+    if (t->n_draft[i] > CSA2_MAX_DRAFT) return CSA2_ERR_UNSUPPORTED;
+    *n_queries += t->n_draft[i];
+  }
+  if (*n_queries > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (*n_queries > 0 && !t->parent) return CSA2_ERR_INVALID_ARG;
+  if (paths) {
+    paths->reset(new (std::nothrow) uint64_t[(size_t)std::max<int64_t>(*n_queries, 1)]);
+    if (!*paths) return CSA2_ERR_OOM;
+  }
+  int64_t first = 0;
+  for (int i = 0; i < t->n_seqs; ++i) {
+    int32_t depth[CSA2_MAX_DRAFT];
+    uint64_t path[CSA2_MAX_DRAFT];
+    if (!tree_paths(t->n_draft[i], t->parent ? t->parent + first : nullptr, depth, path))
+      return CSA2_ERR_INVALID_ARG;
+    if (paths) std::copy(path, path + t->n_draft[i], paths->get() + first);
+    first += t->n_draft[i];
+  }
+  return CSA2_OK;
+}
+
+// What the three attention calls share.
+csa2_status_t window_attn_common(int32_t n_heads, float scale, const csa2_window_opts_t* o,
+                                 WinAttnCommon* p) {
+  if (!std::isfinite(scale)) return CSA2_ERR_INVALID_ARG;
+  if (n_heads != 64 && n_heads != 128) return CSA2_ERR_UNSUPPORTED;
+  p->n_heads = n_heads;
+  p->scale_log2 = scale * 1.4426950408889634f;
+  if (!o) return CSA2_OK;
+  if ((o->rope_out != 0 && o->rope_out != 1) || (o->sink && !aligned16(o->sink)) ||
+      (o->lse && !aligned16(o->lse)))
+    return CSA2_ERR_INVALID_ARG;
+  p->sink = o->sink;
+  p->lse = o->lse;
+  if (o->rope_out) {
+    if (!(o->rope_base == 0.0 || o->rope_base >= 1.0) || !std::isfinite(o->rope_base))
+      return CSA2_ERR_INVALID_ARG;
+    p->rope_out = 1;
+    const double base = o->rope_base > 0.0 ? o->rope_base : 10000.0;
+    for (int t = 0; t < 32; ++t)
+      p->turns[t] = (uint64_t)(std::pow(base, -t / 32.0) * 0.15915494309189535 * 18446744073709551616.0);
+  }
+  return CSA2_OK;
+}
+
+bool sm_count(int* n) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+// Queries and outputs [n * n_heads, 512] as 64-row boxes of 64 channels.
+bool window_maps(const void* q, const void* out, int64_t n, int32_t n_heads, CUtensorMap* mq,
+                 CUtensorMap* mo) {
+  return make_map(mq, q, (uint64_t)n * n_heads, kHeadDim, 64, 64) &&
+         make_map(mo, out, (uint64_t)n * n_heads, kHeadDim, 64, 64);
+}
+
+constexpr int32_t kWinRowLimit = INT32_MAX / 128;   // queries: rows of a map count in int32
+
+}  // namespace
+
+extern "C" {
+
+csa2_status_t csa2_window_reset(const csa2_window_t* w, int32_t seq, csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  const csa2_status_t st = window_rows(w, &r);
+  if (st != CSA2_OK) return st;
+  if (seq < -1 || seq >= w->n_seqs) return CSA2_ERR_INVALID_ARG;
+  const size_t W = (size_t)w->swa, F = (size_t)w->n_first, n = (size_t)w->n_seqs;
+  cudaError_t e = cudaSuccess;
+  if (seq < 0) {
+    if (n) e = cudaMemsetAsync(r.pos, 0xFF, n * (W + F) * 8, S(stream));
+    if (e == cudaSuccess && r.err) e = cudaMemsetAsync(r.err, 0, sizeof(uint32_t), S(stream));
+  } else {
+    e = cudaMemsetAsync(r.pos + seq * W, 0xFF, W * 8, S(stream));
+    if (e == cudaSuccess && F)
+      e = cudaMemsetAsync(r.pos + n * W + seq * F, 0xFF, F * 8, S(stream));
+  }
+  return cuda_status(e);
+}
+
+csa2_status_t csa2_window_append(const csa2_window_t* w, int32_t n_segs, const int32_t* seq_ids,
+                                 const int32_t* n_rows, const int64_t* pos0, const void* rows,
+                                 void* rounded, csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  csa2_status_t st = window_rows(w, &r);
+  if (st != CSA2_OK) return st;
+  if (n_segs < 0) return CSA2_ERR_INVALID_ARG;
+  st = check_sequences(w, n_segs, seq_ids, true);
+  if (st != CSA2_OK) return st;
+  int64_t total = n_rows ? 0 : n_segs;
+  for (int32_t i = 0; n_rows && i < n_segs; ++i) {
+    if (n_rows[i] < 0) return CSA2_ERR_INVALID_ARG;
+    total += n_rows[i];
+  }
+  if (total > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (total == 0) return CSA2_OK;
+  if (!pos0 || !rows || !aligned8(pos0) || !aligned16(rows) || (rounded && !aligned16(rounded)))
+    return CSA2_ERR_INVALID_ARG;
+  WinAppendParams* p = new (std::nothrow) WinAppendParams();
+  if (!p) return CSA2_ERR_OOM;
+  p->w = r;
+  p->identity = !seq_ids && !n_rows;
+  int64_t row = 0;
+  for (int32_t i = 0; i < n_segs && st == CSA2_OK;) {
+    const int32_t n = p->identity ? n_segs : std::min(kWinSegs, n_segs - i);
+    p->pos0 = pos0 + i;
+    p->rows = static_cast<const uint16_t*>(rows) + row * kHeadDim;
+    p->rounded = rounded ? static_cast<uint16_t*>(rounded) + row * kHeadDim : nullptr;
+    p->n_segs = n;
+    p->seq0 = i;
+    if (p->identity) {
+      p->n_rows = n;
+    } else {
+      p->first[0] = 0;
+      for (int32_t k = 0; k < n; ++k) {
+        p->first[k + 1] = p->first[k] + (n_rows ? n_rows[i + k] : 1);
+        p->seq[k] = seq_ids ? seq_ids[i + k] : i + k;
+      }
+      p->n_rows = p->first[n];
+    }
+    if (p->n_rows > 0) st = cuda_status(launch_window_append(*p, S(stream)));
+    row += p->n_rows;
+    i += n;
+  }
+  delete p;
+  return st;
+}
+
+csa2_status_t csa2_window_read(const csa2_window_t* w, int32_t n_segs, const int32_t* seq_ids,
+                               const int64_t* end, int32_t n_rows, void* out, uint8_t* codes,
+                               void* rope, uint8_t* scales, void* first, csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  csa2_status_t st = window_rows(w, &r);
+  if (st != CSA2_OK) return st;
+  if (n_segs < 0 || n_rows < 1 || n_rows > w->swa) return CSA2_ERR_INVALID_ARG;
+  st = check_sequences(w, n_segs, seq_ids, false);
+  if (st != CSA2_OK) return st;
+  const bool fp8 = codes || rope || scales;
+  if (fp8 && (out || !w->fp8 || !codes || !rope || !scales || !aligned16(codes) ||
+              !aligned16(rope) || !aligned8(scales)))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_segs == 0) return CSA2_OK;
+  if ((!fp8 && (!out || !aligned16(out))) || !end || !aligned8(end) || (first && !aligned16(first)))
+    return CSA2_ERR_INVALID_ARG;
+  WinReadParams* p = new (std::nothrow) WinReadParams();
+  if (!p) return CSA2_ERR_OOM;
+  p->w = r;
+  p->n_rows = n_rows;
+  p->identity = !seq_ids;
+  for (int32_t i = 0; i < n_segs && st == CSA2_OK;) {
+    const int32_t n = p->identity ? n_segs : std::min(2 * kWinSegs, n_segs - i);
+    const int64_t at = (int64_t)i * n_rows;
+    p->end = end + i;
+    p->out = out ? static_cast<uint16_t*>(out) + at * kHeadDim : nullptr;
+    p->codes = fp8 ? codes + at * 448 : nullptr;
+    p->rope = fp8 ? static_cast<uint16_t*>(rope) + at * 64 : nullptr;
+    p->scales = fp8 ? scales + at * 8 : nullptr;
+    p->first = first && w->n_first
+                   ? static_cast<uint16_t*>(first) + (int64_t)i * w->n_first * kHeadDim
+                   : nullptr;
+    p->n_segs = n;
+    p->seq0 = i;
+    if (seq_ids) std::copy(seq_ids + i, seq_ids + i + n, p->seq);
+    st = cuda_status(launch_window_read(*p, S(stream)));
+    i += n;
+  }
+  delete p;
+  return st;
+}
+
+csa2_status_t csa2_window_accept_tree(const csa2_window_t* w, const csa2_tree_t* t,
+                                      const int32_t* accepted, const void* draft_kv,
+                                      const uint8_t* draft_codes, const void* draft_rope,
+                                      const uint8_t* draft_scales, csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  csa2_status_t st = window_rows(w, &r);
+  int64_t nq = 0;
+  if (st == CSA2_OK) st = check_tree(t, w, &nq, nullptr);
+  if (st != CSA2_OK || nq == 0) return st;
+  WinDrafts d;
+  st = draft_rows(w, draft_kv, draft_codes, draft_rope, draft_scales, &d);
+  if (st != CSA2_OK) return st;
+  if (!accepted || (reinterpret_cast<uintptr_t>(accepted) & 3u)) return CSA2_ERR_INVALID_ARG;
+  WinAcceptParams* p = new (std::nothrow) WinAcceptParams();
+  if (!p) return CSA2_ERR_OOM;
+  int64_t row = 0;
+  for (int32_t i = 0; i < t->n_seqs && st == CSA2_OK;) {
+    p->w = r;
+    p->d = drafts_from(d, row);
+    p->accepted = accepted + i;
+    p->n_trees = 0;
+    p->first[0] = 0;
+    const int64_t row0 = row;
+    while (i < t->n_seqs && p->n_trees < kWinTrees &&
+           p->first[p->n_trees] + t->n_draft[i] <= kWinDrafts) {
+      const int k = p->n_trees++;
+      p->pos0[k] = t->pos0[i];
+      p->seq[k] = t->seq_ids ? t->seq_ids[i] : i;
+      p->first[k + 1] = p->first[k] + t->n_draft[i];
+      for (int j = 0; j < t->n_draft[i]; ++j)
+        p->parent[p->first[k] + j] = (int8_t)t->parent[row + j];
+      row += t->n_draft[i++];
+    }
+    if (row > row0) st = cuda_status(launch_window_accept(*p, S(stream)));
+  }
+  delete p;
+  return st;
+}
+
+csa2_status_t csa2_window_attn_decode(const csa2_window_t* w, int32_t n_heads, int32_t nq,
+                                      const int32_t* seq_ids, const void* q, const int64_t* pos,
+                                      float scale, void* out, const csa2_window_opts_t* opts,
+                                      csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  csa2_status_t st = window_rows(w, &r);
+  if (st != CSA2_OK) return st;
+  if (nq < 0) return CSA2_ERR_INVALID_ARG;
+  st = check_sequences(w, nq, seq_ids, false);
+  if (st != CSA2_OK) return st;
+  WinDecodeParams* p = new (std::nothrow) WinDecodeParams();
+  if (!p) return CSA2_ERR_OOM;
+  st = window_attn_common(n_heads, scale, opts, p);
+  if (st == CSA2_OK && nq > kWinRowLimit) st = CSA2_ERR_UNSUPPORTED;
+  if (st == CSA2_OK && nq > 0 &&
+      (!q || !out || !pos || !aligned16(q) || !aligned16(out) || !aligned8(pos) || q == out))
+    st = CSA2_ERR_INVALID_ARG;
+  int sms = 0;
+  if (st == CSA2_OK && nq > 0 && !sm_count(&sms)) st = CSA2_ERR_CUDA;
+  p->w = r;
+  p->err = r.err;
+  p->identity = !seq_ids;
+  float* const lse = p->lse;
+  for (int32_t i = 0; i < nq && st == CSA2_OK;) {
+    const int32_t n = p->identity ? nq : std::min(kWinQueries, nq - i);
+    const int64_t row = (int64_t)i * n_heads;
+    p->nq = n;
+    p->pos = pos + i;
+    p->seq0 = i;
+    if (seq_ids) std::copy(seq_ids + i, seq_ids + i + n, p->seq);
+    p->lse = lse ? lse + row : nullptr;
+    CUtensorMap mq, mo;
+    if (!window_maps(static_cast<const uint16_t*>(q) + row * kHeadDim,
+                     static_cast<uint16_t*>(out) + row * kHeadDim, n, n_heads, &mq, &mo) ||
+        launch_window_decode(*p, mq, mo, sms, S(stream)) != cudaSuccess)
+      st = CSA2_ERR_CUDA;
+    i += n;
+  }
+  delete p;
+  return st;
+}
+
+csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t, int32_t n_heads,
+                                    const void* q, const void* draft_kv,
+                                    const uint8_t* draft_codes, const void* draft_rope,
+                                    const uint8_t* draft_scales, float scale, void* out,
+                                    const csa2_window_opts_t* opts, csa2_stream_t stream) {
+  CSA2_RANGE();
+  WinRows r;
+  csa2_status_t st = window_rows(w, &r);
+  if (st != CSA2_OK) return st;
+  int64_t nq = 0;
+  std::unique_ptr<uint64_t[]> paths;
+  st = check_tree(t, w, &nq, &paths);
+  if (st != CSA2_OK) return st;
+  WinTreeParams* p = new (std::nothrow) WinTreeParams();
+  if (!p) return CSA2_ERR_OOM;
+  st = window_attn_common(n_heads, scale, opts, p);
+  if (st == CSA2_OK && nq > kWinRowLimit) st = CSA2_ERR_UNSUPPORTED;
+  WinDrafts d = {};
+  if (st == CSA2_OK && nq > 0) {
+    st = draft_rows(w, draft_kv, draft_codes, draft_rope, draft_scales, &d);
+    if (st == CSA2_OK && (!q || !out || !aligned16(q) || !aligned16(out) || q == out))
+      st = CSA2_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if (st == CSA2_OK && nq > 0 && !sm_count(&sms)) st = CSA2_ERR_CUDA;
+  p->w = r;
+  p->err = r.err;
+  float* const lse = p->lse;
+  int64_t row = 0;
+  for (int32_t i = 0; i < t->n_seqs && st == CSA2_OK;) {
+    // whole trees (of at most 64 drafts each) up to the tables' sizes
+    p->d = drafts_from(d, row);
+    p->nq = 0;
+    int k = 0;
+    const int64_t row0 = row;
+    for (; i < t->n_seqs && k < kWinTreeTrees && p->nq + t->n_draft[i] <= kWinTreeQueries; ++i, ++k) {
+      p->pos0[k] = t->pos0[i];
+      p->seq[k] = t->seq_ids ? t->seq_ids[i] : i;
+      p->first[k] = p->nq;
+      for (int j = 0; j < t->n_draft[i]; ++j) {
+        p->path[p->nq] = paths[(size_t)row + j];
+        p->tree[p->nq++] = (int16_t)k;
+      }
+      row += t->n_draft[i];
+    }
+    if (p->nq == 0) continue;
+    const int64_t at = row0 * n_heads;
+    p->lse = lse ? lse + at : nullptr;
+    CUtensorMap mq, mo;
+    if (!window_maps(static_cast<const uint16_t*>(q) + at * kHeadDim,
+                     static_cast<uint16_t*>(out) + at * kHeadDim, p->nq, n_heads, &mq, &mo) ||
+        launch_window_tree(*p, mq, mo, sms, S(stream)) != cudaSuccess)
+      st = CSA2_ERR_CUDA;
+  }
+  delete p;
+  return st;
+}
+
+csa2_status_t csa2_window_attn_prefill(int32_t n_heads, int32_t nq, int64_t pos0, const void* q,
+                                       const void* rows, int64_t rows_pos0, int64_t n_rows,
+                                       int32_t swa, const void* first, int32_t n_first, float scale,
+                                       void* out, const csa2_window_opts_t* opts,
+                                       csa2_stream_t stream) {
+  CSA2_RANGE();
+  if (nq < 0 || swa < 1 || n_first < 0 || pos0 < 0 || rows_pos0 < 0 || n_rows < 0)
+    return CSA2_ERR_INVALID_ARG;
+  if (swa > 128 || n_first > CSA2_MAX_FIRST) return CSA2_ERR_UNSUPPORTED;
+  WinPrefillParams p;
+  std::memset(&p, 0, sizeof(p));
+  const csa2_status_t st = window_attn_common(n_heads, scale, opts, &p);
+  if (st != CSA2_OK) return st;
+  if (nq == 0) return CSA2_OK;
+  if (nq > kWinRowLimit) return CSA2_ERR_UNSUPPORTED;
+  if (pos0 > INT64_MAX - nq || rows_pos0 > pos0 || n_rows > INT64_MAX - rows_pos0 ||
+      pos0 + nq > rows_pos0 + n_rows || !q || !rows || !out || !aligned16(q) || !aligned16(rows) ||
+      !aligned16(out) || q == out || (first && !aligned16(first)) ||
+      (n_first > 0 && rows_pos0 > 0 && !first))
+    return CSA2_ERR_INVALID_ARG;
+  p.w.swa = swa;
+  p.w.n_first = n_first;
+  p.out = static_cast<uint16_t*>(out);
+  p.err = opts ? opts->error : nullptr;
+  p.nq = nq;
+  p.band = static_cast<const uint16_t*>(rows);
+  p.first = static_cast<const uint16_t*>(first);
+  p.pos0 = pos0;
+  p.band0 = rows_pos0;
+  p.n_band = n_rows;
+  int sms = 0;
+  CUtensorMap mq, mo;
+  if (!sm_count(&sms) || !window_maps(q, out, nq, n_heads, &mq, &mo)) return CSA2_ERR_CUDA;
+  return cuda_status(launch_window_prefill(p, mq, mo, sms, S(stream)));
+}
+
+csa2_status_t csa2_window_device_error(const csa2_window_t* w, csa2_stream_t stream,
+                                       int32_t* device_status) {
+  CSA2_RANGE();
+  if (!w || !device_status || !w->error) return CSA2_ERR_INVALID_ARG;
+  return read_error_word(w->error, stream, device_status);
+}
+
+// ---------------------------------------------------------------- verification of drafts
+csa2_status_t csa2_verify_tree(const csa2_tree_t* t, const csa2_verify_t* v, csa2_stream_t stream) {
+  CSA2_RANGE();
+  int64_t nq = 0;
+  csa2_status_t st = check_tree(t, nullptr, &nq, nullptr);
+  if (st != CSA2_OK) return st;
+  if (!v || v->vocab < 1 || v->ld < v->vocab || (v->fp32 != 0 && v->fp32 != 1))
+    return CSA2_ERR_INVALID_ARG;
+  if (t->n_seqs == 0) return CSA2_OK;
+  const uintptr_t el = v->fp32 ? 3u : 1u;
+  auto off = [](const void* x, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(x) & mask) != 0; };
+  if (!v->accepted || !v->next_token || off(v->accepted, 3) || off(v->next_token, 3) ||
+      off(v->target, el) || off(v->target_root, el) || off(v->draft, el) || off(v->draft_root, el) ||
+      off(v->token, 3) || off(v->temperature, 3) || off(v->uniform, 3) || off(v->noise, 3))
+    return CSA2_ERR_INVALID_ARG;
+  if (nq > 0 && (!v->token || !v->target)) return CSA2_ERR_INVALID_ARG;
+  if (v->temperature && ((nq > 0 && !v->uniform) || !v->noise || v->noise_ld < v->vocab))
+    return CSA2_ERR_INVALID_ARG;
+  // draft logits for every node with children, or for none
+  if (v->draft_root ? !v->target_root || (nq > 0 && !v->draft)
+                    : v->draft != nullptr && v->target_root != nullptr)
+    return CSA2_ERR_INVALID_ARG;
+  if (!v->target_root) {   // one root child at most: the token drawn before
+    int64_t first = 0;
+    for (int i = 0; i < t->n_seqs; ++i) {
+      for (int j = 1; j < t->n_draft[i]; ++j)
+        if (t->parent[first + j] < 0) return CSA2_ERR_INVALID_ARG;
+      first += t->n_draft[i];
+    }
+  }
+  int sms = 0;
+  if (!sm_count(&sms)) return CSA2_ERR_CUDA;
+  VerifyParams* p = new (std::nothrow) VerifyParams();
+  if (!p) return CSA2_ERR_OOM;
+  // shares of the vocabulary: CTAs of a sequence's cluster, as many as leave
+  // no SM idle and have something to read
+  const int64_t bytes = v->fp32 ? 4 : 2;
+  int cluster = 1;
+  while (cluster < 8 && (int64_t)t->n_seqs * cluster * 2 <= sms && v->vocab >= 4096 * cluster * 2)
+    cluster *= 2;
+  auto aligned_rows = [&](const void* x) { return !x || (aligned16(x) && v->ld * bytes % 16 == 0); };
+  p->vec = aligned_rows(v->target) && aligned_rows(v->target_root) && aligned_rows(v->draft) &&
+           aligned_rows(v->draft_root) && (!v->noise || (aligned16(v->noise) && v->noise_ld % 4 == 0));
+  p->ld = v->ld;
+  p->noise_ld = v->noise_ld;
+  p->vocab = v->vocab;
+  int64_t row = 0;
+  auto rows_from = [&](const void* x, int64_t r) -> const void* {
+    return x ? static_cast<const uint8_t*>(x) + r * v->ld * bytes : nullptr;
+  };
+  for (int32_t i = 0; i < t->n_seqs && st == CSA2_OK;) {
+    p->token = v->token ? v->token + row : nullptr;
+    p->uniform = v->uniform ? v->uniform + row : nullptr;
+    p->target = rows_from(v->target, row);
+    p->draft = rows_from(v->draft, row);
+    p->root = rows_from(v->target_root, i);
+    p->draft_root = rows_from(v->draft_root, i);
+    p->temperature = v->temperature ? v->temperature + i : nullptr;
+    p->noise = v->noise ? v->noise + i * v->noise_ld : nullptr;
+    p->accepted = v->accepted + i;
+    p->next_token = v->next_token + i;
+    p->n_trees = 0;
+    p->first[0] = 0;
+    while (i < t->n_seqs && p->n_trees < kVerifyTrees &&
+           p->first[p->n_trees] + t->n_draft[i] <= kVerifyDrafts) {
+      const int k = p->n_trees++;
+      p->first[k + 1] = p->first[k] + t->n_draft[i];
+      for (int j = 0; j < t->n_draft[i]; ++j)
+        p->parent[p->first[k] + j] = (int8_t)t->parent[row + j];
+      row += t->n_draft[i++];
+    }
+    st = cuda_status(launch_verify(*p, v->fp32 != 0, cluster, S(stream)));
+  }
+  delete p;
+  return st;
 }
 
 }  // extern "C"

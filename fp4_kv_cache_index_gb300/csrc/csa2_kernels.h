@@ -330,4 +330,137 @@ cudaError_t launch_attn_tree(const TreeAttnParams& p, const AttnMaps& maps, cuda
 static_assert(sizeof(TreeIndexParams) + 2 * sizeof(CUtensorMap) < 32764, "kernel parameters");
 static_assert(sizeof(TreeAttnParams) + sizeof(AttnMaps) < 32764, "kernel parameters");
 
+// ---------------------------------------------------------------- window rows in a cache
+// Arrays of csa2_window_t.
+struct WinRows {
+  int32_t n_seqs, swa, n_first, fp8;
+  uint16_t* rows;
+  uint8_t* codes;
+  uint16_t* rope;
+  uint8_t* scales;
+  int64_t* pos;
+  uint32_t* err;
+};
+// Segments of one launch (tables of at most 32764 bytes of parameters).
+constexpr int kWinSegs = 2048;
+struct WinAppendParams {
+  WinRows w;
+  const uint16_t* rows;
+  uint16_t* rounded;
+  const int64_t* pos0;       // of the launch's first segment
+  int64_t n_rows;            // of the launch
+  int32_t n_segs;
+  int32_t identity;          // segment i is one row of sequence seq0 + i (no table)
+  int32_t seq0;
+  int32_t first[kWinSegs + 1];   // first row of each segment
+  int32_t seq[kWinSegs];
+};
+cudaError_t launch_window_append(const WinAppendParams& p, cudaStream_t s);
+struct WinReadParams {
+  WinRows w;
+  const int64_t* end;        // of the launch's first segment
+  uint16_t* out;
+  uint8_t* codes;
+  uint16_t* rope;
+  uint8_t* scales;
+  uint16_t* first;
+  int32_t n_rows;
+  int32_t n_segs;
+  int32_t identity;
+  int32_t seq0;
+  int32_t seq[2 * kWinSegs];
+};
+cudaError_t launch_window_read(const WinReadParams& p, cudaStream_t s);
+
+// Rows of drafts in the cache's form.
+struct WinDrafts {
+  const uint16_t* rows;
+  const uint8_t* codes;
+  const uint16_t* rope;
+  const uint8_t* scales;
+};
+constexpr int kWinTrees = 512;
+constexpr int kWinDrafts = 12288;
+struct WinAcceptParams {
+  WinRows w;
+  WinDrafts d;               // from the launch's first draft on
+  const int32_t* accepted;   // of the launch's first tree
+  int32_t n_trees;
+  int64_t pos0[kWinTrees];
+  int32_t seq[kWinTrees];
+  int32_t first[kWinTrees + 1];
+  int8_t parent[kWinDrafts];
+};
+cudaError_t launch_window_accept(const WinAcceptParams& p, cudaStream_t s);
+
+// Attention of window layers.
+struct WinAttnCommon {
+  WinRows w;                 // decode, trees; swa and n_first in a chunk, too
+  uint16_t* out;
+  float* lse;
+  const float* sink;
+  uint32_t* err;
+  int32_t n_heads;
+  int32_t nq;                // queries of the launch
+  float scale_log2;          // scale * log2(e)
+  int32_t rope_out;
+  uint64_t turns[32];        // 2^64 * base^(-2t/64) / (2 pi): the output rotation
+};
+constexpr int kWinQueries = 4096;
+struct WinDecodeParams : WinAttnCommon {
+  const int64_t* pos;        // of the launch's first query
+  int32_t identity;          // query i is of sequence seq0 + i
+  int32_t seq0;
+  int32_t seq[kWinQueries];
+};
+constexpr int kWinTreeQueries = 1792;
+constexpr int kWinTreeTrees = 512;
+struct WinTreeParams : WinAttnCommon {
+  WinDrafts d;               // from the first draft of the launch's first tree on
+  int64_t pos0[kWinTreeTrees];
+  int32_t seq[kWinTreeTrees];
+  int32_t first[kWinTreeTrees];       // a tree's first draft row
+  uint64_t path[kWinTreeQueries];     // a query's path, itself included
+  int16_t tree[kWinTreeQueries];
+};
+struct WinPrefillParams : WinAttnCommon {
+  const uint16_t* band;
+  const uint16_t* first;
+  int64_t pos0, band0, n_band;
+};
+cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q,
+                                 const CUtensorMap& out, int sms, cudaStream_t s);
+cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q,
+                               const CUtensorMap& out, int sms, cudaStream_t s);
+cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q,
+                                  const CUtensorMap& out, int sms, cudaStream_t s);
+static_assert(sizeof(WinAppendParams) < 32764 && sizeof(WinReadParams) < 32764 &&
+              sizeof(WinAcceptParams) < 32764, "kernel parameters");
+static_assert(sizeof(WinDecodeParams) + 3 * sizeof(CUtensorMap) < 32764 &&
+              sizeof(WinTreeParams) + 3 * sizeof(CUtensorMap) < 32764, "kernel parameters");
+
+// ---------------------------------------------------------------- verification of drafts
+constexpr int kVerifyTrees = 512;
+constexpr int kVerifyDrafts = 16384;
+struct VerifyParams {
+  const int32_t* token;      // of the launch's first draft
+  const void* target;
+  const void* root;
+  const void* draft;
+  const void* draft_root;
+  const float* temperature;
+  const float* uniform;
+  const float* noise;
+  int32_t* accepted;
+  int32_t* next_token;
+  int64_t ld, noise_ld;
+  int32_t vocab;
+  int32_t n_trees;
+  int32_t vec;               // rows start at 16-byte boundaries
+  int32_t first[kVerifyTrees + 1];
+  int8_t parent[kVerifyDrafts];
+};
+cudaError_t launch_verify(const VerifyParams& p, bool fp32, int cluster, cudaStream_t s);
+static_assert(sizeof(VerifyParams) < 32764, "kernel parameters");
+
 }  // namespace csa2

@@ -1,0 +1,265 @@
+// k_window.cu -- window rows in a cache: rounded as they are written, read
+// back in position order, and the rows of an accepted path of drafts.
+//
+// A row is 512 channels.  In 8 bits (the V4.1 report, section 2.4.4, keeps
+// the window's KV in FP8): channels 0-447 as E4M3 codes with one power of two
+// per 64 channels, the exponent of their largest magnitude minus 8; channels
+// 448-511 as they are.  A code is the nearest E4M3 number (ties to even,
+// saturating at 448) of x * 2^-e, a product that is exact; the row read back,
+// code * 2^e, is exact in bf16 (4 significant bits).
+//
+// Bound: memory traffic, and for a decode step the launch.  A warp holds a
+// row: lane l has the 16-byte chunks l and l + 32 of 8 channels, so that every
+// access is contiguous over the lanes; the 8 lanes of a 64-channel block find
+// its largest magnitude by three shuffles.  No row is written twice by a call
+// (its segments are of different sequences, and a row that a later row of its
+// segment replaces is not stored), so there is nothing to order.
+#include <cuda_fp16.h>
+
+#include "csa2_device.cuh"
+#include "csa2_kernels.h"
+
+namespace csa2 {
+namespace {
+
+constexpr int kWarps = 8;   // rows in flight of a block of the three kernels
+
+// Eight bf16 of a chunk -> eight E4M3 codes under the scale byte that the
+// block's eight lanes agree on.
+__device__ __forceinline__ uint2 encode_chunk(const uint4& v, uint32_t& byte) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float x[8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const uint32_t ex = (__float_as_uint(amax) >> 23) & 0xFFu;
+  byte = ex >= 8u ? ex - 8u : 0u;
+  // 2^(127 - byte), a normal number: byte is at most 247
+  const float inv = __uint_as_float((254u - byte) << 23);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv),
+                                              __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+__device__ __forceinline__ uint4 decode_chunk(const uint2& c, uint32_t byte) {
+  const float sc = ue8m0_value(byte);
+  const uint32_t w[2] = {c.x, c.y};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+    o[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Row of the cache that holds position x of a sequence in the ring, and among
+// the first tokens.
+__device__ __forceinline__ int64_t ring_row(const WinRows& w, int32_t seq, int64_t x) {
+  return (int64_t)seq * w.swa + x % w.swa;
+}
+__device__ __forceinline__ int64_t first_row(const WinRows& w, int32_t seq, int64_t x) {
+  return (int64_t)w.n_seqs * w.swa + (int64_t)seq * w.n_first + x;
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+    k_win_append(const __grid_constant__ WinAppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (r >= p.n_rows) return;
+  int32_t seg = (int32_t)r, in_seg = 0, left = 1, seq = p.seq0 + (int32_t)r;
+  if (!p.identity) {
+    // the last segment that starts at or before row r (empty ones share a
+    // start with the one behind them)
+    int32_t lo = 0, hi = p.n_segs;
+    while (hi - lo > 1) {
+      const int32_t mid = (lo + hi) >> 1;
+      if (p.first[mid] <= (int32_t)r) lo = mid;
+      else hi = mid;
+    }
+    seg = lo;
+    in_seg = (int32_t)r - p.first[lo];
+    left = p.first[lo + 1] - (int32_t)r;
+    seq = p.seq[lo];
+  }
+  griddep_wait();
+  const int64_t p0 = p.pos0[seg];
+  const int64_t x = p0 + in_seg;
+  const WinRows& w = p.w;
+  const bool ring = p0 >= 0 && left <= w.swa, first = p0 >= 0 && x < w.n_first;
+  if (!ring && !first && !p.rounded) return;
+  const uint4* src = reinterpret_cast<const uint4*>(p.rows + r * kHeadDim);
+  const uint4 a = src[lane], b = src[lane + 32];   // plain: `rounded` may be `rows`
+  uint32_t ba = 0, bb = 0;
+  uint2 ca, cb;
+  if (w.fp8) {
+    ca = encode_chunk(a, ba);
+    cb = encode_chunk(b, bb);   // lanes 24-31: not used
+  }
+  auto store = [&](int64_t row) {
+    if (w.fp8) {
+      uint2* c = reinterpret_cast<uint2*>(w.codes + row * 448);
+      c[lane] = ca;
+      if (lane < 24) c[lane + 32] = cb;
+      else reinterpret_cast<uint4*>(w.rope + row * 64)[lane - 24] = b;
+      uint8_t* s = w.scales + row * 8;
+      if ((lane & 7) == 0) {
+        s[lane >> 3] = (uint8_t)ba;
+        s[4 + (lane >> 3)] = lane < 24 ? (uint8_t)bb : (uint8_t)0;
+      }
+    } else {
+      uint4* d = reinterpret_cast<uint4*>(w.rows + row * kHeadDim);
+      d[lane] = a;
+      d[lane + 32] = b;
+    }
+    if (lane == 0) w.pos[row] = x;
+  };
+  if (ring) store(ring_row(w, seq, x));
+  if (first) store(first_row(w, seq, x));
+  if (p.rounded) {
+    uint4* d = reinterpret_cast<uint4*>(p.rounded + r * kHeadDim);
+    d[lane] = w.fp8 ? decode_chunk(ca, ba) : a;
+    d[lane + 32] = w.fp8 && lane < 24 ? decode_chunk(cb, bb) : b;
+  }
+}
+
+// A warp per row: n_rows window rows of a segment, then its first tokens.
+__global__ void __launch_bounds__(kWarps * 32)
+    k_win_read(const __grid_constant__ WinReadParams p) {
+  const int lane = threadIdx.x & 31;
+  const WinRows& w = p.w;
+  const uint32_t per = (uint32_t)(p.n_rows + (p.first ? w.n_first : 0));
+  const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (i >= (int64_t)p.n_segs * per) return;
+  const int32_t seg = (int32_t)(i / per), j = (int32_t)(i - (int64_t)seg * per);
+  const int32_t seq = p.identity ? p.seq0 + seg : p.seq[seg];
+  griddep_wait();
+  const int64_t end = p.end[seg];
+  const bool first = j >= p.n_rows;
+  const int64_t lo = end > p.n_rows ? end - p.n_rows : 0;
+  const int64_t x = first ? j - p.n_rows : lo + j;
+  const int64_t row = first ? first_row(w, seq, x) : ring_row(w, seq, x);
+  const bool held = x < end && w.pos[row] == x;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if (!first && p.codes) {
+    const int64_t at = (int64_t)seg * p.n_rows + j;
+    const uint2* c = reinterpret_cast<const uint2*>(w.codes + row * 448);
+    uint2* d = reinterpret_cast<uint2*>(p.codes + at * 448);
+    d[lane] = held ? __ldg(c + lane) : make_uint2(0u, 0u);
+    if (lane < 24) {
+      d[lane + 32] = held ? __ldg(c + lane + 32) : make_uint2(0u, 0u);
+    } else {
+      reinterpret_cast<uint4*>(p.rope + at * 64)[lane - 24] =
+          held ? __ldg(reinterpret_cast<const uint4*>(w.rope + row * 64) + lane - 24) : zero;
+    }
+    if (lane == 0)
+      *reinterpret_cast<uint2*>(p.scales + at * 8) =
+          held ? __ldg(reinterpret_cast<const uint2*>(w.scales + row * 8)) : make_uint2(0u, 0u);
+    return;
+  }
+  uint4 a = zero, b = zero;
+  if (held) {
+    if (w.fp8) {
+      const uint2* c = reinterpret_cast<const uint2*>(w.codes + row * 448);
+      const uint8_t* s = w.scales + row * 8;
+      a = decode_chunk(__ldg(c + lane), __ldg(s + (lane >> 3)));
+      b = lane < 24 ? decode_chunk(__ldg(c + lane + 32), __ldg(s + 4 + (lane >> 3)))
+                    : __ldg(reinterpret_cast<const uint4*>(w.rope + row * 64) + lane - 24);
+    } else {
+      const uint4* s = reinterpret_cast<const uint4*>(w.rows + row * kHeadDim);
+      a = __ldg(s + lane);
+      b = __ldg(s + lane + 32);
+    }
+  }
+  uint16_t* out = first ? p.first + ((int64_t)seg * w.n_first + x) * kHeadDim
+                        : p.out + ((int64_t)seg * p.n_rows + j) * kHeadDim;
+  uint4* d = reinterpret_cast<uint4*>(out);
+  d[lane] = a;
+  d[lane + 32] = b;
+}
+
+// A block per tree: the accepted path's rows, copied as they are.
+__global__ void __launch_bounds__(kWarps * 32)
+    k_win_accept(const __grid_constant__ WinAcceptParams p) {
+  const int tree = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const WinRows& w = p.w;
+  const int32_t first = p.first[tree], n = p.first[tree + 1] - first;
+  __shared__ int32_t path[64];   // the path's drafts, the accepted one first
+  __shared__ int32_t len_s;
+  griddep_wait();
+  if (threadIdx.x == 0) {
+    int32_t t = p.accepted[tree], len = 0;
+    if (t < 0 || t >= n) t = -1;
+    for (; t >= 0 && len < 64; t = p.parent[first + t]) path[len++] = t;
+    len_s = len;
+  }
+  __syncthreads();
+  const int32_t len = len_s;
+  for (int d = warp; d < len; d += kWarps) {
+    const int64_t x = p.pos0[tree] + d, src = first + path[len - 1 - d];
+    const bool ring = len - d <= w.swa, head = x < w.n_first;
+    auto copy = [&](int64_t row) {
+      if (w.fp8) {
+        const uint4* c = reinterpret_cast<const uint4*>(p.d.codes + src * 448);
+        if (lane < 28) reinterpret_cast<uint4*>(w.codes + row * 448)[lane] = __ldg(c + lane);
+        if (lane < 8)
+          reinterpret_cast<uint4*>(w.rope + row * 64)[lane] =
+              __ldg(reinterpret_cast<const uint4*>(p.d.rope + src * 64) + lane);
+        if (lane == 31)
+          *reinterpret_cast<uint2*>(w.scales + row * 8) =
+              __ldg(reinterpret_cast<const uint2*>(p.d.scales + src * 8));
+      } else {
+        const uint4* s = reinterpret_cast<const uint4*>(p.d.rows + src * kHeadDim);
+        uint4* o = reinterpret_cast<uint4*>(w.rows + row * kHeadDim);
+        o[lane] = __ldg(s + lane);
+        o[lane + 32] = __ldg(s + lane + 32);
+      }
+      if (lane == 0) w.pos[row] = x;
+    };
+    if (ring) copy(ring_row(w, p.seq[tree], x));
+    if (head) copy(first_row(w, p.seq[tree], x));
+  }
+}
+
+template <class P>
+cudaError_t launch_rows(void (*kernel)(const P), const P& p, int64_t blocks, cudaStream_t s) {
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_window_append(const WinAppendParams& p, cudaStream_t s) {
+  return launch_rows(k_win_append, p, (p.n_rows + kWarps - 1) / kWarps, s);
+}
+
+cudaError_t launch_window_read(const WinReadParams& p, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.n_segs * (p.n_rows + (p.first ? p.w.n_first : 0));
+  return launch_rows(k_win_read, p, (rows + kWarps - 1) / kWarps, s);
+}
+
+cudaError_t launch_window_accept(const WinAcceptParams& p, cudaStream_t s) {
+  return launch_rows(k_win_accept, p, p.n_trees, s);
+}
+
+}  // namespace csa2

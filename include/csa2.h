@@ -669,6 +669,140 @@ typedef struct {
 csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, float eps,
                              double rope_base, csa2_stream_t stream);
 
+/* ---- window rows held in a cache -----------------------------------------
+ * The newest `swa` rows of every sequence of one layer, in the caller's
+ * memory, as bf16 or in the FP8 form of csa2_swa_fp8_quantise ([V41 sec
+ * 2.4.4]), and the rows of its first n_first tokens, which stay visible to
+ * the window layers ([V41 sec 4.2.1]: the first layers see the window only).
+ * Row s * swa + p % swa holds position p of sequence s, row n_seqs * swa + s *
+ * n_first + p that of one of its first tokens (which is in the ring, too, as
+ * long as the window reaches it).  pos names the position that each row holds,
+ * -1 for none: a row that is not held is not seen, whatever lies in its place.
+ * The first n_seqs * swa rows are the window rows of csa2_sparse_attn_decode
+ * (swa_kv, or the FP8 arrays; any order will do there, with swa_len the rows
+ * held): no copy is needed.
+ *   swa: 1 .. 128;  n_first: 0 .. 8;  fp8: 0 or 1;  n_seqs * (swa + n_first)
+ *   rows, at most 2^31;  rows: dev bf16 [rows, 512], or codes: dev u8 [rows,
+ *   448], rope: dev bf16 [rows, 64] and scales: dev u8 [rows, 8] (the others
+ *   are ignored), 16-byte aligned (scales: 8);  pos: dev int64 [rows];
+ *   error: nullable dev word, the sticky error word of the calls that read
+ *   the cache (csa2_window_device_error).
+ * Everything that changes is in device memory: the calls may be captured into
+ * a graph and replayed (with other positions in the same memory).           */
+#define CSA2_MAX_FIRST 8
+typedef struct {
+  int32_t n_seqs;
+  int32_t swa;
+  int32_t n_first;
+  int32_t fp8;
+  void* rows;
+  uint8_t* codes;
+  void* rope;
+  uint8_t* scales;
+  int64_t* pos;
+  uint32_t* error;
+} csa2_window_t;
+
+/* Forgets the rows of sequence seq (-1: of all).  A new cache is reset first:
+ * that also clears the error word.                                          */
+csa2_status_t csa2_window_reset(const csa2_window_t* w, int32_t seq, csa2_stream_t stream);
+
+/* Writes rows at the end of sequences: n_rows[i] of them for sequence
+ * seq_ids[i], at positions pos0[i], pos0[i] + 1, ...  In 8 bits each is
+ * rounded as csa2_swa_fp8_quantise rounds it.  Only what the window still
+ * reaches is stored (the last swa rows of a segment and its first tokens);
+ * a segment whose pos0 is negative is not stored.
+ *   seq_ids: host [n_segs], each at most once, or NULL (segment i is sequence
+ *   i);  n_rows: host [n_segs], or NULL (one row each);  pos0: dev int64
+ *   [n_segs];  rows: dev bf16 [sum n_rows, 512], at most 2^31 - 1 rows;
+ *   rounded: nullable dev bf16 [sum n_rows, 512], all rows as the cache would
+ *   hold them (bf16 holds them exactly), as csa2_window_attn_prefill reads
+ *   them (may be `rows`).                                                   */
+csa2_status_t csa2_window_append(const csa2_window_t* w, int32_t n_segs, const int32_t* seq_ids,
+                                 const int32_t* n_rows, const int64_t* pos0, const void* rows,
+                                 void* rounded, csa2_stream_t stream);
+
+/* Reads windows back in position order: row j of segment i is that of
+ * position max(0, end[i] - n_rows) + j of sequence seq_ids[i] (the newest
+ * n_rows below position end[i], the last of them at row min(n_rows, end[i]) -
+ * 1), zero where that position is not held or not below end[i].  The rows
+ * before a chunk, and the committed rows of csa2_sparse_attn_tree.
+ *   seq_ids: host [n_segs] or NULL, a sequence any number of times;  end: dev
+ *   int64 [n_segs];  n_rows: 1 .. swa;  out: dev bf16 [n_segs, n_rows, 512];
+ *   or, of a cache in 8 bits, out NULL and the three arrays of the FP8 form;
+ *   first: nullable dev bf16 [n_segs, n_first, 512], the first tokens' rows
+ *   (those below end[i] that are held; zero otherwise).                     */
+csa2_status_t csa2_window_read(const csa2_window_t* w, int32_t n_segs, const int32_t* seq_ids,
+                               const int64_t* end, int32_t n_rows, void* out, uint8_t* codes,
+                               void* rope, uint8_t* scales, void* first, csa2_stream_t stream);
+
+/* Options of the window layers' attention (NULL: none): the sink logits, lse
+ * and output rotation of csa2_sparse_attn_decode_ex.  rope_base: at least 1,
+ * or 0 for 10000.                                                           */
+typedef struct {
+  const float* sink;   /* nullable dev fp32 [n_heads]             */
+  float* lse;          /* nullable dev fp32 [n_queries, n_heads]  */
+  int32_t rope_out;
+  double rope_base;
+  uint32_t* error;     /* nullable dev word (csa2_window_attn_prefill only:
+                        * the others use the cache's)             */
+} csa2_window_opts_t;
+
+/* Attention of a window layer: a query at position p sees the rows of the
+ * positions x <= p with p - x < swa or x < n_first that are held,
+ *   l_x = scale * q . kv_x,   out = sum_x softmax(l)_x kv_x.
+ * A query that sees none gives 0 (lse -inf, or the sink).  The probabilities
+ * are rounded to bf16, in the sum as in the product.
+ * One query of each of n_queries sequences; its own row is written first
+ * (csa2_window_append).
+ *   seq_ids: host [n_queries] or NULL (query i is of sequence i), a sequence
+ *   any number of times;  n_heads: 64 or 128;  q, out: dev bf16 [n_queries,
+ *   n_heads, 512], out not q;  pos: dev int64 [n_queries], negative: the
+ *   query sees nothing.                                                     */
+csa2_status_t csa2_window_attn_decode(const csa2_window_t* w, int32_t n_heads, int32_t n_queries,
+                                      const int32_t* seq_ids, const void* q, const int64_t* pos,
+                                      float scale, void* out, const csa2_window_opts_t* opts,
+                                      csa2_stream_t stream);
+
+typedef struct csa2_tree csa2_tree_t;
+
+/* The same for trees of drafted tokens (see below): a draft sees the held
+ * rows of positions below pos0 and those of its own path, as decoding the path
+ * token by token would.  The drafts' rows come in the cache's form: draft_kv
+ * dev bf16 [n_queries, 512], or the three FP8 arrays.                       */
+csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* tree,
+                                    int32_t n_heads, const void* q, const void* draft_kv,
+                                    const uint8_t* draft_codes, const void* draft_rope,
+                                    const uint8_t* draft_scales, float scale, void* out,
+                                    const csa2_window_opts_t* opts, csa2_stream_t stream);
+
+/* Writes the rows of the accepted path of each tree: accepted: dev int32
+ * [n_seqs] (csa2_verify_tree), -1 or out of range: none.  Rows as above.    */
+csa2_status_t csa2_window_accept_tree(const csa2_window_t* w, const csa2_tree_t* tree,
+                                      const int32_t* accepted, const void* draft_kv,
+                                      const uint8_t* draft_codes, const void* draft_rope,
+                                      const uint8_t* draft_scales, csa2_stream_t stream);
+
+/* The same for a chunk of one sequence: query i is at position pos0 + i.
+ * Row r of `rows` holds position rows_pos0 + r (rows_pos0 <= pos0 + 1, the
+ * chunk's last position among them): the rows before the chunk
+ * (csa2_window_read) and the chunk's (`rounded` of csa2_window_append).  Rows
+ * before rows_pos0 are not seen, but for first tokens: `first` holds them.
+ *   rows: dev bf16 [n_rows, 512];  first: dev bf16 [n_first, 512], or NULL
+ *   where rows_pos0 is 0 or n_first is 0 (a first token of the band is read
+ *   from there).
+ * A row that holds an infinity or a NaN makes the outputs of the queries that
+ * see it NaN, no other's.                                                   */
+csa2_status_t csa2_window_attn_prefill(int32_t n_heads, int32_t n_queries, int64_t pos0,
+                                       const void* q, const void* rows, int64_t rows_pos0,
+                                       int64_t n_rows, int32_t swa, const void* first,
+                                       int32_t n_first, float scale, void* out,
+                                       const csa2_window_opts_t* opts, csa2_stream_t stream);
+
+/* Reads and clears the cache's error word, as csa2_get_device_error does.   */
+csa2_status_t csa2_window_device_error(const csa2_window_t* w, csa2_stream_t stream,
+                                       int32_t* device_status);
+
 /* ---- trees of drafted tokens --------------------------------------------
  * Speculative decoding checks a tree of drafted tokens per sequence in one
  * step.  The pages decode with drafts ([V41], speculative decoding) but give
@@ -693,13 +827,13 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
  *   host [n_seqs], 0 .. CSA2_MAX_DRAFT;  pos0: host int64 [n_seqs];  parent:
  *   host [sum n_draft].                                                     */
 #define CSA2_MAX_DRAFT 64
-typedef struct {
+struct csa2_tree {
   int32_t n_seqs;
   const int32_t* seq_ids;
   const int32_t* n_draft;
   const int64_t* pos0;
   const int32_t* parent;
-} csa2_tree_t;
+};
 
 /* Depth of each draft of one tree and its path as a bit mask (bit t: draft t
  * is on it, itself included); host only.  depth, path: nullable host
@@ -767,6 +901,57 @@ csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t
                                     const int32_t* swa_len, const int32_t* topk_idx, float scale,
                                     int32_t rope_out, double rope_base, void* workspace,
                                     size_t workspace_bytes, csa2_stream_t stream);
+
+/* Decides which drafts of each tree are kept, and the token that follows them,
+ * by rejection sampling: the tokens that come out are distributed as the
+ * target's.  The walk starts at the tree's root (the last committed token).
+ * At a node, p = softmax(target / T) and, of the model that drafted, q =
+ * softmax(draft / T); its children are tested in call order, child c with
+ * token x against what is left of p, r = max(p - a q, 0) / b (a = 0, b = 1 at
+ * first): it is accepted if uniform[c] * q(x) < r(x), and the walk goes on from
+ * it; else a grows by b and b becomes sum max(p - a q, 0) (both stay as they
+ * are where that sum is 0).  Where no child is accepted, the next token is the
+ * one with the largest r / noise: drawn from r, if noise holds exponential
+ * variates.  Without draft logits each draft counts as certain (q is 1 at its
+ * token): rejected tokens leave r.  A sequence with T = 0 accepts the first
+ * child that is the target's first largest logit, and that is the next token.
+ * Equal values go to the lower token.  An infinitely negative logit is a
+ * probability of 0; a node whose row holds a NaN or an infinity of the other
+ * sign, or nothing but negative infinities, ends the walk with token -1.
+ *   vocab: 1 .. 2^31 - 1;  token: dev int32 [n_queries], the drafts' tokens
+ *   (one outside the vocabulary is never accepted, and removes nothing);
+ *   target, draft: dev [n_queries, vocab] bf16, or fp32 with fp32 = 1, row
+ *   t the logits after draft t, rows ld elements apart (at least vocab);
+ *   target_root, draft_root: the same for the roots, [n_seqs, vocab].  draft
+ *   and draft_root NULL: no draft logits.  target_root NULL (and draft_root
+ *   with it): the root's only child is taken without a test, as the token
+ *   that the step before has drawn (a tree with several roots is refused, an
+ *   empty one gives accepted -1 and token -1).  Rows of nodes that no walk
+ *   comes to, and draft rows of drafts without children, are not read.
+ *   temperature: nullable dev fp32 [n_seqs], 0 or more (NULL: all 0);
+ *   uniform: dev fp32 [n_queries] in [0, 1);  noise: dev fp32 [n_seqs, vocab],
+ *   positive, rows noise_ld apart (both may be NULL where temperature is);
+ *   accepted: dev int32 [n_seqs], the last accepted draft or -1;  next_token:
+ *   dev int32 [n_seqs].
+ * pos0 and seq_ids of the tree are not used.                                */
+typedef struct {
+  int32_t vocab;
+  int32_t fp32;
+  const int32_t* token;
+  const void* target;
+  const void* target_root;
+  const void* draft;
+  const void* draft_root;
+  int64_t ld;
+  const float* temperature;
+  const float* uniform;
+  const float* noise;
+  int64_t noise_ld;
+  int32_t* accepted;
+  int32_t* next_token;
+} csa2_verify_t;
+csa2_status_t csa2_verify_tree(const csa2_tree_t* tree, const csa2_verify_t* v,
+                               csa2_stream_t stream);
 
 /* Ends the step: of tree i the path of draft accepted[i] (-1: none) becomes
  * committed.  Its entries move up behind the committed ones, the other
