@@ -2418,6 +2418,7 @@ csa2_status_t csa2_verify_tree(const csa2_tree_t* t, const csa2_verify_t* v, csa
   if (st != CSA2_OK) return st;
   if (!v || v->vocab < 1 || v->ld < v->vocab || (v->fp32 != 0 && v->fp32 != 1))
     return CSA2_ERR_INVALID_ARG;
+  if (v->vocab > 1 << 30) return CSA2_ERR_UNSUPPORTED;
   if (t->n_seqs == 0) return CSA2_OK;
   const uintptr_t el = v->fp32 ? 3u : 1u;
   auto off = [](const void* x, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(x) & mask) != 0; };
@@ -2444,15 +2445,8 @@ csa2_status_t csa2_verify_tree(const csa2_tree_t* t, const csa2_verify_t* v, csa
   if (!sm_count(&sms)) return CSA2_ERR_CUDA;
   VerifyParams* p = new (std::nothrow) VerifyParams();
   if (!p) return CSA2_ERR_OOM;
-  // shares of the vocabulary: CTAs of a sequence's cluster, as many as leave
-  // no SM idle and have something to read
   const int64_t bytes = v->fp32 ? 4 : 2;
-  int cluster = 1;
-  while (cluster < 8 && (int64_t)t->n_seqs * cluster * 2 <= sms && v->vocab >= 4096 * cluster * 2)
-    cluster *= 2;
-  auto aligned_rows = [&](const void* x) { return !x || (aligned16(x) && v->ld * bytes % 16 == 0); };
-  p->vec = aligned_rows(v->target) && aligned_rows(v->target_root) && aligned_rows(v->draft) &&
-           aligned_rows(v->draft_root) && (!v->noise || (aligned16(v->noise) && v->noise_ld % 4 == 0));
+  const int cluster = verify_cluster(t->n_seqs, v->vocab, sms);
   p->ld = v->ld;
   p->noise_ld = v->noise_ld;
   p->vocab = v->vocab;

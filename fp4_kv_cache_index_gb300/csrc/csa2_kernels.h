@@ -456,10 +456,10 @@ struct VerifyParams {
   int64_t ld, noise_ld;
   int32_t vocab;
   int32_t n_trees;
-  int32_t vec;               // rows start at 16-byte boundaries
   int32_t first[kVerifyTrees + 1];
   int8_t parent[kVerifyDrafts];
 };
+int verify_cluster(int64_t n_trees, int32_t vocab, int sms);
 cudaError_t launch_verify(const VerifyParams& p, bool fp32, int cluster, cudaStream_t s);
 static_assert(sizeof(VerifyParams) < 32764, "kernel parameters");
 

@@ -18,491 +18,866 @@
 // cluster's first CTA and taken from its shared memory by all, so that all
 // come to the same barriers.
 //
-// fp32 on the rows (a sum of 100,000 terms in 4096 partial sums is good to
-// about 1e-7), 64 bits on the few numbers that a test compares.  The token: a
-// second candidate so near the best that the fp32 scores cannot tell them
-// apart is looked for, and if there is one all such are scored again in 64
-// bits.
+// Sums and tests in fp32 (64 bits take 64 times as long here).  A test whose two
+// sides are nearer to each other than fp32 can tell is made again, with its
+// node's sums, in 64 bits; likewise the token: if the second best score is that
+// near the best, all such candidates are scored again in 64 bits.  So the result
+// is the one of 64-bit arithmetic, whatever the order of the sums.
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 512;
+// Blocks of 256 threads, three of them an SM, and clusters of up to 8: a batch's
+// walks are of very different lengths, and with small shares the long ones have
+// more SMs left to them.
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlocks = 2;       // per SM
 constexpr int kMaxCluster = 8;
 
-// (value, index) of the best so far and the value of the second.
-struct Best {
-  float v, second;
-  int32_t i;
-};
-__device__ __forceinline__ void best_add(Best& b, float v, int32_t i) {
-  if (v > b.v || (v == b.v && (uint32_t)i < (uint32_t)b.i)) {
-    b.second = b.v;
-    b.v = v;
-    b.i = i;
-  } else if (v > b.second) {
-    b.second = v;
-  }
-}
-__device__ __forceinline__ Best best_merge(const Best& a, const Best& b) {
-  const bool first = a.v > b.v || (a.v == b.v && (uint32_t)a.i < (uint32_t)b.i);
-  Best r = first ? a : b;
-  r.second = fmaxf(r.second, first ? b.v : a.v);
-  return r;
+// What a pass gives: merged over a warp's lanes, then over all warps of the cluster.
+// `over(n, lane, scale)`: the merge of lanes 0 .. n - 1 (a power of two, the
+// others hold nothing), the same bits in each of them.
+__device__ __forceinline__ float lanes_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 // Largest logit m of a part of a row, and the sum of exp2((l - m) * scale).  The
 // difference of two logits is formed first: it is all but exact, and the
 // probabilities that count have small ones (l * scale - m * scale would round
-// at the logits' own size).
+// at the logits' own size).  A NaN or an infinity in the row leaves a NaN in z.
 struct Sum {
   float m, z;
+  __device__ __forceinline__ void raise(float to, float scale) {
+    const float d = m - to;
+    // (-inf) - (-inf): nothing in it.  (to is +inf: z is NaN already)
+    z *= d == d || z != z ? fast_exp2(d * scale) : 0.0f;
+    m = to;
+  }
 };
-__device__ __forceinline__ Sum sum_merge(const Sum& a, const Sum& b, float scale) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, 0.0f};
-  return {m, a.z * exp2f((a.m - m) * scale) + b.z * exp2f((b.m - m) * scale)};
-}
-
-struct Part {      // of a CTA, per pass
+struct Sums {
   Sum p, q;
-  float total;
-  uint32_t bad;
-  Best best;
-  double exact;
-  int32_t exact_i;
+  __device__ __forceinline__ void over(int n, int, float scale) {
+    p.raise(lanes_max(p.m), scale);   // lanes without a part hold -inf
+    q.raise(lanes_max(q.m), scale);
+    for (int o = n / 2; o > 0; o >>= 1) {
+      p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
+      q.z += __shfl_xor_sync(0xffffffffu, q.z, o);
+    }
+  }
+  // two parts of one lane
+  __device__ __forceinline__ void add(Sums b, float scale) {
+    const float mp = fmaxf(p.m, b.p.m), mq = fmaxf(q.m, b.q.m);
+    p.raise(mp, scale);
+    b.p.raise(mp, scale);
+    q.raise(mq, scale);
+    b.q.raise(mq, scale);
+    p.z += b.p.z;
+    q.z += b.q.z;
+  }
+  __device__ static Sums none() { return {{-INFINITY, 0.0f}, {-INFINITY, 0.0f}}; }
 };
+// (value, index) of the best so far, the lower index of equal values, and the
+// value of the second; bad: a NaN or an infinity was seen.
+struct Best {
+  float v, second;
+  int32_t i;
+  uint32_t bad;
+  __device__ __forceinline__ void add(const Best& b, float) {
+    const bool first = v > b.v || (v == b.v && (uint32_t)i < (uint32_t)b.i);
+    second = fmaxf(fmaxf(second, b.second), first ? b.v : v);
+    if (!first) {
+      v = b.v;
+      i = b.i;
+    }
+    bad |= b.bad;
+  }
+  __device__ __forceinline__ void over(int n, int, float scale) {
+    for (int o = n / 2; o > 0; o >>= 1)
+      add({__shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, second, o),
+           __shfl_xor_sync(0xffffffffu, i, o), __shfl_xor_sync(0xffffffffu, bad, o)},
+          scale);
+  }
+  __device__ static Best none() { return {-INFINITY, -INFINITY, -1, 0u}; }
+};
+template <class Real>
+struct Total {
+  Real t;
+  __device__ __forceinline__ void add(const Total& b, float) { t += b.t; }
+  __device__ __forceinline__ void over(int n, int, float) {
+    for (int o = n / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  __device__ static Total none() { return {Real(0)}; }
+};
+struct Sums64 {   // exp2 below the maxima that are known already
+  double p, q;
+  __device__ __forceinline__ void add(const Sums64& b, float) {
+    p += b.p;
+    q += b.q;
+  }
+  __device__ __forceinline__ void over(int n, int, float) {
+    for (int o = n / 2; o > 0; o >>= 1) {
+      p += __shfl_xor_sync(0xffffffffu, p, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
+  }
+  __device__ static Sums64 none() { return {0.0, 0.0}; }
+};
+struct Exact {   // a score in 64 bits
+  double v;
+  int32_t i, pad;
+  __device__ __forceinline__ void add(const Exact& b, float) {
+    if (b.v > v || (b.v == v && (uint32_t)b.i < (uint32_t)i)) *this = b;
+  }
+  __device__ __forceinline__ void over(int n, int, float scale) {
+    for (int o = n / 2; o > 0; o >>= 1)
+      add({__shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, i, o), 0}, scale);
+  }
+  __device__ static Exact none() { return {-1.0, -1, 0}; }
+};
+
+constexpr int kPartWords = 4;
+constexpr int kParts = kMaxCluster * kWarps;   // warps of a cluster
+static_assert(kParts <= 64, "two parts a lane");
 struct Kid {       // a child of the node
-  float lp, lq, u;
-  int32_t token;   // -1: outside the vocabulary
+  int32_t token;
+  float u, lp, lq;
+};
+// What a pass leads to: a sum over what is left is needed, the node's numbers in
+// 64 bits, a child is taken, the token is drawn here, or the walk ends without.
+enum Action { kSum, kExact, kGo, kToken, kEnd };
+// Where the tests of a node stand: what is left is max(p - a q, 0) / b.
+template <class Real>
+struct Tests {
+  Real a, a_prev, b;
+  uint64_t todo;             // children that are still to be tested
+  int32_t taken;
+  int32_t removed[2], n_removed;   // lane r: removed tokens r and r + 32
 };
 struct Smem {
-  Part part[2];        // by pass parity: read by the cluster
-  Kid kid[2][64];      // of the cluster's first CTA: read by the cluster
+  // written by the cluster's warps, by pass parity: their parts, and by the
+  // first CTA's the node's children
+  alignas(16) uint32_t part[2][kParts][kPartWords];
+  alignas(16) Kid kid[2][64];
   float temperature;
-  Part all;            // of the cluster
-  Part warp[kWarps];
-  uint64_t kids;       // the node's children
-  double pd[64], qd[64];
-  int32_t tok[64];
-  float u[64];
-  // decision of thread 0
-  double a, b, a_prev;
-  int32_t taken, n_removed;
-  int32_t removed[64];
+  int32_t removed[64];       // for the last pass
 };
 
-__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-// A struct of words at `local` in another CTA of the cluster.
+// 16 bytes or less to `local` of another CTA of the cluster.
 template <class T>
-__device__ __forceinline__ T ld_peer(const T* local, uint32_t rank) {
-  static_assert(sizeof(T) % 4 == 0, "words");
+__device__ __forceinline__ void st_peer(void* local, uint32_t rank, const T& v) {
   const uint32_t at = dsmem_addr(smem_u32(local), rank);
-  T v;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 4); ++k) w[k] = ld_dsmem_u32(at + 4 * k);
-  return v;
-}
-
-template <class T>
-__device__ __forceinline__ float value_at(const T* row, int64_t i) {
-  if constexpr (sizeof(T) == 2) return bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + i));
-  else return __ldg(reinterpret_cast<const float*>(row) + i);
-}
-
-// Eight values of a row.  vec: neighbours, the row at a 16-byte boundary;
-// else a warp's lanes read neighbours, eight rounds of them.
-template <class T>
-__device__ __forceinline__ void load8(const T* row, int64_t i, float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + i));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+  if constexpr (sizeof(T) == 16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(&v);
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y),
+                 "r"(w.z), "r"(w.w)
+                 : "memory");
+  } else if constexpr (sizeof(T) == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(&v);
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(w.x), "r"(w.y) : "memory");
   } else {
-    const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(row) + i);
-    const float4 a = __ldg(s), b = __ldg(s + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    static_assert(sizeof(T) == 4, "words");
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&v))
+                 : "memory");
   }
 }
 
-// The CTA's share of rows a, b (nullable) and c (nullable, fp32): f(n, i, x,
-// y, z) for eight elements at a time, element k at index i(k); those past the
-// end come as `fill`.
-template <class T, bool kVec, class F>
-__device__ __forceinline__ void for_rows(const T* a, const T* b, const float* c, int32_t vocab,
-                                         uint32_t rank, uint32_t ctas, float fill, F f) {
-  const int64_t nt = (int64_t)ctas * kThreads, me = (int64_t)rank * kThreads + threadIdx.x;
-  const int64_t n8 = ((int64_t)vocab + 7) / 8;
-  for (int64_t t = me; t < (kVec ? n8 : (n8 + nt - 1) / nt * nt); t += nt) {
-    // kVec: chunk t; else round t / nt of eight strided elements
-    const int64_t i0 = kVec ? 8 * t : (t - me) * 8 + me, step = kVec ? 1 : nt;
-    float x[8], y[8], z[8];
-    if (kVec && i0 + 8 <= vocab) {
-      load8<T>(a, i0, x);
-      if (b) load8<T>(b, i0, y);
-      if (c) load8<float>(reinterpret_cast<const float*>(c), i0, z);
-    } else {
+// A value's bits, asked for now and looked at later.
+template <class T>
+__device__ __forceinline__ uint32_t bits_now(const T* row, int32_t i) {
+  if constexpr (sizeof(T) == 2) return ldg_now_u16(row + i);
+  else return ldg_now_u32(row + i);
+}
+template <class T>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+  return sizeof(T) == 2 ? bf16_bits_to_float(bits) : __uint_as_float(bits);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x in 64 bits, good to 2e-11: the Taylor series of e^r, |r| <= ln 2 / 2, to
+// the ninth power (the next term is (ln 2 / 2)^10 / 10! = 7e-12).  The one of
+// the library takes three times as long, on a path of single threads.
+__device__ __forceinline__ double exp2_64(double x) {
+  if (!(x > -1000.0)) return x == x ? 0.0 : x;
+  const double n = rint(x), r = (x - n) * 0.693147180559945309;
+  double s = 1.0 / 362880;
+  s = fma(s, r, 1.0 / 40320);
+  s = fma(s, r, 1.0 / 5040);
+  s = fma(s, r, 1.0 / 720);
+  s = fma(s, r, 1.0 / 120);
+  s = fma(s, r, 1.0 / 24);
+  s = fma(s, r, 1.0 / 6);
+  s = fma(s, r, 0.5);
+  s = fma(s, r, 1.0);
+  s = fma(s, r, 1.0);
+  return s * __hiloint2double((int)(1023.0 + fmin(n, 1000.0)) << 20, 0);
+}
+
+// Eight neighbouring values of a row as they are in memory.
+template <class T>
+struct Eight {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int32_t i) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t i = i0 + k * step;
-        const bool in = i < vocab;
-        x[k] = in ? value_at(a, i) : fill;
-        if (b) y[k] = in ? value_at(b, i) : fill;
-        if (c) z[k] = in ? __ldg(c + i) : 1.0f;
+    for (int k = 0; k < (int)(sizeof(T) / 2); ++k) v[k] = ldg_now_v4(row + i + 16 / sizeof(T) * k);
+  }
+  __device__ __forceinline__ void fill(uint32_t w) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(T) / 2); ++k) v[k] = make_uint4(w, w, w, w);
+  }
+  // one by one, `fill` for those outside [0, n)
+  __device__ __forceinline__ void gather(const T* row, int32_t i, int32_t n, uint32_t fill) {
+    uint32_t w[2 * sizeof(T)];
+#pragma unroll
+    for (int k = 0; k < (int)(2 * sizeof(T)); ++k) {
+      if constexpr (sizeof(T) == 2) {
+        const int32_t a = i + 2 * k;
+        const uint32_t lo = a >= 0 && a < n ? (uint32_t)__ldg(row + a) : fill;
+        const uint32_t hi = a + 1 >= 0 && a + 1 < n ? (uint32_t)__ldg(row + a + 1) : fill;
+        w[k] = lo | (hi << 16);
+      } else {
+        w[k] = i + k >= 0 && i + k < n ? __float_as_uint(__ldg(row + i + k)) : fill;
       }
     }
-    f(i0, step, x, y, z);
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(T) / 2); ++k)
+      v[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+  __device__ __forceinline__ float at(int k) const {
+    const int j = k * (int)sizeof(T) / 4;
+    const uint4& q = v[j >> 2];
+    const uint32_t w = (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
+    if constexpr (sizeof(T) == 2) return __uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16);
+    else return __uint_as_float(w);
+  }
+  // the largest value (NaN left out)
+  __device__ __forceinline__ float max() const {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t m;
+      asm("{\n .reg .b32 a, b;\n max.bf16x2 a, %1, %2;\n max.bf16x2 b, %3, %4;\n"
+          " max.bf16x2 %0, a, b;\n}"
+          : "=r"(m) : "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w));
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    } else {
+      float m = at(0);
+#pragma unroll
+      for (int k = 1; k < 8; ++k) m = fmaxf(m, at(k));
+      return m;
+    }
+  }
+};
+
+// exp2((x - base) * scale) of two values.
+__device__ __forceinline__ float2 exps(float x, float y, uint64_t neg_base, uint64_t scale2) {
+  const float2 d = unpack2(mul2(add2(pack2(x, y), neg_base), scale2));
+  return make_float2(fast_exp2(d.x), fast_exp2(d.y));
+}
+
+// Chunks into a thread's sum.
+template <class T, int kN>
+__device__ __forceinline__ void add_chunks(Sum& s, const Eight<T> (&l)[kN], float scale,
+                                           uint64_t scale2) {
+  float m = l[0].max();
+#pragma unroll
+  for (int j = 1; j < kN; ++j) m = fmaxf(m, l[j].max());
+  if (m > s.m) {
+    s.z *= fast_exp2((s.m - m) * scale);
+    s.m = m;
+  }
+  const float base = s.m == -INFINITY ? 0.0f : s.m;
+  const uint64_t nb = pack2(-base, -base);
+  uint64_t z[2] = {0, 0};   // zeros
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float2 e = exps(l[j].at(k), l[j].at(k + 1), nb, scale2);
+      z[(k >> 1) & 1] = add2(z[(k >> 1) & 1], pack2(e.x, e.y));
+    }
+  const float2 z2 = unpack2(add2(z[0], z[1]));
+  s.z += z2.x + z2.y;
+}
+
+// Chunks of two rows that a thread has in flight.
+template <class T>
+constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+
+// The CTA's share of one or two rows of logits (and of the noise) in chunks of
+// eight elements, kUnroll of them at a time: f(i0, x, y, z), chunk k the elements
+// from i0[k] = 8 t - (elements by which the row misses a 16-byte boundary).  A
+// row's ends are read element by element, and so is all of a row that misses the
+// boundary by another amount than the first; elements outside the row come as
+// -inf (noise: 1).  The rows go to L2 ahead of the loads: a thread's loads are
+// in flight only between two batches.
+template <class T, int kUnroll, bool kNoise, class F>
+__device__ __forceinline__ void for_rows(const T* a, const T* b, const float* c, int32_t vocab,
+                                         uint32_t rank, uint32_t ctas, F f) {
+  constexpr uint32_t kFill = sizeof(T) == 2 ? 0xFF80u : 0xFF800000u;   // -inf
+  constexpr uint32_t kFill2 = sizeof(T) == 2 ? 0xFF80FF80u : kFill;
+  const int32_t nt = (int32_t)ctas * kThreads, me = (int32_t)rank * kThreads + (int32_t)threadIdx.x;
+  const int32_t shift = (int32_t)((reinterpret_cast<uintptr_t>(a) & 15u) / sizeof(T));
+  const bool two = b != nullptr;
+  const bool alike =
+      !two || ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15u) == 0;
+  const bool noise_alike =
+      kNoise && ((reinterpret_cast<uintptr_t>(c) - 4u * (uintptr_t)shift) & 15u) == 0;
+  const int32_t n8 = (vocab + shift + 7) / 8;
+  constexpr int kLine = 128 / (8 * (int)sizeof(T));   // chunks of a line
+  if (!kNoise && threadIdx.x % kLine == 0)
+    for (int32_t t = me + kUnroll * nt; t < n8; t += nt) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a + max(8 * t - shift, 0)));
+      if (two) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + max(8 * t - shift, 0)));
+    }
+#pragma unroll 1
+  for (int32_t t0 = me; t0 < n8; t0 += kUnroll * nt) {
+    Eight<T> x[kUnroll], y[kUnroll];
+    Eight<float> z[kNoise ? kUnroll : 1];
+    int32_t i0[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const int32_t i = i0[k] = 8 * (t0 + k * nt) - shift;
+      const bool inside = i >= 0 && i + 8 <= vocab;
+      if (inside) x[k].load(a, i);
+      else x[k].fill(kFill2);
+      if (inside && alike) y[k].load(two ? b : a, i);
+      else y[k].fill(kFill2);
+      if constexpr (kNoise) {
+        if (inside && noise_alike) z[k].load(c, i);
+        else z[k].fill(0x3F800000u);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const bool inside = i0[k] >= 0 && i0[k] + 8 <= vocab;
+      if (inside && alike && (!kNoise || noise_alike)) continue;
+      if (i0[k] >= vocab) continue;
+      if (!inside) x[k].gather(a, i0[k], vocab, kFill);
+      if (two && !(inside && alike)) y[k].gather(b, i0[k], vocab, kFill);
+      if constexpr (kNoise)
+        if (!(inside && noise_alike)) z[k].gather(c, i0[k], vocab, 0x3F800000u);
+    }
+    f(i0, x, y, z);
   }
 }
 
-template <class T, bool kVec>
-__global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ VerifyParams p,
-                                                     const int ctas) {
+// What is left of a token in 64 bits, over its noise; a leaf's relative to 2^base.
+__device__ __noinline__ double exact_score(bool leaf, float base, float temp, float l, const Sum& sp,
+                                           bool two, float d, const Sum& sq, double a, float e) {
+  const double c = 1.4426950408889634 / (double)temp;
+  if (leaf) return exp2((double)l * c - floor((double)base)) / (double)e;
+  double s = exp2(((double)l - (double)sp.m) * c) / (double)sp.z;
+  if (two) s = fmax(s - a * (exp2(((double)d - (double)sq.m) * c) / (double)sq.z), 0.0);
+  return s / (double)e;
+}
+
+// The passes over a node's rows, a function each so that each has its own
+// registers (inlined into one kernel they spilled).
+
+// Of the logits: maxima and sums.
+template <class T>
+__device__ __forceinline__ Sums pass_sums(const T* tr, const T* dr, int32_t V, uint32_t rank,
+                                          uint32_t ctas, float scale) {
+  const uint64_t scale2 = pack2(scale, scale);
+  Sums x = Sums::none();
+  for_rows<T, kRows<T>, false>(tr, dr, nullptr, V, rank, ctas,
+                               [&](auto&, auto& l, auto& d, auto&) {
+                                 add_chunks(x.p, l, scale, scale2);
+                                 if (dr) add_chunks(x.q, d, scale, scale2);
+                               });
+  return x;
+}
+
+// The first largest logit.
+template <class T>
+__device__ __noinline__ Best pass_largest(const T* tr, int32_t V, uint32_t rank, uint32_t ctas) {
+  Best x = Best::none();
+  for_rows<T, kRows<T>, false>(
+      tr, static_cast<const T*>(nullptr), nullptr, V, rank, ctas,
+      [&](auto& i0, auto& l, auto&, auto&) {
+#pragma unroll
+        for (int j = 0; j < kRows<T>; ++j)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float v = l[j].at(k);
+            if (!(v < INFINITY)) x.bad = 1u;
+            if (v > x.v) {   // a thread's indices go up
+              x.v = v;
+              x.i = i0[j] + k;
+            }
+          }
+      });
+  return x;
+}
+
+// What is left of p, sum max(p - a q, 0).
+template <class T>
+__device__ __noinline__ Total<float> pass_total(const T* tr, const T* dr, int32_t V, uint32_t rank,
+                                                uint32_t ctas, float scale, Sum sp, Sum sq, float a) {
+  Total<float> y = {0.0f};
+  const uint64_t bp = pack2(-sp.m, -sp.m), bq = pack2(-sq.m, -sq.m), scale2 = pack2(scale, scale);
+  const float ip = 1.0f / sp.z, aq = a / sq.z;
+  for_rows<T, kRows<T>, false>(
+      tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kRows<T>; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float2 pe = exps(l[j].at(e), l[j].at(e + 1), bp, scale2);
+            const float2 qe = exps(d[j].at(e), d[j].at(e + 1), bq, scale2);
+            s += fmaxf(fmaf(pe.x, ip, -qe.x * aq), 0.0f) + fmaxf(fmaf(pe.y, ip, -qe.y * aq), 0.0f);
+          }
+        y.t += s;
+      });
+  return y;
+}
+
+// The two in 64 bits.
+template <class T>
+__device__ __noinline__ Sums64 pass_sums64(const T* tr, const T* dr, int32_t V, uint32_t rank,
+                                           uint32_t ctas, double scale, float mp, float mq) {
+  Sums64 x = {0.0, 0.0};
+  for_rows<T, 1, false>(tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x.p += exp2_64(((double)l[0].at(k) - (double)mp) * scale);
+      if (dr) x.q += exp2_64(((double)d[0].at(k) - (double)mq) * scale);
+    }
+  });
+  return x;
+}
+template <class T>
+__device__ __noinline__ Total<double> pass_total64(const T* tr, const T* dr, int32_t V, uint32_t rank,
+                                                   uint32_t ctas, double scale, float mp, float mq,
+                                                   double zp, double zq, double a) {
+  Total<double> y = {0.0};
+  const double ip = 1.0 / zp, aq = a / zq;
+  for_rows<T, 1, false>(tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      y.t += fmax(exp2_64(((double)l[0].at(k) - (double)mp) * scale) * ip -
+                      exp2_64(((double)d[0].at(k) - (double)mq) * scale) * aq,
+                  0.0);
+  });
+  return y;
+}
+
+// The scores of the last pass: in log2 units where no sum is known (a leaf),
+// else what is left over the noise.
+struct Scores {
+  bool leaf, two;
+  float scale, ip, aq;
+  Sum sp;
+  float mq;
+  int32_t n_removed;
+  uint32_t removed_bits[2];
+  const int32_t* removed;   // in shared memory
+  template <class T>
+  __device__ __forceinline__ void of(int32_t i0, const Eight<T>& l, const Eight<T>& d,
+                                     const Eight<float>& e, float (&v)[8], uint32_t& bad) const {
+    if (leaf) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float lk = l.at(k);
+        if (!(lk < INFINITY)) bad = 1u;
+        v[k] = fmaf(lk, scale, -__log2f(e.at(k)));
+      }
+      return;
+    }
+    const uint64_t bp = pack2(-sp.m, -sp.m), bq = pack2(-mq, -mq), scale2 = pack2(scale, scale);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float2 pe = exps(l.at(k), l.at(k + 1), bp, scale2);
+      v[k] = pe.x * ip;
+      v[k + 1] = pe.y * ip;
+      if (two) {
+        const float2 qe = exps(d.at(k), d.at(k + 1), bq, scale2);
+        v[k] = fmaxf(v[k] - qe.x * aq, 0.0f);
+        v[k + 1] = fmaxf(v[k + 1] - qe.y * aq, 0.0f);
+      }
+      v[k] = __fdividef(v[k], e.at(k));
+      v[k + 1] = __fdividef(v[k + 1], e.at(k + 1));
+    }
+    if (n_removed) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if ((removed_bits[((i0 + k) >> 5) & 1] >> ((i0 + k) & 31)) & 1u)
+          for (int r = 0; r < n_removed; ++r)
+            if (removed[r] == i0 + k) v[k] = 0.0f;
+    }
+  }
+};
+
+// The best score and the value of the second.
+template <class T>
+__device__ __noinline__ Best pass_token(const T* tr, const T* dr, const float* noise, int32_t V,
+                                        uint32_t rank, uint32_t ctas, const Scores& sc) {
+  constexpr int kN = kRows<T> / 2;
+  Best x = Best::none();
+  for_rows<T, kN, true>(
+      tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          float v[8];
+          sc.of(i0[j], l[j], d[j], e[j], v, x.bad);
+          float m = v[0];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
+          if (m > x.second) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int32_t i = i0[j] + k;
+              if (v[k] > x.second && i >= 0 && i < V) {
+                if (v[k] > x.v) {
+                  x.second = x.v;
+                  x.v = v[k];
+                  x.i = i;
+                } else {
+                  x.second = v[k];
+                }
+              }
+            }
+          }
+        }
+      });
+  return x;
+}
+
+// Again, the candidates from `near` up in 64 bits.
+template <class T>
+__device__ __noinline__ Exact pass_near(const T* tr, const T* dr, const float* noise, int32_t V,
+                                        uint32_t rank, uint32_t ctas, const Scores& sc, float top,
+                                        float near, float temp, Sum sq, double a) {
+  Exact best = Exact::none();
+  for_rows<T, 1, true>(
+      tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
+        float v[8];
+        uint32_t bad;
+        sc.of(i0[0], l[0], d[0], e[0], v, bad);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int32_t i = i0[0] + k;
+          if (!(v[k] >= near) || i < 0 || i >= V) continue;
+          const double s = exact_score(sc.leaf, top, temp, l[0].at(k), sc.sp, sc.two,
+                                       sc.two ? d[0].at(k) : 0.0f, sq, a, e[0].at(k));
+          best.add({s, i, 0}, 0.0f);
+        }
+      });
+  return best;
+}
+
+// Tests of the children in `todo`, in call order, by a whole warp (every warp of
+// the cluster does the same): lane k has what belongs to children k and k + 32;
+// `p`, `q`: of their tokens.
+template <class Real>
+__device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const Kid (&kid)[2],
+                                                const Real (&p)[2], const Real (&q)[2], int lane) {
+  constexpr bool kFast = sizeof(Real) == 4;
+  while (s.todo) {
+    const int k = __ffsll((long long)s.todo) - 1, h = k >> 5, l = k & 31;
+    s.todo &= s.todo - 1;
+    const int32_t t = __shfl_sync(0xffffffffu, h ? kid[1].token : kid[0].token, l);
+    if (t < 0) continue;
+    const Real pk = __shfl_sync(0xffffffffu, h ? p[1] : p[0], l);
+    const Real qk = __shfl_sync(0xffffffffu, h ? q[1] : q[0], l);
+    const Real uk = __shfl_sync(0xffffffffu, h ? kid[1].u : kid[0].u, l);
+    // certain drafts: nothing is left of a token that was removed
+    if (!two && __any_sync(0xffffffffu, s.removed[0] == t || s.removed[1] == t)) continue;
+    const Real x = uk * qk * s.b, y = two ? pk - s.a * qk : pk;
+    // the probabilities are good to 2e-6 of themselves (of a token 2^-30 as likely
+    // as the first), a and b to 2e-6 (1 + a)
+    if (kFast) {
+      const float near = two ? (s.a + uk * (1.0f + s.a)) * qk : uk;
+      if (fabsf((float)(x - y)) <= 1e-5f * (float)(pk + near)) return kExact;
+    }
+    if (x < y) {
+      s.taken = k;
+      return kGo;
+    }
+    if (two) {
+      s.a_prev = s.a;
+      s.a += s.b;
+      if (s.todo) return kSum;           // else the sum that is left is not needed
+    } else if (s.b - pk > Real(0)) {
+      s.b -= pk;
+      if (lane == (s.n_removed & 31)) {
+        if (s.n_removed < 32) s.removed[0] = t;
+        else s.removed[1] = t;
+      }
+      ++s.n_removed;
+    }
+  }
+  return kToken;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    k_verify(const __grid_constant__ VerifyParams p, const int ctas) {
   __shared__ Smem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = (uint32_t)blockIdx.x % (uint32_t)ctas;   // of the cluster
   const int tree = (int)((uint32_t)blockIdx.x / (uint32_t)ctas);
   const int32_t d0 = p.first[tree], n = p.first[tree + 1] - d0, V = p.vocab;
-  griddep_wait();
-  if (tid == 0) {
-    float t = p.temperature ? p.temperature[tree] : 0.0f;
-    sm.temperature = t > 0.0f ? t : 0.0f;
-  }
-  __syncthreads();
-  cluster_arrive();
-  cluster_wait();
-  float temp;
-  {
-    const uint32_t at = dsmem_addr(smem_u32(&sm.temperature), 0);
-    temp = ld_dsmem_f32(at);
-  }
-  const bool greedy = temp == 0.0f;
-  const float scale = greedy ? 1.0f : 1.4426950408889634f / temp;   // logits to log2 units
   const T* root = static_cast<const T*>(p.root);
   const T* droot = static_cast<const T*>(p.draft_root);
+  const float* noise = p.noise + (int64_t)tree * p.noise_ld;
+  // lane k of every warp has the parents of drafts k and k + 32
+  int32_t parent[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) parent[h] = lane + 32 * h < n ? p.parent[d0 + lane + 32 * h] : -2;
+  const int halves = n > 32 ? 2 : 1;
+  griddep_wait();
+  // the first CTA's: their tokens and numbers
+  int32_t token[2] = {-1, -1};
+  float uniform[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (rank == 0 && lane + 32 * h < n) {
+      token[h] = __ldg(p.token + d0 + lane + 32 * h);
+      if (p.uniform) uniform[h] = __ldg(p.uniform + d0 + lane + 32 * h);
+    }
+  if (rank == 0 && tid == 0) {
+    const float t = p.temperature ? p.temperature[tree] : 0.0f;
+    sm.temperature = t > 0.0f ? t : 0.0f;
+  }
+  // a row's share on its way to L2 while the cluster is not ready to read it
+  auto prefetch = [&](const auto* r) {
+    constexpr int kLine = 128 / sizeof(*r);
+    for (int32_t i = kLine * ((int32_t)rank * kThreads + tid); i < V; i += kLine * ctas * kThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(r + i));
+  };
+  if (root) prefetch(root + (int64_t)tree * p.ld);
+  if (droot) prefetch(droot + (int64_t)tree * p.ld);
+  cluster_arrive();
+  cluster_wait();
+  const float temp = ld_dsmem_f32(dsmem_addr(smem_u32(&sm.temperature), 0));
+  const bool greedy = temp == 0.0f;
+  const float scale = greedy ? 1.0f : 1.4426950408889634f / temp;   // logits to log2 units
   auto row_of = [&](const void* rows, const T* roots, int node) -> const T* {
     return node < 0 ? (roots ? roots + (int64_t)tree * p.ld : nullptr)
                     : (rows ? static_cast<const T*>(rows) + ((int64_t)d0 + node) * p.ld : nullptr);
   };
   int pass = 0;
 
-  // Joins the threads' parts over the cluster into sm.all; `kids`: the
-  // children's data of the first CTA into sm.tok / u (and pd, qd: the logits)
-  auto join = [&](Part x, bool kids) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Sum yp = {__shfl_xor_sync(0xffffffffu, x.p.m, o), __shfl_xor_sync(0xffffffffu, x.p.z, o)};
-      const Sum yq = {__shfl_xor_sync(0xffffffffu, x.q.m, o), __shfl_xor_sync(0xffffffffu, x.q.z, o)};
-      const Best yb = {__shfl_xor_sync(0xffffffffu, x.best.v, o),
-                       __shfl_xor_sync(0xffffffffu, x.best.second, o),
-                       __shfl_xor_sync(0xffffffffu, x.best.i, o)};
-      // the lower lane's part first: both lanes get the same sum
-      const bool lo = (lane & o) == 0;
-      x.p = lo ? sum_merge(x.p, yp, scale) : sum_merge(yp, x.p, scale);
-      x.q = lo ? sum_merge(x.q, yq, scale) : sum_merge(yq, x.q, scale);
-      x.best = best_merge(x.best, yb);
-      x.total += __shfl_xor_sync(0xffffffffu, x.total, o);
-      x.bad |= __shfl_xor_sync(0xffffffffu, x.bad, o);
-      const double e = __shfl_xor_sync(0xffffffffu, x.exact, o);
-      const int32_t ei = __shfl_xor_sync(0xffffffffu, x.exact_i, o);
-      if (e > x.exact || (e == x.exact && (uint32_t)ei < (uint32_t)x.exact_i)) {
-        x.exact = e;
-        x.exact_i = ei;
-      }
-    }
-    auto merge = [&](Part& s, const Part& y) {
-      s.p = sum_merge(s.p, y.p, scale);
-      s.q = sum_merge(s.q, y.q, scale);
-      s.best = best_merge(s.best, y.best);
-      s.total += y.total;
-      s.bad |= y.bad;
-      if (y.exact > s.exact || (y.exact == s.exact && (uint32_t)y.exact_i < (uint32_t)s.exact_i)) {
-        s.exact = y.exact;
-        s.exact_i = y.exact_i;
-      }
-    };
-    if (lane == 0) sm.warp[warp] = x;
-    __syncthreads();
-    const int par = pass & 1;
+  // The threads' parts merged over the cluster, in every thread: each warp
+  // sends its own to all CTAs, and after the barrier merges all of them.
+  auto join = [&](auto x) {
+    using Part = decltype(x);
+    static_assert(sizeof(Part) <= 4 * kPartWords, "parts");
+    const int par = pass & 1, n_parts = ctas * kWarps;
     ++pass;
-    if (tid == 0) {
-      Part s = sm.warp[0];
-      for (int w = 1; w < kWarps; ++w) merge(s, sm.warp[w]);
-      sm.part[par] = s;
-    }
-    __syncthreads();
+    x.over(32, lane, scale);
+    if (lane < ctas) st_peer(sm.part[par][rank * kWarps + warp], lane, x);
     cluster_arrive();
     cluster_wait();
-    if (tid == 0) {
-      Part s = ld_peer(&sm.part[par], 0);
-      for (int r = 1; r < ctas; ++r) merge(s, ld_peer(&sm.part[par], r));
-      sm.all = s;
-    }
-    if (kids && tid >= 64 && tid < 128 && ((sm.kids >> (tid - 64)) & 1ull)) {
-      const int k = tid - 64;
-      const Kid y = ld_peer(&sm.kid[par][k], 0);
-      sm.tok[k] = y.token;
-      sm.u[k] = y.u;
-      sm.pd[k] = y.lp;
-      sm.qd[k] = y.lq;
-    }
-    __syncthreads();
+    x = lane < n_parts ? *reinterpret_cast<const Part*>(sm.part[par][lane]) : Part::none();
+    if (lane + 32 < n_parts) x.add(*reinterpret_cast<const Part*>(sm.part[par][lane + 32]), scale);
+    x.over(n_parts < 32 ? n_parts : 32, lane, scale);
+    // (fewer parts than lanes: lane 0's)
+    Part y;
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(&x);
+    uint32_t* to = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(Part) / 4); ++k) to[k] = __shfl_sync(0xffffffffu, from[k], 0);
+    return y;
   };
-  const Part none = {{-INFINITY, 0.0f}, {-INFINITY, 0.0f}, 0.0f, 0u, {-INFINITY, -INFINITY, -1}, -1.0, -1};
 
   int node = -1, last = -1;
   int32_t result = -1;
+  bool first = true;
   if (!root) {
     // the root's only child is the token that the last step has drawn
     if (n > 0) node = last = 0;
   }
   while (root || node >= 0) {
-    // ---- the node's children
-    uint64_t kids = 0;
-    {
-      const bool kid = tid < 64 && tid < n && p.parent[d0 + tid] == node;
-      const uint32_t m = __ballot_sync(0xffffffffu, kid);
-      __syncthreads();
-      if (warp < 2 && lane == 0) reinterpret_cast<uint32_t*>(&sm.kids)[warp] = m;
-      __syncthreads();
-      kids = sm.kids;
-    }
+    const uint64_t kids =
+        (uint64_t)__ballot_sync(0xffffffffu, parent[0] == node) |
+        ((uint64_t)__ballot_sync(0xffffffffu, parent[1] == node) << 32);
     const T* tr = row_of(p.target, root, node);
     const T* dr = kids && !greedy ? row_of(p.draft, droot, node) : nullptr;
-    if (rank == 0 && tid < 64 && ((kids >> tid) & 1ull)) {
-      Kid k = {-INFINITY, -INFINITY, 0.0f, p.token[d0 + tid]};
-      if (k.token < 0 || k.token >= V) k.token = -1;
-      if (!greedy) {
-        k.u = p.uniform[d0 + tid];
-        if (k.token >= 0) {
-          k.lp = value_at(tr, k.token);
-          if (dr) k.lq = value_at(dr, k.token);
-        }
+    const bool leaf = !kids;
+    // the children, by way of the first CTA: its warp r reads their logits and,
+    // with its part of the pass, sends them to CTA r
+    Kid kid[2] = {{-1, 0.0f, 0.0f, 0.0f}, {-1, 0.0f, 0.0f, 0.0f}};
+    const int kid_par = pass & 1;
+    uint32_t lp[2], lq[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lp[h] = lq[h] = 0u;
+      if (rank == 0 && h < halves && !leaf && !greedy) {
+        const int32_t t = token[h] >= 0 && token[h] < V ? token[h] : 0;
+        lp[h] = bits_now(tr, t);
+        if (dr) lq[h] = bits_now(dr, t);
       }
-      sm.kid[pass & 1][tid] = k;
     }
+    auto send_kids = [&] {
+      if (rank == 0 && warp < ctas) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (parent[h] == node)
+            st_peer(&sm.kid[kid_par][lane + 32 * h], warp,
+                    Kid{token[h] >= 0 && token[h] < V ? token[h] : -1, uniform[h],
+                        value_of<T>(lp[h]), value_of<T>(lq[h])});
+      }
+    };
+    auto take_kids = [&] {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (parent[h] == node) kid[h] = sm.kid[kid_par][lane + 32 * h];
+    };
 
     if (greedy) {
-      Part x = none;
-      for_rows<T, kVec>(tr, static_cast<const T*>(nullptr), nullptr, V, rank, ctas, -INFINITY,
-                        [&](int64_t i0, int64_t step, const float (&l)[8], const float (&)[8],
-                            const float (&)[8]) {
-#pragma unroll
-                          for (int k = 0; k < 8; ++k) {
-                            if (!(l[k] < INFINITY)) x.bad = 1u;
-                            if (l[k] > x.best.v) {
-                              x.best.v = l[k];
-                              x.best.i = (int32_t)(i0 + k * step);
-                            }
-                          }
-                        });
-      join(x, true);
-      if (sm.all.bad || sm.all.best.i < 0) break;
-      const int32_t top = sm.all.best.i;
-      int32_t taken = -1;
-      for (uint64_t m = kids; m; m &= m - 1) {
-        const int k = __ffsll((long long)m) - 1;
-        if (sm.tok[k] == top) {
-          taken = k;
-          break;
-        }
-      }
-      __syncthreads();
-      if (taken < 0) {
-        result = top;
+      Best x = pass_largest(tr, V, rank, ctas);
+      send_kids();
+      x = join(x);
+      take_kids();
+      if (x.bad || x.i < 0) break;
+      // the first child with that token
+      const uint64_t same =
+          (uint64_t)__ballot_sync(0xffffffffu, parent[0] == node && kid[0].token == x.i) |
+          ((uint64_t)__ballot_sync(0xffffffffu, parent[1] == node && kid[1].token == x.i) << 32);
+      if (!same) {
+        result = x.i;
         break;
       }
-      node = last = taken;
+      node = last = __ffsll((long long)same) - 1;
       continue;
     }
 
-    // rows p and q of the node for the last pass: p * ip and q * iq
-    double a = 0.0, a_prev = 0.0;
-    int32_t n_removed = 0;
+    // what is left at the node
     Sum sp = {0.0f, 1.0f}, sq = {0.0f, 1.0f};
-    if (kids) {
-      // ---- maxima and sums of the node's rows
-      Part x = none;
-      auto add = [&](Sum& s, const float (&l)[8]) {
-        float m = -INFINITY;
+    float left_a = 0.0f, left_a_prev = 0.0f;
+    int32_t n_removed = 0;
+    uint32_t removed_bits[2] = {0u, 0u};   // of the removed tokens' last six bits
+    if (!leaf) {
+      Sums x = pass_sums(tr, dr, V, rank, ctas, scale);
+      send_kids();
+      x = join(x);
+      take_kids();
+      // the noise is read once, at the walk's end: on its way to L2 meanwhile
+      if (first) prefetch(noise);
+      first = false;
+      if (!(x.p.z < INFINITY && x.p.m > -INFINITY)) break;
+      if (dr && !(x.q.z < INFINITY && x.q.m > -INFINITY)) break;
+      sp = x.p;
+      if (dr) sq = x.q;
+      // ---- tests; those too near to call again with numbers in 64 bits
+      Action action;
+      int32_t taken, removed[2];
+      {
+        Tests<float> s = {0.0f, 0.0f, 1.0f, kids, -1, {-1, -1}, 0};
+        float pk[2] = {0.0f, 0.0f}, qk[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (!(l[k] < INFINITY)) x.bad = 1u;
-          m = fmaxf(m, l[k]);
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves) break;
+          pk[h] = __fdividef(exp2f((kid[h].lp - sp.m) * scale), sp.z);
+          qk[h] = dr ? __fdividef(exp2f((kid[h].lq - sq.m) * scale), sq.z) : 1.0f;
         }
-        if (m > s.m) {
-          s.z *= fast_exp2((s.m - m) * scale);
-          s.m = m;
+        while ((action = test_children<float>(s, dr, kid, pk, qk, lane)) == kSum) {
+          const Total<float> y = join(pass_total(tr, dr, V, rank, ctas, scale, sp, sq, s.a));
+          if (y.t > 0.0f) s.b = y.t;
+          else s.a = s.a_prev;
         }
-        const float base = s.m == -INFINITY ? 0.0f : s.m;
-        float z = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) z += fast_exp2((l[k] - base) * scale);
-        s.z += z;
-      };
-      for_rows<T, kVec>(tr, dr, nullptr, V, rank, ctas, -INFINITY,
-                        [&](int64_t, int64_t, const float (&l)[8], const float (&d)[8],
-                            const float (&)[8]) {
-                          add(x.p, l);
-                          if (dr) add(x.q, d);
-                        });
-      join(x, true);
-      sp = sm.all.p;
-      sq = sm.all.q;
-      if (sm.all.bad || sp.m == -INFINITY || (dr && sq.m == -INFINITY)) break;
-      // ---- probabilities of the children's tokens, in 64 bits
-      if (tid < 64 && ((kids >> tid) & 1ull)) {
+        taken = s.taken;
+        left_a = s.a;
+        left_a_prev = s.a_prev;
+        n_removed = s.n_removed;
+        removed[0] = s.removed[0];
+        removed[1] = s.removed[1];
+      }
+      if (action == kExact) {
         const double c = 1.4426950408889634 / (double)temp;
-        const bool in = sm.tok[tid] >= 0;
-        sm.pd[tid] = in ? exp2((sm.pd[tid] - (double)sp.m) * c) / (double)sp.z : 0.0;
-        sm.qd[tid] = !in ? 0.0 : dr ? exp2((sm.qd[tid] - (double)sq.m) * c) / (double)sq.z : 1.0;
-      }
-      __syncthreads();
-      // ---- tests, in call order
-      double b = 1.0;
-      int32_t taken = -1;
-      uint64_t m = kids;
-      while (m) {
-        const int k = __ffsll((long long)m) - 1;
-        m &= m - 1;
-        const int32_t t = sm.tok[k];
-        if (t < 0) continue;
-        const double pk = sm.pd[k], qk = sm.qd[k], u = sm.u[k];
-        if (dr) {
-          if (u * qk * b < pk - a * qk) {
-            taken = k;
-            break;
-          }
-          a_prev = a;
-          a += b;
-          if (!m) break;                 // the sum that is left is not needed
-          Part y = none;
-          const float ip = 1.0f / sp.z, iq = (float)(a / (double)sq.z);
-          for_rows<T, kVec>(tr, dr, nullptr, V, rank, ctas, -INFINITY,
-                            [&](int64_t, int64_t, const float (&l)[8], const float (&d)[8],
-                                const float (&)[8]) {
-                              float s = 0.0f;
+        const Sums64 z = join(pass_sums64(tr, dr, V, rank, ctas, c, sp.m, sq.m));
+        Tests<double> s = {0.0, 0.0, 1.0, kids, -1, {-1, -1}, 0};
+        double pk[2], qk[2];
 #pragma unroll
-                              for (int e = 0; e < 8; ++e)
-                                s += fmaxf(fast_exp2((l[e] - sp.m) * scale) * ip -
-                                               fast_exp2((d[e] - sq.m) * scale) * iq,
-                                           0.0f);
-                              y.total += s;
-                            });
-          join(y, false);
-          if (sm.all.total > 0.0f) b = sm.all.total;
-          else a = a_prev;
-          __syncthreads();
-        } else {
-          bool gone = false;
-          for (int r = 0; r < n_removed; ++r) gone |= sm.removed[r] == t;
-          if (gone) continue;            // nothing of it is left
-          if (u * b < pk) {
-            taken = k;
-            break;
-          }
-          if (b - pk > 0.0) {
-            b -= pk;
-            __syncthreads();
-            if (tid == 0) sm.removed[n_removed] = t;
-            ++n_removed;
-            __syncthreads();
-          }
+        for (int h = 0; h < 2; ++h) {
+          pk[h] = exp2(((double)kid[h].lp - (double)sp.m) * c) / z.p;
+          qk[h] = dr ? exp2(((double)kid[h].lq - (double)sq.m) * c) / z.q : 1.0;
         }
+        while ((action = test_children<double>(s, dr, kid, pk, qk, lane)) == kSum) {
+          const Total<double> y =
+              join(pass_total64(tr, dr, V, rank, ctas, c, sp.m, sq.m, z.p, z.q, s.a));
+          if (y.t > 0.0) s.b = y.t;
+          else s.a = s.a_prev;
+        }
+        taken = s.taken;
+        left_a = (float)s.a;
+        left_a_prev = (float)s.a_prev;
+        n_removed = s.n_removed;
+        removed[0] = s.removed[0];
+        removed[1] = s.removed[1];
       }
-      __syncthreads();
-      if (taken >= 0) {
+      if (action == kGo) {
         node = last = taken;
         continue;
+      }
+      if (n_removed) {
+        for (int r = 0; r < n_removed; ++r) {
+          const int32_t t = __shfl_sync(0xffffffffu, r < 32 ? removed[0] : removed[1], r & 31);
+          removed_bits[(t >> 5) & 1] |= 1u << (t & 31);
+          if (tid == 0) sm.removed[r] = t;
+        }
+        __syncthreads();
       }
     }
 
     // ---- the next token
-    const float* noise = p.noise + (int64_t)tree * p.noise_ld;
-    const bool leaf = !kids;
-    // scores in log2 units where no sum is needed (a leaf), else probabilities
-    // over noise; 64-bit form of element i
-    auto exact_score = [&](int32_t i) -> double {
-      const double c = 1.4426950408889634 / (double)temp, e = (double)__ldg(noise + i);
-      const double l = (double)value_at(tr, i);
-      if (leaf) return exp2(l * c - floor((double)sm.all.best.v)) / e;
-      const double pv = exp2((l - (double)sp.m) * c) / (double)sp.z;
-      if (!dr) return pv / e;
-      const double qv = exp2(((double)value_at(dr, i) - (double)sq.m) * c) / (double)sq.z;
-      return fmax(pv - a * qv, 0.0) / e;
-    };
     bool again = false;
     while (true) {
-      const float ip = 1.0f / sp.z, iq = dr ? (float)(a / (double)sq.z) : 0.0f;
-      Part x = none;
-      auto score = [&](int32_t i, float l, float d, float e) -> float {
-        if (leaf) {
-          if (!(l < INFINITY)) x.bad = 1u;
-          return fmaf(l, scale, -__log2f(e));
-        }
-        float v = fast_exp2((l - sp.m) * scale) * ip;
-        if (dr) v = fmaxf(v - fast_exp2((d - sq.m) * scale) * iq, 0.0f);
-        for (int r = 0; r < n_removed; ++r)
-          if (sm.removed[r] == i) v = 0.0f;
-        return __fdividef(v, e);
-      };
-      // with the same scores, the candidates within `near` of the best in 64 bits
-      auto scan = [&](float near, bool exact) {
-        for_rows<T, kVec>(tr, dr, noise, V, rank, ctas, -INFINITY,
-                          [&](int64_t i0, int64_t step, const float (&l)[8], const float (&d)[8],
-                              const float (&e)[8]) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                              const int64_t i = i0 + k * step;
-                              const float v = score((int32_t)i, l[k], dr ? d[k] : 0.0f, e[k]);
-                              if (i >= V) continue;
-                              if (!exact) {
-                                if (v > x.best.second) best_add(x.best, v, (int32_t)i);
-                              } else if (v >= near) {
-                                const double s = exact_score((int32_t)i);
-                                if (s > x.exact || (s == x.exact && (int32_t)i < x.exact_i)) {
-                                  x.exact = s;
-                                  x.exact_i = (int32_t)i;
-                                }
-                              }
-                            }
-                          });
-      };
-      scan(0.0f, false);
-      join(x, false);
-      const Part& all = sm.all;
-      if (leaf ? (all.bad || !(all.best.v > -INFINITY)) : !(all.best.v > 0.0f)) {
-        // a node's row that nothing is left of: as before the last rejection
-        if (!leaf && dr && !again && a != a_prev) {
+      Scores sc;
+      sc.leaf = leaf;
+      sc.two = dr != nullptr;
+      sc.scale = scale;
+      sc.sp = sp;
+      sc.ip = 1.0f / sp.z;
+      sc.mq = sq.m;
+      const float a = again ? left_a_prev : left_a;
+      sc.aq = dr ? a / sq.z : 0.0f;
+      sc.n_removed = n_removed;
+      sc.removed_bits[0] = removed_bits[0];
+      sc.removed_bits[1] = removed_bits[1];
+      sc.removed = sm.removed;
+      const Best top = join(pass_token(tr, dr, noise, V, rank, ctas, sc));
+      if (leaf ? (top.bad || !(top.v > -INFINITY)) : !(top.v > 0.0f)) {
+        // nothing is left: as before the last rejection
+        if (dr && !again && left_a != left_a_prev) {
           again = true;
-          a = a_prev;
-          __syncthreads();
           continue;
         }
         break;
       }
-      result = all.best.i;
-      const float near = leaf ? all.best.v - 2e-6f * (fabsf(all.best.v) + 256.0f)
-                              : all.best.v * (1.0f - 1e-4f);
-      if (all.best.second >= near) {
-        x = none;
-        scan(near, true);
-        __syncthreads();
-        join(x, false);
-        result = sm.all.exact_i;
-      }
+      result = top.i;
+      // candidates that the fp32 scores may have in the wrong order: a leaf's
+      // are off by a few 2^-24 of the logit in log2 units, the others by less
+      // than 2^-14 of themselves unless p and a q are all but equal
+      const float near = leaf ? top.v - 2e-6f * (fabsf(top.v) + 256.0f) : top.v * (1.0f - 1e-4f);
+      if (top.second >= near)
+        result = join(pass_near(tr, dr, noise, V, rank, ctas, sc, top.v, near, temp, sq, a)).i;
       break;
     }
     break;
@@ -511,7 +886,7 @@ __global__ void __launch_bounds__(kThreads) k_verify(const __grid_constant__ Ver
     p.accepted[tree] = last;
     p.next_token[tree] = result;
   }
-  // no CTA leaves while another may read its shared memory
+  // no CTA leaves while another may write to its shared memory
   cluster_arrive();
   cluster_wait();
 }
@@ -529,11 +904,18 @@ cudaError_t launch(const VerifyParams& p, int cluster, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return p.vec ? cudaLaunchKernelEx(&cfg, k_verify<T, true>, p, cluster)
-               : cudaLaunchKernelEx(&cfg, k_verify<T, false>, p, cluster);
+  return cudaLaunchKernelEx(&cfg, k_verify<T>, p, cluster);
 }
 
 }  // namespace
+
+// CTAs of a sequence's cluster: as many as run at once over the whole GPU, with
+// a share of the vocabulary worth a pass each.
+int verify_cluster(int64_t n_trees, int32_t vocab, int sms) {
+  int c = 1;
+  while (c < kMaxCluster && n_trees * c * 2 <= (int64_t)sms * kBlocks && vocab >= 4096 * c) c *= 2;
+  return c;
+}
 
 cudaError_t launch_verify(const VerifyParams& p, bool fp32, int cluster, cudaStream_t s) {
   if (p.n_trees <= 0) return cudaSuccess;

@@ -918,7 +918,7 @@ csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t
  * Equal values go to the lower token.  An infinitely negative logit is a
  * probability of 0; a node whose row holds a NaN or an infinity of the other
  * sign, or nothing but negative infinities, ends the walk with token -1.
- *   vocab: 1 .. 2^31 - 1;  token: dev int32 [n_queries], the drafts' tokens
+ *   vocab: 1 .. 2^30;  token: dev int32 [n_queries], the drafts' tokens
  *   (one outside the vocabulary is never accepted, and removes nothing);
  *   target, draft: dev [n_queries, vocab] bf16, or fp32 with fp32 = 1, row
  *   t the logits after draft t, rows ld elements apart (at least vocab);

@@ -297,6 +297,41 @@ def test_near_ties_are_decided_exactly():
     assert got == want
 
 
+@pytest.mark.parametrize("kind", ["logits", "certain"])
+def test_tests_at_their_border_are_decided_exactly(kind):
+    """Uniform numbers next to the probability that they are compared with, nearer
+    than fp32 can tell: first children, and second ones after a rejection."""
+    V, S = 3000, 120
+    parents = [[-1, -1, 0, 1]] * S
+    d = make(parents, V, torch.float32, 31)
+    d["temperature"].fill_(0.75)
+    if kind == "certain":
+        d["draft_logits"] = d["draft_root"] = None
+    d["uniform"].fill_(0.999999)
+    for i in range(S):
+        p = torch.softmax(d["root_logits"][i].double() / 0.75, 0)
+        x, y = d["tokens"][4 * i].item(), (d["tokens"][4 * i].item() + 1 + i) % V
+        d["tokens"][4 * i + 1] = y
+        if kind == "certain":
+            q = torch.zeros_like(p)
+            q[x] = 1
+        else:
+            q = torch.softmax(d["draft_root"][i].double() / 0.75, 0)
+        if i % 2 == 0:
+            u, c = (p[x] / q[x]).item(), 4 * i
+        else:
+            rest = (p - q).clamp(min=0)
+            rest /= rest.sum()
+            u, c = (rest[y] / (1.0 if kind == "certain" else q[y])).item(), 4 * i + 1
+        u = torch.tensor(u if u < 0.9 else 0.5, dtype=torch.float32)
+        for _ in range(i % 3):
+            u = torch.nextafter(u, torch.tensor(float(i % 4 < 2)))
+        d["uniform"][c] = u
+    got, want = run(parents, d), expect(parents, d)
+    assert got == want
+    assert 10 < sum(a >= 0 for a, _ in want) < S
+
+
 def test_strides_streams_and_graphs():
     c = C()
     parents = [random_tree(6, i) for i in range(5)]
