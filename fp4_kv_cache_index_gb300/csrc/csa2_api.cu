@@ -2102,11 +2102,9 @@ bool sm_count(int* n) {
          cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-// Queries and outputs [n * n_heads, 512] as 64-row boxes of 64 channels.
-bool window_maps(const void* q, const void* out, int64_t n, int32_t n_heads, CUtensorMap* mq,
-                 CUtensorMap* mo) {
-  return make_map(mq, q, (uint64_t)n * n_heads, kHeadDim, 64, 64) &&
-         make_map(mo, out, (uint64_t)n * n_heads, kHeadDim, 64, 64);
+// Queries [n * n_heads, 512] as 64-row boxes of 64 channels.
+bool window_map(const void* q, int64_t n, int32_t n_heads, CUtensorMap* m) {
+  return make_map(m, q, (uint64_t)n * n_heads, kHeadDim, 64, 64);
 }
 
 constexpr int32_t kWinRowLimit = INT32_MAX / 128;   // queries: rows of a map count in int32
@@ -2298,10 +2296,10 @@ csa2_status_t csa2_window_attn_decode(const csa2_window_t* w, int32_t n_heads, i
     p->seq0 = i;
     if (seq_ids) std::copy(seq_ids + i, seq_ids + i + n, p->seq);
     p->lse = lse ? lse + row : nullptr;
-    CUtensorMap mq, mo;
-    if (!window_maps(static_cast<const uint16_t*>(q) + row * kHeadDim,
-                     static_cast<uint16_t*>(out) + row * kHeadDim, n, n_heads, &mq, &mo) ||
-        launch_window_decode(*p, mq, mo, sms, S(stream)) != cudaSuccess)
+    p->out = static_cast<uint16_t*>(out) + row * kHeadDim;
+    CUtensorMap mq;
+    if (!window_map(static_cast<const uint16_t*>(q) + row * kHeadDim, n, n_heads, &mq) ||
+        launch_window_decode(*p, mq, sms, S(stream)) != cudaSuccess)
       st = CSA2_ERR_CUDA;
     i += n;
   }
@@ -2357,10 +2355,10 @@ csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t
     if (p->nq == 0) continue;
     const int64_t at = row0 * n_heads;
     p->lse = lse ? lse + at : nullptr;
-    CUtensorMap mq, mo;
-    if (!window_maps(static_cast<const uint16_t*>(q) + at * kHeadDim,
-                     static_cast<uint16_t*>(out) + at * kHeadDim, p->nq, n_heads, &mq, &mo) ||
-        launch_window_tree(*p, mq, mo, sms, S(stream)) != cudaSuccess)
+    p->out = static_cast<uint16_t*>(out) + at * kHeadDim;
+    CUtensorMap mq;
+    if (!window_map(static_cast<const uint16_t*>(q) + at * kHeadDim, p->nq, n_heads, &mq) ||
+        launch_window_tree(*p, mq, sms, S(stream)) != cudaSuccess)
       st = CSA2_ERR_CUDA;
   }
   delete p;
@@ -2398,9 +2396,9 @@ csa2_status_t csa2_window_attn_prefill(int32_t n_heads, int32_t nq, int64_t pos0
   p.band0 = rows_pos0;
   p.n_band = n_rows;
   int sms = 0;
-  CUtensorMap mq, mo;
-  if (!sm_count(&sms) || !window_maps(q, out, nq, n_heads, &mq, &mo)) return CSA2_ERR_CUDA;
-  return cuda_status(launch_window_prefill(p, mq, mo, sms, S(stream)));
+  CUtensorMap mq;
+  if (!sm_count(&sms) || !window_map(q, nq, n_heads, &mq)) return CSA2_ERR_CUDA;
+  return cuda_status(launch_window_prefill(p, mq, sms, S(stream)));
 }
 
 csa2_status_t csa2_window_device_error(const csa2_window_t* w, csa2_stream_t stream,

@@ -428,12 +428,12 @@ struct WinPrefillParams : WinAttnCommon {
   const uint16_t* first;
   int64_t pos0, band0, n_band;
 };
-cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q,
-                                 const CUtensorMap& out, int sms, cudaStream_t s);
-cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q,
-                               const CUtensorMap& out, int sms, cudaStream_t s);
-cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q,
-                                  const CUtensorMap& out, int sms, cudaStream_t s);
+cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q, int sms,
+                                 cudaStream_t s);
+cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q, int sms,
+                               cudaStream_t s);
+cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q, int sms,
+                                  cudaStream_t s);
 static_assert(sizeof(WinAppendParams) < 32764 && sizeof(WinReadParams) < 32764 &&
               sizeof(WinAcceptParams) < 32764, "kernel parameters");
 static_assert(sizeof(WinDecodeParams) + 3 * sizeof(CUtensorMap) < 32764 &&

@@ -21,7 +21,7 @@
 //
 // Roles: warp 0 loads Q (TMA), warp 1 issues the MMAs, warps 2 and 3 load
 // rows, warps 4-11 (two for each quadrant of tensor memory lanes) do the
-// softmax and the outputs, which leave through shared memory by TMA.
+// softmax and the outputs, which go to memory from registers.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -40,25 +40,35 @@ constexpr int kRing = 17;               // blocks of 8 window rows
 constexpr int kFirstSlot = 8 * 16;      // first tokens, decode and trees
 constexpr int kChunkFirst = 8 * kRing;  // first tokens, chunks
 constexpr int kBlk = kSlots * 128;      // bytes of a 64-channel block of rows
-constexpr int kStages = 3;              // Q: 128 rows x 64 channels each
-constexpr int kStageBytes = 128 * 128;
+constexpr int kBox = 64 * 128;          // Q: 64 rows x 64 channels
+constexpr int kQBytes = 10 * kBox;      // a stage is a box or two, in turn
+constexpr int kMaxStages = 9;
 constexpr int kLoadWarps = 2, kSoftWarps = 8;
 constexpr int kRowWarps = kLoadWarps + kSoftWarps;
 
 constexpr int kKvOff = 0;
 constexpr int kQOff = kKvOff + 8 * kBlk;
-constexpr int kOutOff = kQOff + kStages * kStageBytes;   // two boxes on their way out
-constexpr int kSmallOff = kOutOff + 2 * kStageBytes;
+constexpr int kSmallOff = kQOff + kQBytes;
 struct Small {
   float red[2][128];            // [half of the columns][row]: maxima, then sums
-  float2 rope[2][2][32];        // [item parity][token]: cos, sin of each channel pair
-  uint32_t vis[2][5];           // rows that each token sees
+  float2 rope[2][32];           // [token]: cos, sin of each channel pair
+  int64_t at[2];                // [item parity]: position of the first token
+  uint32_t vis[2][2][5];        // [item parity][token]: rows that it sees
   uint32_t bad[5];              // rows that hold an infinity or a NaN (chunks)
   alignas(4) uint8_t bad8[kRing + 1][4];   // the same, 8 rows of each block, by quarter of its loads
-  uint8_t path[kRowWarps][64];  // trees: the path's drafts, every loading warp its own
+  // cache: [item parity] what each slot takes: a row of the cache (-2), none
+  // (-1) or a draft of the tree
+  int8_t slot[2][kSlots];
+  // trees: [item parity] the path's drafts by depth, the slots that the item
+  // takes otherwise than the one before it (or, of its tree's first item, those
+  // that take drafts), and how many those are
+  uint8_t draft[2][64], list[2][kSlots];
+  int32_t n_list[2];
   uint32_t tmem;
-  uint64_t q_full[kStages], q_empty[kStages];
-  uint64_t kv_full, kv_empty, s_full, p_full, o_full, o_empty, end;
+  uint64_t q_full[kMaxStages], q_empty[kMaxStages];
+  // a wait tells neighbouring phases of a barrier apart only: those whose two
+  // sides may be two items apart are two, for items in turn
+  uint64_t kv_full[2], kv_empty[2], s_full, p_full, o_full, o_empty, tab_full, end;
 };
 constexpr int kSmemBytes = kSmallOff + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -82,12 +92,45 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int32_t x,
-                                             int32_t y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(smem_u32(src)), "r"(x), "r"(y)
-               : "memory");
+// A warp's 32 rows (a lane each) of 32 words to memory, in whole 128-byte lines:
+// four neighbouring lanes exchange their rows' quarters, after which lane j of
+// them has quarter j of all four rows.  (A lane storing its own row touches 32
+// lines an instruction, which took the store path 3400 cycles for 64 KB.)
+__device__ __forceinline__ void store_rows(uint16_t* rows, int64_t stride, uint32_t (&w)[32], int lane,
+                                           bool wide) {
+  const bool b1 = lane & 2, b0 = lane & 1;
+  uint32_t a[2][16];   // two quarters of row (lane & ~2) and of row (lane | 2)
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t keep = b1 ? w[i + 16] : w[i], give = b1 ? w[i] : w[i + 16];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 2);
+    a[0][i] = b1 ? got : keep;
+    a[1][i] = b1 ? keep : got;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[2][8];  // a quarter of row (lane & ~1) and of row (lane | 1) of those
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t keep = b0 ? a[h][i + 8] : a[h][i], give = b0 ? a[h][i] : a[h][i + 8];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+      o[0][i] = b0 ? got : keep;
+      o[1][i] = b0 ? keep : got;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint16_t* to = rows + ((lane & ~3) + 2 * h + r) * stride + 16 * (lane & 3);
+      if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(o[r][0]),
+                     "r"(o[r][1]), "r"(o[r][2]), "r"(o[r][3]), "r"(o[r][4]), "r"(o[r][5]),
+                     "r"(o[r][6]), "r"(o[r][7])
+                     : "memory");
+      else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(o[r][0], o[r][1], o[r][2], o[r][3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(o[r][4], o[r][5], o[r][6], o[r][7]);
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
@@ -113,19 +156,41 @@ __device__ __forceinline__ bool not_finite(const uint4& v) {
   return ((((v.x & m) + c) | ((v.y & m) + c) | ((v.z & m) + c) | ((v.w & m) + c)) & 0x80008000u) != 0u;
 }
 
-// Eight E4M3 codes (two words) x sc -> eight bf16, exact.
-__device__ __forceinline__ uint4 e4m3_piece(uint32_t w0, uint32_t w1, float sc) {
+// Eight E4M3 codes (two words) -> eight bf16 times a power of two, exact (in bf16's
+// normal range).  E4M3's seven lower bits four places up in a bf16 are its value times 2^-120,
+// subnormal numbers too; the sign goes to the top.  The power comes as two
+// factors (code_scales): with 2^120 it may pass bf16's range.
+__device__ __forceinline__ uint4 e4m3_piece(uint32_t w0, uint32_t w1, uint2 scales) {
   const uint32_t w[2] = {w0, w1};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-    o[i] = *reinterpret_cast<const uint32_t*>(&b);
+    const uint32_t t = prmt(w[i >> 1], 0u, (i & 1) ? 0x3424u : 0x1404u);   // a code on top of each half
+    o[i] = bf16x2_mul(bf16x2_mul(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), scales.x), scales.y);
+  }
+  // a code with all seven bits set is a NaN
+  if ((((w0 & 0x7F7F7F7Fu) + 0x01010101u) | ((w1 & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = w[i >> 1] >> (16 * (i & 1));
+      if ((c & 0x7Fu) == 0x7Fu) o[i] |= 0x7FFFu;
+      if ((c & 0x7F00u) == 0x7F00u) o[i] |= 0x7FFF0000u;
+    }
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// 2^(byte - 7) = 2^120 2^(byte - 127) as two bf16, each in both halves.
+__device__ __forceinline__ uint2 code_scales(uint32_t byte) {
+  const uint32_t a = byte >> 1, b = byte - a;   // exponents a - 3 and b - 4
+  return make_uint2(((a + 124u) << 7) * 0x10001u, ((b + 123u) << 7) * 0x10001u);
+}
+
+// 16 bytes to shared memory, asynchronously, around the L1.
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <class P>
@@ -135,8 +200,7 @@ constexpr bool kIsTree = std::is_same<P, WinTreeParams>::value;
 
 template <class P, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_window_attn(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_q,
-                  const __grid_constant__ CUtensorMap tm_out) {
+    k_window_attn(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_q) {
   constexpr bool kChunk = kIsChunk<P>, kTree = kIsTree<P>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* kv = smem + kKvOff;
@@ -148,22 +212,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int item0 = (int)((int64_t)n_items * blockIdx.x / gridDim.x);
   const int item1 = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
   const int W = p.w.swa, F = p.w.n_first;
+  // stages of Q: five of two boxes, or nine of one (the tensor core reads two
+  // boxes' rows from each, those behind the first are of no account)
+  const int boxes = H / 64 * (pair ? 2 : 1);
+  const uint32_t stages = boxes == 2 ? 5u : 9u, stage_bytes = (uint32_t)boxes * kBox;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
     }
-    mbar_init(&sm.kv_full, kChunk ? kLoadWarps : kRowWarps);
-    mbar_init(&sm.kv_empty, 1);
+    mbar_init(&sm.kv_full[0], kChunk ? kLoadWarps : kSoftWarps);
+    mbar_init(&sm.kv_full[1], kChunk ? kLoadWarps : kSoftWarps);
+    mbar_init(&sm.kv_empty[0], 1);
+    mbar_init(&sm.kv_empty[1], 1);
     mbar_init(&sm.s_full, 1);
     mbar_init(&sm.p_full, kSoftWarps);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, kSoftWarps);
+    mbar_init(&sm.tab_full, kLoadWarps);
     mbar_init(&sm.end, 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_out);
   }
   if (warp == 1) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
   tc_fence_before();
@@ -183,23 +253,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto piece = [&](int slot, int cb, int k) {
     return reinterpret_cast<uint4*>(kv + cb * kBlk + slot * 128 + ((k ^ (slot & 7)) << 4));
   };
+  // the newest block of 8 positions that an item sees
+  auto block_of = [&](int item) -> int64_t {
+    if constexpr (kChunk) return (p.pos0 + first_token(item) + tokens_of(item) - 1) >> 3;
+    else return 0;
+  };
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  bool ok = true;
 
   // ---------------------------------------------------------- rows, chunks
   // Ring block a holds the positions 8 g .. 8 g + 7 of the newest g = a mod 17
-  // that is not above g_hi; positions out of the band are zeros.
-  auto chunk_block_pos = [&](int64_t g_hi, int a) -> int64_t {
-    int64_t d = (g_hi - a) % kRing;
-    if (d < 0) d += kRing;
-    return 8 * (g_hi - d);
+  // that is not above g_hi (g_mod: g_hi mod 17); positions out of the band are
+  // zeros.
+  auto chunk_block_pos = [&](int64_t g_hi, int g_mod, int a) -> int64_t {
+    const int d = g_mod - a;
+    return 8 * (g_hi - (d < 0 ? d + kRing : d));
   };
   // A quarter of a block's rows (unit v of 4): four 16-byte pieces a lane, of
-  // row lane / 4.  kept in v[]; written by chunk_store.
-  auto chunk_load = [&](int64_t g_hi, int a, int v, uint4 (&x)[4]) {
+  // row lane / 4.  Kept in x[]; written by chunk_store.
+  auto chunk_load = [&](int64_t g_hi, int g_mod, int a, int v, uint4 (&x)[4]) {
     if constexpr (kChunk) {
       const int r = lane >> 2;
       const uint16_t* src = nullptr;
       if (a < kRing) {
-        const int64_t row = chunk_block_pos(g_hi, a) + r - p.band0;
+        const int64_t row = chunk_block_pos(g_hi, g_mod, a) + r - p.band0;
         if (row >= 0 && row < p.n_band) src = p.band + row * kHeadDim;
       } else if (r < F) {
         if (r >= p.band0) {
@@ -209,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[i] = src ? ldg_now_v4(src + 8 * (4 * (4 * v + i) + (lane & 3))) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 4; ++i) x[i] = src ? ldg_now_v4(src + 8 * (4 * (4 * v + i) + (lane & 3))) : zero;
     }
   };
   auto chunk_store = [&](int a, int v, const uint4 (&x)[4]) {
@@ -222,214 +298,303 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool b = not_finite(x[i]);
       bad |= b;
       // a probability of 0 times such a value would not be 0
-      *piece(slot, c >> 3, c & 7) = b ? make_uint4(0u, 0u, 0u, 0u) : x[i];
+      *piece(slot, c >> 3, c & 7) = b ? zero : x[i];
     }
     const uint32_t any = __ballot_sync(0xffffffffu, bad);
     const uint32_t rows = __ballot_sync(0xffffffffu, lane < 8 && ((any >> (4 * lane)) & 15u));
     if (lane == 0) sm.bad8[a][v] = (uint8_t)rows;
   };
+  // Which rows hold an infinity or a NaN: slots 32 word .. of the lanes.
+  auto chunk_bad = [&](int word) {
+    const int j = 32 * word + lane;
+    uint32_t q = 0;
+    if (j < kSlots) q = *reinterpret_cast<const uint32_t*>(sm.bad8[j >> 3]);
+    const bool b = ((q | (q >> 8) | (q >> 16) | (q >> 24)) >> (j & 7)) & 1u;
+    const uint32_t m = __ballot_sync(0xffffffffu, b);
+    if (lane == 0) sm.bad[word] = m;
+  };
 
   // ---------------------------------------------------------- rows, cache
-  // Ring row j holds position x, the one that is j mod W among the W newest up
-  // to `at`; first token f its own.  -1: none.
-  auto slot_pos = [&](int64_t at, int at_mod, int j) -> int64_t {
-    if (j < W) {
-      int d = at_mod - j;
-      if (d < 0) d += W;
-      const int64_t x = at - d;
-      return x >= F ? x : -1;
-    }
-    const int f = j - kFirstSlot;
-    return f >= 0 && f < F && f <= at ? f : -1;
-  };
   struct Query {
     int64_t at, pos0;   // its position; positions from pos0 on are drafts'
-    int32_t seq, draft0;
+    int64_t ring, first;   // the sequence's rows in the cache
+    int32_t draft0;
     int at_mod;
   };
   auto query_of = [&](int q) -> Query {
     Query t = {};
+    int32_t seq = 0;
     if constexpr (kTree) {
       const int tr = p.tree[q];
       t.pos0 = p.pos0[tr];
       t.at = t.pos0 + __popcll(p.path[q]) - 1;
-      t.seq = p.seq[tr];
       t.draft0 = p.first[tr];
+      seq = p.seq[tr];
     } else if constexpr (!kChunk) {
-      t.at = p.pos[q];
+      t.at = __ldg(p.pos + q);
       t.pos0 = INT64_MAX;
-      t.seq = p.identity ? p.seq0 + q : p.seq[q];
+      seq = p.identity ? p.seq0 + q : p.seq[q];
     }
     t.at_mod = t.at >= 0 ? (int)(t.at % W) : 0;
+    t.ring = (int64_t)seq * W;
+    t.first = (int64_t)p.w.n_seqs * W + (int64_t)seq * F;
     return t;
   };
-  // Row of the cache (>= 0) or of a draft (-2 - row) for slot j; -1: none.  A
-  // row of the cache counts only if it holds position x.
-  auto slot_row = [&](const Query& t, int j, int64_t& x) -> int64_t {
-    x = slot_pos(t.at, t.at_mod, j);
+  // What slot j takes (sm.slot).  Ring row j holds position x, the one that is j
+  // mod W among the W newest up to the query's; slot 128 + f first token f.  A row
+  // of the cache counts only if it holds that position.
+  auto slot_of = [&](const Query& t, int j) -> int {
+    int64_t x = -1, row = 0;
+    if (j < W) {
+      int d = t.at_mod - j;
+      if (d < 0) d += W;
+      x = t.at - d;
+      if (x < F) x = -1;
+      row = t.ring + j;
+    } else if (j >= kFirstSlot && j - kFirstSlot < F && j - kFirstSlot <= t.at) {
+      x = j - kFirstSlot;
+      row = t.first + x;
+    }
     if (x < 0) return -1;
-    if constexpr (kTree) {
-      if (x >= t.pos0) return -2 - (t.draft0 + (int64_t)sm.path[lw][x - t.pos0]);
-    }
-    return j < W ? (int64_t)t.seq * W + j : (int64_t)p.w.n_seqs * W + (int64_t)t.seq * F + x;
-  };
-  // All rows of an item: a warp takes 16 rows x 2 chunks at a time (32-byte
-  // pieces of 16 rows: every sector is read once and the swizzled stores have
-  // no conflicts), several of them in flight.
-  auto cache_load = [&](int item, int w0, int n_warps) {
-    if constexpr (!kChunk) {
-      const Query t = query_of(item);
-      constexpr int kPairs = kFp8 ? 18 : 32;       // chunk pairs of a row
-      constexpr int kUnits = kSlots / 16 * kPairs;
-      constexpr int kBatch = 7;
-      for (int u0 = w0; u0 < kUnits; u0 += kBatch * n_warps) {
-        uint4 d[kBatch];
-        uint32_t sb[kBatch];
-        int64_t tag[kBatch], want[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int u = u0 + b * n_warps;
-          d[b] = make_uint4(0u, 0u, 0u, 0u);
-          sb[b] = 0;
-          tag[b] = want[b] = 0;
-          if (u < kUnits) {
-            const int j = u / kPairs * 16 + (lane >> 1), c = u % kPairs * 2 + (lane & 1);
-            int64_t x;
-            int64_t row = slot_row(t, j, x);
-            if (row != -1) {
-              const uint16_t* rows = p.w.rows;
-              const uint8_t* codes = p.w.codes;
-              const uint16_t* rope = p.w.rope;
-              const uint8_t* scales = p.w.scales;
-              bool draft = false;
-              if constexpr (kTree) {
-                if (row < 0) {
-                  draft = true;
-                  row = -2 - row;
-                  rows = p.d.rows;
-                  codes = p.d.codes;
-                  rope = p.d.rope;
-                  scales = p.d.scales;
-                }
-              }
-              if (!draft) {
-                want[b] = x;
-                tag[b] = p.w.pos[row];
-              }
-              if constexpr (kFp8) {
-                if (c < 28) {
-                  d[b] = ldg_now_v4(codes + row * 448 + 16 * c);
-                  sb[b] = ldg_now_u8(scales + row * 8 + (c >> 2));
-                } else {
-                  d[b] = ldg_now_v4(rope + row * 64 + 8 * (c - 28));
-                }
-              } else {
-                d[b] = ldg_now_v4(rows + row * kHeadDim + 8 * c);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int u = u0 + b * n_warps;
-          if (u >= kUnits) break;
-          const int j = u / kPairs * 16 + (lane >> 1), c = u % kPairs * 2 + (lane & 1);
-          const bool held = tag[b] == want[b];
-          if constexpr (kFp8) {
-            if (c < 28) {
-              const float sc = held ? ue8m0_value(sb[b]) : 0.0f;
-              if (!held) d[b] = make_uint4(0u, 0u, 0u, 0u);
-              const int cb = c >> 2, k = 2 * (c & 3);
-              *piece(j, cb, k) = e4m3_piece(d[b].x, d[b].y, sc);
-              *piece(j, cb, k + 1) = e4m3_piece(d[b].z, d[b].w, sc);
-            } else {
-              *piece(j, 7, c - 28) = held ? d[b] : make_uint4(0u, 0u, 0u, 0u);
-            }
-          } else {
-            *piece(j, c >> 3, c & 7) = held ? d[b] : make_uint4(0u, 0u, 0u, 0u);
-          }
-        }
-      }
-    }
+    if (kTree && x >= t.pos0) return (int)(x - t.pos0);   // the path's draft of that depth
+    return p.w.pos[row] == x ? -2 : -1;
   };
 
-  // ---------------------------------------------------------- masks, rotation
-  // Rows that each token of an item sees (the two loading warps: slots 0-127,
-  // then 128-143 by the first), and the sines of the output rotation.
+  // Whether an item is a draft of the tree of the one before it, whose rows are
+  // still there.
+  auto same_tree = [&](int item) {
+    if constexpr (kTree) return item > item0 && p.tree[item] == p.tree[item - 1];
+    else return false;
+  };
+  // Tables of an item, by the two loading warps: the rows that each token sees
+  // (of a cache: what each slot takes), and its position.
   auto item_tables = [&](int item) {
     const int par = (item - item0) & 1;
     const int n_tok = tokens_of(item), t0 = first_token(item);
-    auto bits = [&](int j, int word) {
-      bool v0 = false, v1 = false, b = false;
-      if constexpr (kChunk) {
-        const int64_t at0 = p.pos0 + t0, hi = at0 + n_tok - 1;
+    int64_t at = 0;
+    if constexpr (kChunk) {
+      at = p.pos0 + t0;
+      const int64_t hi = at + n_tok - 1;
+      const int g_mod = (int)((hi >> 3) % kRing);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int word = 2 * k + lw, j = 32 * word + lane;
+        if (word > 4) break;
         int64_t x = -1;
         bool first = false;
         if (j < kChunkFirst) {
-          x = chunk_block_pos(hi >> 3, j >> 3) + (j & 7);
+          x = chunk_block_pos(hi >> 3, g_mod, j >> 3) + (j & 7);
           if (x < F || x < p.band0) x = -1;
-        } else {
+        } else if (j < kSlots) {
           first = true;
           x = j - kChunkFirst < F ? j - kChunkFirst : -1;
         }
-        v0 = x >= 0 && x <= at0 && (first || x > at0 - W);
-        v1 = n_tok > 1 && x >= 0 && x <= hi && (first || x > hi - W);
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(sm.bad8[j >> 3]);
-        b = ((q | (q >> 8) | (q >> 16) | (q >> 24)) >> (j & 7)) & 1u;
-      } else {
-        const Query t = query_of(item);
-        int64_t x;
-        const int64_t row = slot_row(t, j, x);
-        v0 = row < -1 || (row >= 0 && p.w.pos[row] == x);
+        const bool v0 = x >= 0 && x <= at && (first || x > at - W);
+        const bool v1 = n_tok > 1 && x >= 0 && x <= hi && (first || x > hi - W);
+        const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
+        if (lane == 0) {
+          sm.vis[par][0][word] = m0;
+          sm.vis[par][1][word] = m1;
+        }
       }
-      const uint32_t m0 = __ballot_sync(0xffffffffu, v0), m1 = __ballot_sync(0xffffffffu, v1);
-      const uint32_t mb = __ballot_sync(0xffffffffu, b);
-      if (lane == 0) {
-        sm.vis[0][word] = m0;
-        sm.vis[1][word] = m1;
-        sm.bad[word] = mb;
+    } else {
+      const Query t = query_of(item);
+      at = t.at;
+      if constexpr (kTree) {
+        const uint64_t path = p.path[item];
+        if (lw == 0)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int b = lane + 32 * h;
+            if ((path >> b) & 1ull) sm.draft[par][__popcll(path & ((1ull << b) - 1ull))] = (uint8_t)b;
+          }
       }
-    };
-    bits(64 * lw + lane, 2 * lw);
-    bits(64 * lw + 32 + lane, 2 * lw + 1);
-    if (lw == 0) bits(128 + (lane & 15), 4);
-    if (p.rope_out) {
-      const int tk = lw;
-      if (tk < n_tok) {
-        int64_t at;
-        if constexpr (kChunk) at = p.pos0 + t0 + tk;
-        else at = query_of(item).at;
-        const uint64_t turn = (uint64_t)(-at) * p.turns[lane];
-        float sn, cs;
-        sincospif((float)(int64_t)turn * 0x1p-63f, &sn, &cs);
-        sm.rope[par][tk][lane] = make_float2(cs, sn);
+      int v[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {   // the tags' loads together
+        const int j = 32 * (2 * k + lw) + lane;
+        v[k] = j < kSlots ? slot_of(t, j) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int word = 2 * k + lw, j = 32 * word + lane;
+        if (word > 4) break;
+        if (j < kSlots) sm.slot[par][j] = (int8_t)v[k];
+        const uint32_t m = __ballot_sync(0xffffffffu, v[k] != -1);
+        if (lane == 0) sm.vis[par][0][word] = m;
+      }
+      if constexpr (kTree) {
+        ok = named_bar_and(3, 32 * kLoadWarps, ok);   // both warps' halves
+        if (lw == 1) {
+          const bool same = same_tree(item);
+          int n = 0;
+          for (int j = lane; j < 160; j += 32) {
+            bool put = false;
+            if (j < kSlots) {
+              const int now = sm.slot[par][j], old = sm.slot[par ^ 1][j];
+              put = same ? now != old || (now >= 0 && sm.draft[par][now] != sm.draft[par ^ 1][now])
+                         : now >= 0;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, put);
+            if (put) sm.list[par][n + __popc(m & ((1u << lane) - 1u))] = (uint8_t)j;
+            n += __popc(m);
+          }
+          if (lane == 0) sm.n_list[par] = n;
+        }
       }
     }
+    if (lw == 0 && lane == 0) sm.at[par] = at;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.tab_full);
   };
-  auto tree_path = [&](int item) {
-    if constexpr (kTree) {
-      const uint64_t path = p.path[item];
-      __syncwarp();
+  // Rows of an item out of the cache, by the softmax warps: warp w has channels
+  // 64 w .. 64 w + 63 of all rows, 8 rows x 4 pieces of 16 bytes at a time (whole
+  // sectors, and stores without conflicts).  bf16 pieces go straight to their
+  // places; codes go to the first halves of their rows' places, from where the
+  // warp that has brought them takes them again.  Loops, not straight code: most
+  // CTAs come here once, and unrolled it was the fetching of instructions that
+  // took the time.
+  auto cache_rows = [&](int item) {
+    if constexpr (!kChunk) {
+      const uint32_t k = (uint32_t)(item - item0);
+      const int par = k & 1, cb = warp - 4;
+      const Query t = query_of(item);
+      constexpr int kGroups = 17;                        // of 8 slots
+      const int r8 = lane >> 2, c4 = lane & 3;
+      const bool codes = kFp8 && cb < 7;
+      uint8_t* const mine = kv + cb * kBlk + r8 * 128;   // this lane's row of group 0
+      const bool same = same_tree(item);
+      uint32_t sc[5] = {0u, 0u, 0u, 0u, 0u};             // of slots lane + 32 i
+      if (k > 0) ok = mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err) && ok;
+      if (!same) {
+        if (codes) {
+          const uint8_t* src = p.w.codes + (t.ring + r8) * 448 + 64 * cb + 16 * c4;
+#pragma unroll 1
+          for (int j = r8, g = 0; g < 16; ++g, j += 8, src += 8 * 448)
+            if (j < W) copy_async(mine + g * 1024 + 16 * c4, src);
+          if (r8 < F)
+            copy_async(mine + 16 * 1024 + 16 * c4, p.w.codes + (t.first + r8) * 448 + 64 * cb + 16 * c4);
 #pragma unroll
-      for (int b = lane; b < 64; b += 32)
-        if ((path >> b) & 1ull) sm.path[lw][__popcll(path & ((1ull << b) - 1ull))] = (uint8_t)b;
+          for (int i = 0; i < 5; ++i) {
+            const int j = lane + 32 * i;
+            if (i < 4 ? j < W : lane < F)
+              sc[i] = ldg_now_u8(p.w.scales + (i < 4 ? t.ring + j : t.first + lane) * 8 + cb);
+          }
+        } else {
+          const int64_t step = kFp8 ? 64 : kHeadDim;
+          const uint16_t* base = kFp8 ? p.w.rope + 8 * c4 : p.w.rows + 64 * cb + 8 * c4;
+          const uint16_t* src = base + (t.ring + r8) * step;
+#pragma unroll 1
+          for (int j = r8, g = 0; g < kGroups; ++g, j += 8, src += 8 * step) {
+            if (g == 16) src = base + (t.first + r8) * step;
+            if (g < 16 ? j < W : r8 < F) {
+              copy_async(mine + g * 1024 + ((c4 ^ r8) << 4), src);
+              copy_async(mine + g * 1024 + (((4 + c4) ^ r8) << 4), src + 32);
+            }
+          }
+        }
+      }
+      ok = mbar_wait(&sm.tab_full, par, err) && ok;
+      if (!same) {
+        copy_async_wait();
+        __syncwarp();
+        if (codes) {
+#pragma unroll 1
+          for (int i = 0; i < 5; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int g = 4 * i + e;
+              if (g >= kGroups) break;
+              const uint32_t byte = __shfl_sync(0xffffffffu, sc[0], 8 * e + r8);
+              uint8_t* row = mine + g * 1024;
+              const bool there = sm.slot[par][8 * g + r8] == -2;
+              const uint4 v = there ? *reinterpret_cast<const uint4*>(row + 16 * c4) : zero;
+              const uint2 f = code_scales(byte);
+              const uint4 lo = e4m3_piece(v.x, v.y, f), hi = e4m3_piece(v.z, v.w, f);
+              __syncwarp();
+              *reinterpret_cast<uint4*>(row + (((2 * c4) ^ r8) << 4)) = lo;
+              *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ r8) << 4)) = hi;
+            }
+            sc[0] = sc[1];
+            sc[1] = sc[2];
+            sc[2] = sc[3];
+            sc[3] = sc[4];
+          }
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g)
+            if (sm.slot[par][8 * g + r8] != -2) {
+              *reinterpret_cast<uint4*>(mine + g * 1024 + ((c4 ^ r8) << 4)) = zero;
+              *reinterpret_cast<uint4*>(mine + g * 1024 + (((4 + c4) ^ r8) << 4)) = zero;
+            }
+        }
+      }
+      if constexpr (kTree) {
+        // drafts' rows, and what takes the places of the last path's, four groups
+        // in flight
+        __syncwarp();
+        const int n = sm.n_list[par];
+#pragma unroll 1
+        for (int g0 = 0; g0 < n; g0 += 32) {
+          uint4 d[4], e[4];
+          uint32_t byte[4];
+          int slot[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = g0 + 8 * i + r8;
+            slot[i] = -1;
+            d[i] = e[i] = zero;
+            byte[i] = 0u;
+            if (at >= n) continue;
+            slot[i] = sm.list[par][at];
+            const int what = sm.slot[par][slot[i]];
+            if (what == -1) continue;
+            const WinDrafts& x = p.d;
+            const int64_t row = what >= 0 ? (int64_t)t.draft0 + sm.draft[par][what]
+                                : slot[i] < W ? t.ring + slot[i] : t.first + slot[i] - kFirstSlot;
+            if (codes) {
+              d[i] = ldg_now_v4((what >= 0 ? x.codes : p.w.codes) + row * 448 + 64 * cb + 16 * c4);
+              byte[i] = ldg_now_u8((what >= 0 ? x.scales : p.w.scales) + row * 8 + cb);
+            } else {
+              const uint16_t* src = kFp8 ? (what >= 0 ? x.rope : p.w.rope) + row * 64
+                                         : (what >= 0 ? x.rows : p.w.rows) + row * kHeadDim + 64 * cb;
+              d[i] = ldg_now_v4(src + 8 * c4);
+              e[i] = ldg_now_v4(src + 32 + 8 * c4);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (slot[i] < 0) continue;
+            if (codes) {
+              const uint2 f = code_scales(byte[i]);
+              *piece(slot[i], cb, 2 * c4) = e4m3_piece(d[i].x, d[i].y, f);
+              *piece(slot[i], cb, 2 * c4 + 1) = e4m3_piece(d[i].z, d[i].w, f);
+            } else {
+              *piece(slot[i], cb, c4) = d[i];
+              *piece(slot[i], cb, 4 + c4) = e[i];
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.kv_full[par]);
     }
   };
 
-  bool ok = true;
   if constexpr (kChunk) {
     // the first item's whole window: 18 blocks in quarters over the ten
     // loading and softmax warps, four quarters in flight
     if ((loader || soft) && item0 < item1) {
-      const int64_t hi = p.pos0 + first_token(item0) + tokens_of(item0) - 1;
+      const int64_t g = (p.pos0 + first_token(item0) + tokens_of(item0) - 1) >> 3;
+      const int g_mod = (int)(g % kRing);
       constexpr int kJobs = (kRing + 1) * 4, kBatch = 4;
       for (int j0 = lw; j0 < kJobs; j0 += kBatch * kRowWarps) {
         uint4 x[kBatch][4];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
           const int j = j0 + b * kRowWarps;
-          if (j < kJobs) chunk_load(hi >> 3, j >> 2, j & 3, x[b]);
+          if (j < kJobs) chunk_load(g, g_mod, j >> 2, j & 3, x[b]);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -439,30 +604,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
     }
-    __syncthreads();
+  } else if (warp >= 2) {
+    // slots that no row ever takes: read by the products all the same
+    for (int i = tid - 64; i < 8 * 8 * 8; i += kThreads - 64)
+      *piece(kSlots - 8 + (i & 7), (i >> 3) & 7, i >> 6) = zero;
+    fence_proxy_async_smem();
   }
+  __syncthreads();
 
   if (warp == 0) {
     // ------------------------------------------------------------ Q
     if (lane == 0) {
       uint32_t n = 0;
       for (int item = item0; item < item1 && ok; ++item) {
-        const int boxes = tokens_of(item) * H / 64;
+        const int now = tokens_of(item) * H / 64;   // boxes of the item: the last may have one
         const int32_t row = first_token(item) * H;
         for (int cb = 0; cb < 8 && ok; ++cb, ++n) {
-          const uint32_t s = n % kStages, use = n / kStages;
+          const uint32_t s = n % stages, use = n / stages;
           if (use > 0) ok = mbar_wait(&sm.q_empty[s], (use - 1) & 1, err);
           if (!ok) break;
-          mbar_arrive_expect_tx(&sm.q_full[s], boxes * 8192);
-          uint8_t* dst = smem + kQOff + s * kStageBytes;
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(dst + b * 8192, &tm_q, 64 * cb, row + 64 * b, &sm.q_full[s]);
+          mbar_arrive_expect_tx(&sm.q_full[s], now * kBox);
+          uint8_t* dst = smem + kQOff + s * stage_bytes;
+          for (int b = 0; b < now; ++b)
+            tma_load_2d(dst + b * kBox, &tm_q, 64 * cb, row + 64 * b, &sm.q_full[s]);
         }
       }
       // the copies in flight must land before the CTA exits
       if (!ok)
-        for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k)
-          mbar_wait(&sm.q_full[k % kStages], (k / kStages) & 1, err, drain_limit(0));
+        for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
+          mbar_wait(&sm.q_full[k % stages], (k / stages) & 1, err, drain_limit(0));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -473,32 +643,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t d_k = sdesc_sw128(smem_u32(kv), 16, 1024);
       const uint64_t d_v = sdesc_sw128(smem_u32(kv), kBlk, 1024);
       uint32_t n = 0, chunk = 0;
-      for (int item = item0; item < item1 && ok; ++item) {
-        const uint32_t ph = (uint32_t)(item - item0) & 1u;
-        ok = mbar_wait(&sm.kv_full, ph, err);
-        for (int cb = 0; cb < 8 && ok; ++cb, ++n) {
-          const uint32_t s = n % kStages;
-          ok = mbar_wait(&sm.q_full[s], (n / kStages) & 1, err);
+      // channel blocks c0 .. c1 - 1 of an item's S
+      auto issue_s = [&](int item, int c0, int c1) {
+        const uint32_t j = (uint32_t)(item - item0);
+        if (c0 == 0) ok = mbar_wait(&sm.kv_full[j & 1], (j >> 1) & 1, err);
+        for (int cb = c0; cb < c1 && ok; ++cb, ++n) {
+          const uint32_t s = n % stages;
+          ok = mbar_wait(&sm.q_full[s], (n / stages) & 1, err);
           if (!ok) break;
           tc_fence_after();
           for (int k = 0; k < 4; ++k)
-            umma_bf16(tmem + kSCol, d_q + ((s * kStageBytes + 32 * k) >> 4),
+            umma_bf16(tmem + kSCol, d_q + ((s * stage_bytes + 32 * k) >> 4),
                       d_k + ((cb * kBlk + 32 * k) >> 4), id_s, (cb | k) ? 1u : 0u);
           umma_commit(&sm.q_empty[s]);
         }
-        if (!ok) break;
-        umma_commit(&sm.s_full);
-        ok = mbar_wait(&sm.p_full, ph, err);
-        for (int h = 0; h < 2 && ok; ++h, ++chunk) {
-          if (chunk > 0) ok = mbar_wait(&sm.o_empty, (chunk - 1) & 1, err);
-          if (!ok) break;
-          tc_fence_after();
-          for (int ks = 0; ks < kSlots / 16; ++ks)
-            umma_bf16_ts(tmem + kOCol, tmem + kPCol + 8 * ks,
-                         d_v + ((4 * h * kBlk + ks * 2048) >> 4), id_o, ks ? 1u : 0u);
-          umma_commit(&sm.o_full);
+        if (ok && c1 == 8) umma_commit(&sm.s_full);
+      };
+      auto issue_o = [&](int h) {
+        if (chunk > 0) ok = mbar_wait(&sm.o_empty, (chunk - 1) & 1, err);
+        if (!ok) return;
+        tc_fence_after();
+        for (int ks = 0; ks < kSlots / 16; ++ks)
+          umma_bf16_ts(tmem + kOCol, tmem + kPCol + 8 * ks, d_v + ((4 * h * kBlk + ks * 2048) >> 4),
+                       id_o, ks ? 1u : 0u);
+        umma_commit(&sm.o_full);
+        ++chunk;
+      };
+      if (item0 < item1) issue_s(item0, 0, 8);
+      for (int item = item0; item < item1 && ok; ++item) {
+        const uint32_t k = (uint32_t)(item - item0);
+        ok = mbar_wait(&sm.p_full, k & 1, err);
+        if (ok) issue_o(0);
+        // half of the next S while the outputs' first half is read out, where the
+        // rows stay as they are
+        int c0 = 0;
+        if constexpr (kChunk) {
+          if (ok && item + 1 < item1 && block_of(item + 1) == block_of(item)) {
+            issue_s(item + 1, 0, 4);
+            c0 = 4;
+          }
         }
-        if (ok) umma_commit(&sm.kv_empty);
+        if (ok) issue_o(1);
+        if (ok) umma_commit(&sm.kv_empty[k & 1]);
+        if (ok && item + 1 < item1) issue_s(item + 1, c0, 8);
       }
       if (!ok) {   // the MMAs issued so far must end before the CTA exits
         umma_commit(&sm.end);
@@ -506,62 +693,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (loader) {
-    // ------------------------------------------------------------ rows
+    // ------------------------------------------------------------ rows, tables
     int64_t g_have = 0;
     for (int item = item0; item < item1 && ok; ++item) {
       const uint32_t k = (uint32_t)(item - item0);
       if constexpr (kChunk) {
-        const int64_t g = (p.pos0 + first_token(item) + tokens_of(item) - 1) >> 3;
+        const int64_t g = block_of(item);
+        const int a = (int)(g % kRing);
         // at most one new block an item (of at most two tokens)
         const bool fresh = k > 0 && g != g_have;
         g_have = g;
         uint4 x[2][4];
-        const int a = (int)(g % kRing);
         if (fresh) {
-          chunk_load(g, a, 2 * lw, x[0]);
-          chunk_load(g, a, 2 * lw + 1, x[1]);
+          chunk_load(g, a, a, 2 * lw, x[0]);
+          chunk_load(g, a, a, 2 * lw + 1, x[1]);
         }
-        if (k > 0) ok = mbar_wait_sleep(&sm.kv_empty, (k - 1) & 1, err);
-        if (fresh && ok) {
-          chunk_store(a, 2 * lw, x[0]);
-          chunk_store(a, 2 * lw + 1, x[1]);
+        // the tables' place was that of the item before the last one; the rows'
+        // is needed where one comes in
+        if (k > 1) ok = mbar_wait_sleep(&sm.kv_empty[k & 1], ((k - 2) >> 1) & 1, err);
+        item_tables(item);
+        if (fresh) {
+          ok = mbar_wait_sleep(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
+          if (ok) {
+            chunk_store(a, 2 * lw, x[0]);
+            chunk_store(a, 2 * lw + 1, x[1]);
+          }
         }
         ok = named_bar_and(3, 32 * kLoadWarps, ok);
         if (!ok) break;
-        item_tables(item);
+        if (fresh || k == 0) {
+          chunk_bad(lw);
+          chunk_bad(2 + lw);
+          if (lw == 0) chunk_bad(4);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.kv_full[k & 1]);
       } else {
-        if (k > 0) ok = mbar_wait_sleep(&sm.kv_empty, (k - 1) & 1, err);
-        if (!ok) break;
-        tree_path(item);
-        cache_load(item, lw, kRowWarps);
+        // not before all warps have the last item's: a wait tells neighbouring
+        // phases apart only
+        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1], ((k - 1) >> 1) & 1, err);
         item_tables(item);
+        if (!ok) break;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kv_full);
     }
   } else if (soft) {
     // ------------------------------------------------------------ softmax, outputs
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const bool issuer = quad == 0 && lane == 0;   // of the half's copies out
-    uint8_t* stage = smem + kOutOff + half * kStageBytes;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     uint32_t chunk = 0;
     for (int item = item0; item < item1; ++item) {
       const uint32_t k = (uint32_t)(item - item0), ph = k & 1u;
-      if constexpr (!kChunk) {
-        if (k > 0) ok = mbar_wait(&sm.kv_empty, (k - 1) & 1, err) && ok;
-        tree_path(item);
-        cache_load(item, lw, kRowWarps);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.kv_full);
-      }
+      // (its last products are done: their outputs are stored)
+      if constexpr (!kChunk) cache_rows(item);
       const int n_rows = tokens_of(item) * H;
       const bool live = quad * 32 < n_rows;       // of the warp's rows, all or none
       const int tk = pair ? row >> 6 : 0;
-      ok = mbar_wait(&sm.kv_full, ph, err) && ok;
+      ok = mbar_wait(&sm.kv_full[ph], (k >> 1) & 1, err) && ok;
       ok = mbar_wait(&sm.s_full, ph, err) && ok;
       ok = named_bar_and(1, 32 * kSoftWarps, ok);
       if (!ok) break;
@@ -580,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 5; ++g) {
           if (g < ng) {
-            const uint32_t v = sm.vis[tk][(g0 + g) >> 1] >> (16 * ((g0 + g) & 1));
+            const uint32_t v = sm.vis[ph][tk][(g0 + g) >> 1] >> (16 * ((g0 + g) & 1));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float x = (v >> i) & 1u ? __uint_as_float(s[g][i]) * p.scale_log2 : -INFINITY;
@@ -600,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kChunk) {   // before the next item's masks may come
           uint32_t b = 0;
 #pragma unroll
-          for (int i = 0; i < 5; ++i) b |= sm.vis[tk][i] & sm.bad[i];
+          for (int i = 0; i < 5; ++i) b |= sm.vis[ph][tk][i] & sm.bad[i];
           bad = b != 0;
         }
         const float m0 = m == -INFINITY ? 0.0f : m;
@@ -625,6 +815,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full);
+      if (p.rope_out && half == 1 && (quad & 1) == 0) {
+        // sines of the output rotation, by warps with fewer columns: of token
+        // quad / 2 (all have left the item before this one)
+        const uint64_t turn = (uint64_t)(-(sm.at[ph] + (quad >> 1))) * p.turns[lane];
+        float sn, cs;
+        sincospif((float)(int64_t)turn * 0x1p-63f, &sn, &cs);
+        sm.rope[quad >> 1][lane] = make_float2(cs, sn);
+      }
       named_bar(1, 32 * kSoftWarps);
       float inv = 0.0f;
       if (live) {
@@ -642,30 +840,35 @@ __global__ void __launch_bounds__(kThreads, 1)
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
                                : (M + log2f(L)) * 0.69314718055994531f;
       }
-      const int32_t out_row = first_token(item) * H;
+      // outputs, 32 rows x 64 channels at a time
+      uint16_t* out = p.out + ((int64_t)first_token(item) * H + 32 * quad) * kHeadDim;
       for (int h = 0; h < 2; ++h, ++chunk) {
         ok = mbar_wait(&sm.o_full, chunk & 1, err) && ok;
         tc_fence_after();
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
-          const int cb = 2 * half + b;            // 64-channel block of the half
+          const int c = 128 * half + 64 * b;      // column of the half
           uint32_t w[32];
           if (live) {
+            const bool turn = p.rope_out && h == 1 && c == 192;
+            uint32_t r[2][32];
+            tmem_ld32x2(tmem + lanes + kOCol + c, tmem + lanes + kOCol + c + 32, r[0], r[1]);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t r[32];
-              tmem_ld32(tmem + lanes + kOCol + 64 * cb + 32 * g, r);
+            for (int i = 0; i < 32; ++i) {
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(__uint_as_float(r[i >> 4][(2 * i) & 31]) * inv,
+                                        __uint_as_float(r[i >> 4][(2 * i + 1) & 31]) * inv);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            if (turn) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a = __uint_as_float(r[2 * i]) * inv, c = __uint_as_float(r[2 * i + 1]) * inv;
-                if (p.rope_out && h == 1 && cb == 3) {
-                  const float2 t = sm.rope[ph][tk][16 * g + i];
-                  const float a2 = fmaf(a, t.x, -(c * t.y));
-                  c = fmaf(a, t.y, c * t.x);
-                  a = a2;
-                }
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, c);
-                w[16 * g + i] = *reinterpret_cast<const uint32_t*>(&b2);
+              for (int i = 0; i < 32; ++i) {
+                const float x = __uint_as_float(r[i >> 4][(2 * i) & 31]) * inv;
+                const float y = __uint_as_float(r[i >> 4][(2 * i + 1) & 31]) * inv;
+                const float2 t = sm.rope[tk][i];
+                const __nv_bfloat162 b2 =
+                    __floats2bfloat162_rn(fmaf(x, t.x, -(y * t.y)), fmaf(x, t.y, y * t.x));
+                w[i] = *reinterpret_cast<const uint32_t*>(&b2);
               }
             }
           }
@@ -674,24 +877,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_empty);
           }
-          if (issuer) bulk_wait_read();
-          named_bar(4 + half, 16 * kSoftWarps);
-          if (live) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4)) =
-                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-          }
-          fence_proxy_async_smem();
-          named_bar(4 + half, 16 * kSoftWarps);
-          if (issuer && ok) {
-            for (int i = 0; i < n_rows / 64; ++i)
-              tma_store_2d(&tm_out, stage + 8192 * i, 64 * (4 * h + cb), out_row + 64 * i);
-          }
+          if (live && ok) store_rows(out + 256 * h + c, kHeadDim, w, lane, wide);
         }
       }
     }
-    if (issuer) bulk_wait_read();
   }
   tc_fence_before();
   __syncthreads();
@@ -702,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <class P, bool kFp8>
-cudaError_t launch(const P& p, const CUtensorMap& q, const CUtensorMap& out, int items, int sms,
+cudaError_t launch(const P& p, const CUtensorMap& q, int items, int sms,
                    cudaStream_t s) {
   if (items <= 0) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(
@@ -716,26 +905,23 @@ cudaError_t launch(const P& p, const CUtensorMap& q, const CUtensorMap& out, int
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_window_attn<P, kFp8>, p, q, out);
+  return cudaLaunchKernelEx(&cfg, k_window_attn<P, kFp8>, p, q);
 }
 
 }  // namespace
 
-cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q,
-                                 const CUtensorMap& out, int sms, cudaStream_t s) {
-  return p.w.fp8 ? launch<WinDecodeParams, true>(p, q, out, p.nq, sms, s)
-                 : launch<WinDecodeParams, false>(p, q, out, p.nq, sms, s);
+cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
+  return p.w.fp8 ? launch<WinDecodeParams, true>(p, q, p.nq, sms, s)
+                 : launch<WinDecodeParams, false>(p, q, p.nq, sms, s);
 }
 
-cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q,
-                               const CUtensorMap& out, int sms, cudaStream_t s) {
-  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, out, p.nq, sms, s)
-                 : launch<WinTreeParams, false>(p, q, out, p.nq, sms, s);
+cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
+  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, p.nq, sms, s)
+                 : launch<WinTreeParams, false>(p, q, p.nq, sms, s);
 }
 
-cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q,
-                                  const CUtensorMap& out, int sms, cudaStream_t s) {
-  return launch<WinPrefillParams, false>(p, q, out, p.n_heads == 64 ? (p.nq + 1) / 2 : p.nq, sms, s);
+cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
+  return launch<WinPrefillParams, false>(p, q, p.n_heads == 64 ? (p.nq + 1) / 2 : p.nq, sms, s);
 }
 
 }  // namespace csa2

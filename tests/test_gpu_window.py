@@ -273,6 +273,22 @@ def test_rows_that_are_not_held_are_not_seen():
         assert not out.any()
 
 
+def test_nan_in_8_bits():
+    """A row that held a NaN keeps it (the code of all ones, of either sign)."""
+    c = C()
+    win = c.Window(2, 128)
+    rows = make_rows(40, 1)
+    rows[30, 64 * 3 + 5] = math.nan
+    rows[31, 447] = -math.nan
+    rounded = torch.empty_like(rows)
+    c.csa2_window_append(win, rows, dev64([0, 0]), [20, 20], rounded=rounded)
+    assert rounded[30].isnan().sum() == 1 and rounded[31].isnan().sum() == 1
+    q = make_q(2, 64, 2)
+    out = c.csa2_window_attn_decode(win, q, dev64([19, 19]), SCALE)
+    check(out[0], None, attend(q[0], round8(rows[:20])))
+    assert out[1].isnan().all()
+
+
 def test_values_that_are_not_finite():
     """A NaN or an infinity of a query's own stays with that query."""
     c = C()
@@ -413,6 +429,24 @@ def test_chunk(heads, swa, n_first, pos0, n):
         if first is not None:
             kv = [first[f] for f in range(min(n_first, band0))] + kv
         check(out[i], lse[i], attend(q[i], torch.stack(kv).double(), sink=sink, at=p if rope else None))
+
+
+@pytest.mark.parametrize("heads,n", [(64, 6001), (128, 2000)])
+def test_long_chunk(heads, n):
+    """Many items a CTA: bit for bit what short chunks over the same rows give."""
+    c = C()
+    rows, q = make_rows(n + 100, 1), make_q(n, heads, 2)
+    first = make_rows(4, 3)
+    whole = c.csa2_window_attn_prefill(q, 1100, rows, 1000, SCALE, 90, 4, first)
+    for a in range(0, n, 200):
+        b = min(n, a + 200)
+        back = min(89, a + 100)
+        part = c.csa2_window_attn_prefill(q[a:b], 1100 + a, rows[a + 100 - back:b + 100],
+                                          1100 + a - back, SCALE, 90, 4, first)
+        assert torch.equal(part, whole[a:b]), a
+    for i in (0, 1, n // 2, n - 1):
+        kv = torch.cat([first, rows[max(0, i + 11):i + 101]]).double()
+        check(whole[i], None, attend(q[i], kv))
 
 
 @pytest.mark.parametrize("fp8", [True, False])
