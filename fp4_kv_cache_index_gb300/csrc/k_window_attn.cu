@@ -41,14 +41,16 @@ constexpr int kFirstSlot = 8 * 16;      // first tokens, decode and trees
 constexpr int kChunkFirst = 8 * kRing;  // first tokens, chunks
 constexpr int kBlk = kSlots * 128;      // bytes of a 64-channel block of rows
 constexpr int kBox = 64 * 128;          // Q: 64 rows x 64 channels
-constexpr int kQBytes = 10 * kBox;      // a stage is a box or two, in turn
-constexpr int kMaxStages = 9;
+constexpr int kQBytes = 8 * kBox;       // a stage is a box or two, in turn
+constexpr int kMaxStages = 8;
+constexpr int kOutBox = 32 * 64;        // outputs: 32 rows x 32 channels
 constexpr int kLoadWarps = 2, kSoftWarps = 8;
 constexpr int kRowWarps = kLoadWarps + kSoftWarps;
 
 constexpr int kKvOff = 0;
 constexpr int kQOff = kKvOff + 8 * kBlk;
-constexpr int kSmallOff = kQOff + kQBytes;
+constexpr int kOutOff = kQOff + kQBytes;              // a box for each softmax warp
+constexpr int kSmallOff = kOutOff + kSoftWarps * kOutBox;
 struct Small {
   float red[2][128];            // [half of the columns][row]: maxima, then sums
   float2 rope[2][32];           // [token]: cos, sin of each channel pair
@@ -85,52 +87,35 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// 32 columns, the wait apart (see tmem_ld16_issue).
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%"
+      "14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
-}
-
-// A warp's 32 rows (a lane each) of 32 words to memory, in whole 128-byte lines:
-// four neighbouring lanes exchange their rows' quarters, after which lane j of
-// them has quarter j of all four rows.  (A lane storing its own row touches 32
-// lines an instruction, which took the store path 3400 cycles for 64 KB.)
-__device__ __forceinline__ void store_rows(uint16_t* rows, int64_t stride, uint32_t (&w)[32], int lane,
-                                           bool wide) {
-  const bool b1 = lane & 2, b0 = lane & 1;
-  uint32_t a[2][16];   // two quarters of row (lane & ~2) and of row (lane | 2)
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t keep = b1 ? w[i + 16] : w[i], give = b1 ? w[i] : w[i + 16];
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 2);
-    a[0][i] = b1 ? got : keep;
-    a[1][i] = b1 ? keep : got;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t o[2][8];  // a quarter of row (lane & ~1) and of row (lane | 1) of those
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t keep = b0 ? a[h][i + 8] : a[h][i], give = b0 ? a[h][i] : a[h][i + 8];
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-      o[0][i] = b0 ? got : keep;
-      o[1][i] = b0 ? keep : got;
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint16_t* to = rows + ((lane & ~3) + 2 * h + r) * stride + 16 * (lane & 3);
-      if (wide)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(o[r][0]),
-                     "r"(o[r][1]), "r"(o[r][2]), "r"(o[r][3]), "r"(o[r][4]), "r"(o[r][5]),
-                     "r"(o[r][6]), "r"(o[r][7])
-                     : "memory");
-      else {
-        reinterpret_cast<uint4*>(to)[0] = make_uint4(o[r][0], o[r][1], o[r][2], o[r][3]);
-        reinterpret_cast<uint4*>(to)[1] = make_uint4(o[r][4], o[r][5], o[r][6], o[r][7]);
-      }
-    }
-  }
 }
 
 __device__ __forceinline__ void named_bar(int id, int threads) {
@@ -212,10 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int item0 = (int)((int64_t)n_items * blockIdx.x / gridDim.x);
   const int item1 = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
   const int W = p.w.swa, F = p.w.n_first;
-  // stages of Q: five of two boxes, or nine of one (the tensor core reads two
+  // stages of Q: four of two boxes, or eight of one (the tensor core reads two
   // boxes' rows from each, those behind the first are of no account)
   const int boxes = H / 64 * (pair ? 2 : 1);
-  const uint32_t stages = boxes == 2 ? 5u : 9u, stage_bytes = (uint32_t)boxes * kBox;
+  const uint32_t stages = boxes == 2 ? 4u : 8u, stage_bytes = (uint32_t)boxes * kBox;
 
   if (tid == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -742,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+    uint8_t* const box = smem + kOutOff + (warp - 4) * kOutBox;
     uint32_t chunk = 0;
     for (int item = item0; item < item1; ++item) {
       const uint32_t k = (uint32_t)(item - item0), ph = k & 1u;
@@ -753,8 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tk = pair ? row >> 6 : 0;
       ok = mbar_wait(&sm.kv_full[ph], (k >> 1) & 1, err) && ok;
       ok = mbar_wait(&sm.s_full, ph, err) && ok;
-      ok = named_bar_and(1, 32 * kSoftWarps, ok);
-      if (!ok) break;
       tc_fence_after();
       // a thread has a half of its row: columns 0-79 or 80-143
       const int g0 = half ? 5 : 0, ng = half ? 4 : 5;
@@ -781,7 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         sm.red[half][row] = m;
       }
-      named_bar(1, 32 * kSoftWarps);
+      // (all of them leave together where a wait ran out)
+      ok = named_bar_and(1, 32 * kSoftWarps, ok);
+      if (!ok) break;
       if (live) m = fmaxf(m, sm.red[half ^ 1][row]);
       named_bar(1, 32 * kSoftWarps);
       float sum = 0.0f;
@@ -840,44 +825,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
                                : (M + log2f(L)) * 0.69314718055994531f;
       }
-      // outputs, 32 rows x 64 channels at a time
-      uint16_t* out = p.out + ((int64_t)first_token(item) * H + 32 * quad) * kHeadDim;
+      // outputs, 32 rows x 32 channels at a time: rounded, turned in the warp's own
+      // box so that four lanes have 64 bytes of a row (a lane that stores its own
+      // row touches 32 lines an instruction), the next ones on their way
+      uint16_t* out = p.out + ((int64_t)first_token(item) * H + 32 * quad + (lane >> 2)) * kHeadDim + 8 * (lane & 3);
       for (int h = 0; h < 2; ++h, ++chunk) {
         ok = mbar_wait(&sm.o_full, chunk & 1, err) && ok;
         tc_fence_after();
-#pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          const int c = 128 * half + 64 * b;      // column of the half
-          uint32_t w[32];
-          if (live) {
-            const bool turn = p.rope_out && h == 1 && c == 192;
-            uint32_t r[2][32];
-            tmem_ld32x2(tmem + lanes + kOCol + c, tmem + lanes + kOCol + c + 32, r[0], r[1]);
+        const uint32_t from = tmem + lanes + kOCol + 128 * half;
+        uint32_t r[2][32];
+        if (live) tmem_ld32_issue(from, r[0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const __nv_bfloat162 b2 =
-                  __floats2bfloat162_rn(__uint_as_float(r[i >> 4][(2 * i) & 31]) * inv,
-                                        __uint_as_float(r[i >> 4][(2 * i + 1) & 31]) * inv);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            if (turn) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = __uint_as_float(r[i >> 4][(2 * i) & 31]) * inv;
-                const float y = __uint_as_float(r[i >> 4][(2 * i + 1) & 31]) * inv;
-                const float2 t = sm.rope[tk][i];
-                const __nv_bfloat162 b2 =
-                    __floats2bfloat162_rn(fmaf(x, t.x, -(y * t.y)), fmaf(x, t.y, y * t.x));
-                w[i] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-            }
-          }
-          if (b == 1) {
+        for (int b = 0; b < 4; ++b) {
+          const int c = 128 * half + 32 * b;      // column of the half
+          if (live) tmem_ld32_wait(r[b & 1]);
+          if (b < 3) {
+            if (live) tmem_ld32_issue(from + 32 * (b + 1), r[(b + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_empty);
           }
-          if (live && ok) store_rows(out + 256 * h + c, kHeadDim, w, lane, wide);
+          if (!live) continue;
+          uint32_t(&x)[32] = r[b & 1];
+          if (p.rope_out && h == 1 && c >= 192) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 t = sm.rope[tk][(c - 192) / 2 + i];
+              const float u = __uint_as_float(x[2 * i]), v = __uint_as_float(x[2 * i + 1]);
+              x[2 * i] = __float_as_uint(fmaf(u, t.x, -(v * t.y)));
+              x[2 * i + 1] = __float_as_uint(fmaf(u, t.y, v * t.x));
+            }
+          }
+          __syncwarp();   // the box's last contents are read
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[8 * q + 2 * i]) * inv,
+                                                              __uint_as_float(x[8 * q + 2 * i + 1]) * inv);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row_ = 8 * i + (lane >> 2);
+              *reinterpret_cast<uint4*>(out + 8 * i * kHeadDim + 256 * h + c) = *reinterpret_cast<const uint4*>(
+                  box + row_ * 64 + (((lane & 3) ^ ((row_ >> 1) & 3)) << 4));
+            }
+          }
         }
       }
     }
