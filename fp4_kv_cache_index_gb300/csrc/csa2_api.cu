@@ -2072,6 +2072,33 @@ csa2_status_t check_tree(const csa2_tree_t* t, const csa2_window_t* w, int64_t* 
   return CSA2_OK;
 }
 
+// How many drafts the deeper of two paths has that the other has not.
+int path_more(uint64_t a, uint64_t b) {
+  if (__builtin_popcountll(a) > __builtin_popcountll(b)) std::swap(a, b);
+  return __builtin_popcountll(b & ~a);
+}
+
+// A tree's drafts branch by branch: each before its children, a child's whole
+// branch before the next child's.
+void branch_order(int n, const int32_t* parent, int* order) {
+  int child[CSA2_MAX_DRAFT + 1], next[CSA2_MAX_DRAFT];   // [0]: of the root
+  std::fill(child, child + n + 1, -1);
+  for (int t = n - 1; t >= 0; --t) {
+    next[t] = child[parent[t] + 1];
+    child[parent[t] + 1] = t;
+  }
+  int at = n > 0 ? child[0] : -1;
+  for (int k = 0; k < n; ++k) {
+    order[k] = at;
+    if (child[at + 1] >= 0) {
+      at = child[at + 1];
+      continue;
+    }
+    while (at >= 0 && next[at] < 0) at = parent[at];
+    if (at >= 0) at = next[at];
+  }
+}
+
 // What the three attention calls share.
 csa2_status_t window_attn_common(int32_t n_heads, float scale, const csa2_window_opts_t* o,
                                  WinAttnCommon* p) {
@@ -2340,15 +2367,29 @@ csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t
     // whole trees (of at most 64 drafts each) up to the tables' sizes
     p->d = drafts_from(d, row);
     p->nq = 0;
+    p->n_items = 0;
     int k = 0;
     const int64_t row0 = row;
     for (; i < t->n_seqs && k < kWinTreeTrees && p->nq + t->n_draft[i] <= kWinTreeQueries; ++i, ++k) {
       p->pos0[k] = t->pos0[i];
       p->seq[k] = t->seq_ids ? t->seq_ids[i] : i;
       p->first[k] = p->nq;
-      for (int j = 0; j < t->n_draft[i]; ++j) {
-        p->path[p->nq] = paths[(size_t)row + j];
-        p->tree[p->nq++] = (int16_t)k;
+      const uint64_t* path = &paths[(size_t)row];
+      const int n = t->n_draft[i], first = p->nq;
+      int order[CSA2_MAX_DRAFT];
+      branch_order(n, t->parent + row, order);
+      for (int j = 0; j < n; ++j) {
+        // neighbours share an item of 128 heads if the deeper one's path has
+        // few drafts that the other's has not
+        const bool two = n_heads == 64 && j + 1 < n &&
+                         path_more(path[order[j]], path[order[j + 1]]) <= kWinPairDrafts;
+        p->item[p->n_items++] = (uint16_t)(p->nq | (two ? 0x8000 : 0));
+        for (const int end = j + two; ; ++j) {
+          p->query[p->nq] = (uint16_t)(first + order[j]);
+          p->path[p->nq] = path[order[j]];
+          p->tree[p->nq++] = (int16_t)k;
+          if (j == end) break;
+        }
       }
       row += t->n_draft[i];
     }

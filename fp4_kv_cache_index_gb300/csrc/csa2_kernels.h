@@ -413,15 +413,22 @@ struct WinDecodeParams : WinAttnCommon {
   int32_t seq0;
   int32_t seq[kWinQueries];
 };
-constexpr int kWinTreeQueries = 1792;
+constexpr int kWinTreeQueries = 1536;
 constexpr int kWinTreeTrees = 512;
+// Of a tree's two queries that share an item of 128 heads: drafts of the deeper
+// one's path that the other's has not.
+constexpr int kWinPairDrafts = 8;
 struct WinTreeParams : WinAttnCommon {
   WinDrafts d;               // from the first draft of the launch's first tree on
   int64_t pos0[kWinTreeTrees];
   int32_t seq[kWinTreeTrees];
   int32_t first[kWinTreeTrees];       // a tree's first draft row
-  uint64_t path[kWinTreeQueries];     // a query's path, itself included
+  // queries, a tree's so that neighbours have much of their paths in common
+  uint64_t path[kWinTreeQueries];     // the drafts on the path, itself included
   int16_t tree[kWinTreeQueries];
+  uint16_t query[kWinTreeQueries];    // its row of q and of the outputs
+  uint16_t item[kWinTreeQueries];     // of an item: its first query; the top bit: it has two
+  int32_t n_items;
 };
 struct WinPrefillParams : WinAttnCommon {
   const uint16_t* band;

@@ -38,6 +38,8 @@ constexpr int kThreads = 384;
 constexpr int kSlots = 144;             // rows of the tile
 constexpr int kRing = 17;               // blocks of 8 window rows
 constexpr int kFirstSlot = 8 * 16;      // first tokens, decode and trees
+constexpr int kMoreSlot = 8 * 17;       // drafts of one of an item's two queries only
+static_assert(kMoreSlot + kWinPairDrafts <= kSlots, "slots");
 constexpr int kChunkFirst = 8 * kRing;  // first tokens, chunks
 constexpr int kBlk = kSlots * 128;      // bytes of a 64-channel block of rows
 constexpr int kBox = 64 * 128;          // Q: 64 rows x 64 channels
@@ -54,17 +56,18 @@ constexpr int kSmallOff = kOutOff + kSoftWarps * kOutBox;
 struct Small {
   float red[2][128];            // [half of the columns][row]: maxima, then sums
   float2 rope[2][32];           // [token]: cos, sin of each channel pair
-  int64_t at[2];                // [item parity]: position of the first token
+  int64_t at[2][2];             // [item parity][token]: its position
   uint32_t vis[2][2][5];        // [item parity][token]: rows that it sees
   uint32_t bad[5];              // rows that hold an infinity or a NaN (chunks)
   alignas(4) uint8_t bad8[kRing + 1][4];   // the same, 8 rows of each block, by quarter of its loads
+  uint32_t bad_cb[kSoftWarps][5];          // the same (caches), by block of channels
   // cache: [item parity] what each slot takes: a row of the cache (-2), none
   // (-1) or a draft of the tree
   int8_t slot[2][kSlots];
-  // trees: [item parity] the path's drafts by depth, the slots that the item
-  // takes otherwise than the one before it (or, of its tree's first item, those
-  // that take drafts), and how many those are
-  uint8_t draft[2][64], list[2][kSlots];
+  // trees: a path's drafts by depth (each loading warp's own), and [item parity]
+  // the slots that the item takes otherwise than the one before it (or, of its
+  // tree's first item, those that take drafts), and how many those are
+  uint8_t draft[kLoadWarps][64], list[2][kSlots];
   int32_t n_list[2];
   uint32_t tmem;
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];
@@ -85,30 +88,6 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// 32 columns, the wait apart (see tmem_ld16_issue).
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%"
-      "14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -143,31 +122,38 @@ __device__ __forceinline__ bool not_finite(const uint4& v) {
 
 // Eight E4M3 codes (two words) -> eight bf16 times a power of two, exact (in bf16's
 // normal range).  E4M3's seven lower bits four places up in a bf16 are its value times 2^-120,
-// subnormal numbers too; the sign goes to the top.  The power comes as two
-// factors (code_scales): with 2^120 it may pass bf16's range.
-__device__ __forceinline__ uint4 e4m3_piece(uint32_t w0, uint32_t w1, uint2 scales) {
-  const uint32_t w[2] = {w0, w1};
+// subnormal numbers too; the sign goes to the top.
+__device__ __forceinline__ uint4 e4m3_eight(uint32_t w0, uint32_t w1, uint32_t factor) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t t = prmt(w[i >> 1], 0u, (i & 1) ? 0x3424u : 0x1404u);   // a code on top of each half
-    o[i] = bf16x2_mul(bf16x2_mul(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), scales.x), scales.y);
-  }
-  // a code with all seven bits set is a NaN
-  if ((((w0 & 0x7F7F7F7Fu) + 0x01010101u) | ((w1 & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c = w[i >> 1] >> (16 * (i & 1));
-      if ((c & 0x7Fu) == 0x7Fu) o[i] |= 0x7FFFu;
-      if ((c & 0x7F00u) == 0x7F00u) o[i] |= 0x7FFF0000u;
-    }
+    const uint32_t t = prmt(i < 2 ? w0 : w1, 0u, (i & 1) ? 0x3424u : 0x1404u);   // a code on top of each half
+    o[i] = bf16x2_mul(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), factor);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// 2^(byte - 7) = 2^120 2^(byte - 127) as two bf16, each in both halves.
-__device__ __forceinline__ uint2 code_scales(uint32_t byte) {
-  const uint32_t a = byte >> 1, b = byte - a;   // exponents a - 3 and b - 4
-  return make_uint2(((a + 124u) << 7) * 0x10001u, ((b + 123u) << 7) * 0x10001u);
+// Sixteen codes of rows with scale 2^(byte - 127); whether one of them is a NaN (all
+// seven bits set) or the value is above bf16's range: then they come as zeros.  By
+// all lanes of a warp.  The factor 2^(byte - 7) is a bf16 up to byte 134; above, which
+// rows of ordinary values do not have, there is a second one.
+__device__ __forceinline__ bool e4m3_sixteen(uint4 v, uint32_t byte, uint4& lo, uint4& hi) {
+  const uint32_t m = 0x7F7F7F7Fu, c = 0x01010101u;
+  bool bad = ((((v.x & m) + c) | ((v.y & m) + c) | ((v.z & m) + c) | ((v.w & m) + c)) & 0x80808080u) != 0u;
+  if (bad) v = make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t f = (min(byte, 134u) + 120u) * 0x00800080u;
+  lo = e4m3_eight(v.x, v.y, f);
+  hi = e4m3_eight(v.z, v.w, f);
+  if (__any_sync(0xffffffffu, byte > 134u)) {
+    const uint32_t g = (max(byte, 134u) - 7u) * 0x00800080u;   // 2^(byte - 134)
+    uint32_t* const x[2] = {&lo.x, &hi.x};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i >> 2][i & 3] = bf16x2_mul(x[i >> 2][i & 3], g);
+    if (not_finite(lo) || not_finite(hi)) {
+      bad = true;
+      lo = hi = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  return bad;
 }
 
 // 16 bytes to shared memory, asynchronously, around the L1.
@@ -192,8 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Small& sm = *reinterpret_cast<Small*>(smem + kSmallOff);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = p.n_heads;
-  const bool pair = kChunk && H == 64;    // an item is two tokens
-  const int n_items = pair ? (p.nq + 1) / 2 : p.nq;
+  const bool pair = (kChunk || kTree) && H == 64;   // an item is up to two tokens
+  int n_items = p.nq;
+  if constexpr (kTree) n_items = p.n_items;
+  else if (pair) n_items = (p.nq + 1) / 2;
   const int item0 = (int)((int64_t)n_items * blockIdx.x / gridDim.x);
   const int item1 = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
   const int W = p.w.swa, F = p.w.n_first;
@@ -233,8 +221,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lw = warp - 2;
   const bool loader = warp == 2 || warp == 3, soft = warp >= 4;
 
-  auto tokens_of = [&](int item) { return pair ? min(2, p.nq - 2 * item) : 1; };
-  auto first_token = [&](int item) { return pair ? 2 * item : item; };
+  auto tokens_of = [&](int item) -> int {
+    if constexpr (kTree) return 1 + (p.item[item] >> 15);
+    else return pair ? min(2, p.nq - 2 * item) : 1;
+  };
+  auto first_token = [&](int item) -> int {
+    if constexpr (kTree) return p.item[item] & 0x7FFF;
+    else return pair ? 2 * item : item;
+  };
+  // the query of a token of an item: its row of q and of the outputs
+  auto query_row = [&](int item, int tk) -> int {
+    if constexpr (kTree) return p.query[first_token(item) + tk];
+    else return first_token(item) + tk;
+  };
   auto piece = [&](int slot, int cb, int k) {
     return reinterpret_cast<uint4*>(kv + cb * kBlk + slot * 128 + ((k ^ (slot & 7)) << 4));
   };
@@ -325,11 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.first = (int64_t)p.w.n_seqs * W + (int64_t)seq * F;
     return t;
   };
-  // What slot j takes (sm.slot).  Ring row j holds position x, the one that is j
-  // mod W among the W newest up to the query's; slot 128 + f first token f.  A row
-  // of the cache counts only if it holds that position.
-  auto slot_of = [&](const Query& t, int j) -> int {
-    int64_t x = -1, row = 0;
+  // An item's query whose rows the slots take: of a tree's two the one that is
+  // less deep, whose window begins no later.  Its depth-k draft and the other's
+  // are of one position; what only the other one's path has goes to slots of its own.
+  auto base_of = [&](int item) -> int {
+    const int q = first_token(item);
+    if constexpr (kTree) {
+      if (tokens_of(item) > 1 && __popcll(p.path[q + 1]) < __popcll(p.path[q])) return q + 1;
+    }
+    return q;
+  };
+  // What slot j takes (sm.slot), and x, the position of that row.  Ring row j holds
+  // the position that is j mod W among the W newest up to the query's; slot 128 + f
+  // first token f.  A row of the cache counts only if it holds that position.
+  auto slot_of = [&](const Query& t, int j, int64_t& x) -> int {
+    int64_t row = 0;
+    x = -1;
     if (j < W) {
       int d = t.at_mod - j;
       if (d < 0) d += W;
@@ -341,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       row = t.first + x;
     }
     if (x < 0) return -1;
-    if (kTree && x >= t.pos0) return (int)(x - t.pos0);   // the path's draft of that depth
+    if (kTree && x >= t.pos0) return sm.draft[lw & 1][x - t.pos0];
     return p.w.pos[row] == x ? -2 : -1;
   };
 
-  // Whether an item is a draft of the tree of the one before it, whose rows are
-  // still there.
+  // Whether an item is of the tree of the one before it, whose rows are still
+  // there.
   auto same_tree = [&](int item) {
-    if constexpr (kTree) return item > item0 && p.tree[item] == p.tree[item - 1];
+    if constexpr (kTree) return item > item0 && p.tree[first_token(item)] == p.tree[first_token(item - 1)];
     else return false;
   };
   // Tables of an item, by the two loading warps: the rows that each token sees
@@ -356,9 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto item_tables = [&](int item) {
     const int par = (item - item0) & 1;
     const int n_tok = tokens_of(item), t0 = first_token(item);
-    int64_t at = 0;
+    int64_t at = 0, at_1 = 0;   // the tokens' positions
     if constexpr (kChunk) {
       at = p.pos0 + t0;
+      at_1 = at + 1;
       const int64_t hi = at + n_tok - 1;
       const int g_mod = (int)((hi >> 3) % kRing);
 #pragma unroll
@@ -383,30 +394,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      const Query t = query_of(item);
+      const int base = base_of(item);
+      const Query t = query_of(base);
       at = t.at;
+      uint64_t path = 0, other = 0;
+      int64_t at1 = 0;
+      int mine = 0;               // the base's place in the item
       if constexpr (kTree) {
-        const uint64_t path = p.path[item];
-        if (lw == 0)
+        path = p.path[base];
+        mine = base - t0;
+        if (n_tok > 1) {
+          other = p.path[2 * t0 + 1 - base];
+          at1 = t.pos0 + __popcll(other) - 1;
+        }
+        __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int b = lane + 32 * h;
-            if ((path >> b) & 1ull) sm.draft[par][__popcll(path & ((1ull << b) - 1ull))] = (uint8_t)b;
-          }
+        for (int h = 0; h < 2; ++h) {
+          const int b = lane + 32 * h;
+          if ((path >> b) & 1ull) sm.draft[lw][__popcll(path & ((1ull << b) - 1ull))] = (uint8_t)b;
+        }
+        __syncwarp();
+        at_1 = mine ? t.at : at1;
+        if (mine) at = at1;
       }
       int v[3];
+      int64_t x[3];
 #pragma unroll
       for (int k = 0; k < 3; ++k) {   // the tags' loads together
         const int j = 32 * (2 * k + lw) + lane;
-        v[k] = j < kSlots ? slot_of(t, j) : -1;
+        x[k] = -1;
+        v[k] = j < kMoreSlot ? slot_of(t, j, x[k]) : -1;
       }
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         const int word = 2 * k + lw, j = 32 * word + lane;
         if (word > 4) break;
-        if (j < kSlots) sm.slot[par][j] = (int8_t)v[k];
+        const bool near = j >= kFirstSlot || x[k] > at1 - W;
         const uint32_t m = __ballot_sync(0xffffffffu, v[k] != -1);
-        if (lane == 0) sm.vis[par][0][word] = m;
+        if constexpr (kTree) {
+          bool sees = n_tok > 1 && near && (v[k] == -2 || (v[k] >= 0 && ((other >> (v[k] & 63)) & 1ull)));
+          if (j >= kMoreSlot && j < kSlots) {
+            // the other path's drafts that this one has not
+            uint64_t left = other & ~path;
+            for (int i = kMoreSlot; i < j; ++i) left &= left - 1ull;
+            if (left) {
+              v[k] = __ffsll((long long)left) - 1;
+              const int64_t y = t.pos0 + __popcll(other & ((1ull << v[k]) - 1ull));
+              sees = y < F || y > at1 - W;
+            }
+          }
+          const uint32_t m1 = __ballot_sync(0xffffffffu, sees);
+          if (lane == 0) sm.vis[par][mine ^ 1][word] = m1;
+        }
+        if (j < kSlots) sm.slot[par][j] = (int8_t)v[k];
+        if (lane == 0) sm.vis[par][mine][word] = m;
       }
       if constexpr (kTree) {
         ok = named_bar_and(3, 32 * kLoadWarps, ok);   // both warps' halves
@@ -417,8 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool put = false;
             if (j < kSlots) {
               const int now = sm.slot[par][j], old = sm.slot[par ^ 1][j];
-              put = same ? now != old || (now >= 0 && sm.draft[par][now] != sm.draft[par ^ 1][now])
-                         : now >= 0;
+              put = same ? now != old : now >= 0 || (item > item0 && j >= kMoreSlot && old >= 0);
             }
             const uint32_t m = __ballot_sync(0xffffffffu, put);
             if (put) sm.list[par][n + __popc(m & ((1u << lane) - 1u))] = (uint8_t)j;
@@ -426,11 +466,83 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) sm.n_list[par] = n;
         }
+        named_bar(3, 32 * kLoadWarps);
       }
     }
-    if (lw == 0 && lane == 0) sm.at[par] = at;
+    if (lw == 0 && lane == 0) {
+      sm.at[par][0] = at;
+      sm.at[par][1] = at_1;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.tab_full);
+  };
+  // Trees: the rows of the listed slots, drafts' and those that take the places of
+  // the last path's.  A warp has channel blocks cb0, cb0 + 2, .. (kBlocks of them),
+  // 8 rows x 4 pieces of 16 bytes at a time, `ready` comes between the first loads
+  // and the first stores.
+  auto listed_rows = [&](const Query& t, int par, int cb0, auto blocks, auto ready) {
+    if constexpr (kTree) {
+      constexpr int kBlocks = decltype(blocks)::value, kFlight = kBlocks == 1 ? 4 : 8;
+      const int r8 = lane >> 2, c4 = lane & 3;
+      const int n = sm.n_list[par], jobs = (n + 7) / 8 * kBlocks;
+      int j0 = 0;
+#pragma unroll 1
+      do {
+        uint4 d[kFlight], e[kFlight];
+        uint32_t byte[kFlight];
+        int slot[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          const int at = (j0 + i) / kBlocks * 8 + r8, cb = cb0 + 2 * (i % kBlocks);
+          slot[i] = -1;
+          d[i] = e[i] = zero;
+          byte[i] = 0u;
+          if (at >= n) continue;
+          slot[i] = sm.list[par][at];
+          const int what = sm.slot[par][slot[i]];
+          if (what == -1) continue;
+          const WinDrafts& x = p.d;
+          const int64_t row = what >= 0 ? (int64_t)t.draft0 + what
+                              : slot[i] < W ? t.ring + slot[i] : t.first + slot[i] - kFirstSlot;
+          if (kFp8 && cb < 7) {
+            d[i] = ldg_now_v4((what >= 0 ? x.codes : p.w.codes) + row * 448 + 64 * cb + 16 * c4);
+            byte[i] = ldg_now_u8((what >= 0 ? x.scales : p.w.scales) + row * 8 + cb);
+          } else {
+            const uint16_t* src = kFp8 ? (what >= 0 ? x.rope : p.w.rope) + row * 64
+                                       : (what >= 0 ? x.rows : p.w.rows) + row * kHeadDim + 64 * cb;
+            d[i] = ldg_now_v4(src + 8 * c4);
+            e[i] = ldg_now_v4(src + 32 + 8 * c4);
+          }
+        }
+        bool bad[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          if (kFp8 && cb0 + 2 * (i % kBlocks) < 7) {
+            if (j0 + i < jobs) bad[i] = e4m3_sixteen(d[i], byte[i], d[i], e[i]);
+          } else {
+            bad[i] = not_finite(d[i]) || not_finite(e[i]);
+            if (bad[i]) d[i] = e[i] = zero;
+          }
+        }
+        if (j0 == 0) ready();
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+          if (j0 + i >= jobs) break;
+          const int cb = cb0 + 2 * (i % kBlocks);
+          const int p0 = kFp8 && cb < 7 ? 2 * c4 : c4, p1 = kFp8 && cb < 7 ? 2 * c4 + 1 : 4 + c4;
+          const uint32_t any = __ballot_sync(0xffffffffu, bad[i]);
+          if (slot[i] < 0) continue;
+          *piece(slot[i], cb, p0) = d[i];
+          *piece(slot[i], cb, p1) = e[i];
+          if (c4 == 0) {
+            const uint32_t bit = 1u << (slot[i] & 31);
+            if ((any >> lane) & 15u) atomicOr(&sm.bad_cb[cb][slot[i] >> 5], bit);
+            else atomicAnd(&sm.bad_cb[cb][slot[i] >> 5], ~bit);
+          }
+        }
+        j0 += kFlight;
+      } while (j0 < jobs);
+    }
   };
   // Rows of an item out of the cache, by the softmax warps: warp w has channels
   // 64 w .. 64 w + 63 of all rows, 8 rows x 4 pieces of 16 bytes at a time (whole
@@ -443,124 +555,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kChunk) {
       const uint32_t k = (uint32_t)(item - item0);
       const int par = k & 1, cb = warp - 4;
-      const Query t = query_of(item);
+      const Query t = query_of(base_of(item));
       constexpr int kGroups = 17;                        // of 8 slots
       const int r8 = lane >> 2, c4 = lane & 3;
       const bool codes = kFp8 && cb < 7;
       uint8_t* const mine = kv + cb * kBlk + r8 * 128;   // this lane's row of group 0
-      const bool same = same_tree(item);
+      uint32_t bad = 0u;         // groups in whose row this lane had an infinity or a NaN
       uint32_t sc[5] = {0u, 0u, 0u, 0u, 0u};             // of slots lane + 32 i
       if (k > 0) ok = mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err) && ok;
-      if (!same) {
-        if (codes) {
-          const uint8_t* src = p.w.codes + (t.ring + r8) * 448 + 64 * cb + 16 * c4;
+      if (codes) {
+        const uint8_t* src = p.w.codes + (t.ring + r8) * 448 + 64 * cb + 16 * c4;
 #pragma unroll 1
-          for (int j = r8, g = 0; g < 16; ++g, j += 8, src += 8 * 448)
-            if (j < W) copy_async(mine + g * 1024 + 16 * c4, src);
-          if (r8 < F)
-            copy_async(mine + 16 * 1024 + 16 * c4, p.w.codes + (t.first + r8) * 448 + 64 * cb + 16 * c4);
+        for (int j = r8, g = 0; g < 16; ++g, j += 8, src += 8 * 448)
+          if (j < W) copy_async(mine + g * 1024 + 16 * c4, src);
+        if (r8 < F)
+          copy_async(mine + 16 * 1024 + 16 * c4, p.w.codes + (t.first + r8) * 448 + 64 * cb + 16 * c4);
 #pragma unroll
-          for (int i = 0; i < 5; ++i) {
-            const int j = lane + 32 * i;
-            if (i < 4 ? j < W : lane < F)
-              sc[i] = ldg_now_u8(p.w.scales + (i < 4 ? t.ring + j : t.first + lane) * 8 + cb);
-          }
-        } else {
-          const int64_t step = kFp8 ? 64 : kHeadDim;
-          const uint16_t* base = kFp8 ? p.w.rope + 8 * c4 : p.w.rows + 64 * cb + 8 * c4;
-          const uint16_t* src = base + (t.ring + r8) * step;
+        for (int i = 0; i < 5; ++i) {
+          const int j = lane + 32 * i;
+          if (i < 4 ? j < W : lane < F)
+            sc[i] = ldg_now_u8(p.w.scales + (i < 4 ? t.ring + j : t.first + lane) * 8 + cb);
+        }
+      } else {
+        const int64_t step = kFp8 ? 64 : kHeadDim;
+        const uint16_t* base = kFp8 ? p.w.rope + 8 * c4 : p.w.rows + 64 * cb + 8 * c4;
+        const uint16_t* src = base + (t.ring + r8) * step;
 #pragma unroll 1
-          for (int j = r8, g = 0; g < kGroups; ++g, j += 8, src += 8 * step) {
-            if (g == 16) src = base + (t.first + r8) * step;
-            if (g < 16 ? j < W : r8 < F) {
-              copy_async(mine + g * 1024 + ((c4 ^ r8) << 4), src);
-              copy_async(mine + g * 1024 + (((4 + c4) ^ r8) << 4), src + 32);
-            }
+        for (int j = r8, g = 0; g < kGroups; ++g, j += 8, src += 8 * step) {
+          if (g == 16) src = base + (t.first + r8) * step;
+          if (g < 16 ? j < W : r8 < F) {
+            copy_async(mine + g * 1024 + ((c4 ^ r8) << 4), src);
+            copy_async(mine + g * 1024 + (((4 + c4) ^ r8) << 4), src + 32);
           }
         }
       }
       ok = mbar_wait(&sm.tab_full, par, err) && ok;
-      if (!same) {
-        copy_async_wait();
-        __syncwarp();
-        if (codes) {
+      copy_async_wait();
+      __syncwarp();
+      if (codes) {
+        // the next group's codes on their way while a group's are converted
+        auto take = [&](int g) {
+          return sm.slot[par][8 * g + r8] == -2 ? *reinterpret_cast<const uint4*>(mine + g * 1024 + 16 * c4) : zero;
+        };
+        uint4 next = take(0);
 #pragma unroll 1
-          for (int i = 0; i < 5; ++i) {
+        for (int g = 0; g < kGroups; ++g) {
+          const uint32_t byte = __shfl_sync(0xffffffffu, sc[0], 8 * (g & 3) + r8);
+          const uint4 v = next;
+          if (g + 1 < kGroups) next = take(g + 1);
+          uint4 lo, hi;
+          if (e4m3_sixteen(v, byte, lo, hi)) bad |= 1u << g;
+          __syncwarp();
+          uint8_t* const row = mine + g * 1024;
+          *reinterpret_cast<uint4*>(row + (((2 * c4) ^ r8) << 4)) = lo;
+          *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ r8) << 4)) = hi;
+          if ((g & 3) == 3) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int g = 4 * i + e;
-              if (g >= kGroups) break;
-              const uint32_t byte = __shfl_sync(0xffffffffu, sc[0], 8 * e + r8);
-              uint8_t* row = mine + g * 1024;
-              const bool there = sm.slot[par][8 * g + r8] == -2;
-              const uint4 v = there ? *reinterpret_cast<const uint4*>(row + 16 * c4) : zero;
-              const uint2 f = code_scales(byte);
-              const uint4 lo = e4m3_piece(v.x, v.y, f), hi = e4m3_piece(v.z, v.w, f);
-              __syncwarp();
-              *reinterpret_cast<uint4*>(row + (((2 * c4) ^ r8) << 4)) = lo;
-              *reinterpret_cast<uint4*>(row + (((2 * c4 + 1) ^ r8) << 4)) = hi;
-            }
-            sc[0] = sc[1];
-            sc[1] = sc[2];
-            sc[2] = sc[3];
-            sc[3] = sc[4];
+            for (int i = 0; i < 4; ++i) sc[i] = sc[i + 1];
           }
-        } else {
+        }
+      } else {
 #pragma unroll 1
+        for (int g = 0; g < kGroups; ++g) {
+          uint4* const a = reinterpret_cast<uint4*>(mine + g * 1024 + ((c4 ^ r8) << 4));
+          uint4* const b = reinterpret_cast<uint4*>(mine + g * 1024 + (((4 + c4) ^ r8) << 4));
+          bool put = sm.slot[par][8 * g + r8] != -2;
+          if constexpr (kTree) {
+            if (!put && (not_finite(*a) || not_finite(*b))) {
+              put = true;
+              bad |= 1u << g;
+            }
+          }
+          if (put) *a = *b = zero;
+        }
+      }
+      // Rows of a cache with infinities and NaN are zeros in the products (a
+      // probability of 0 times such a value would not be 0): other queries of the
+      // tree may not see them.  Those who do answer NaN.
+      if constexpr (kTree || kFp8) {
+        if (lane < 5) sm.bad_cb[cb][lane] = 0u;
+        __syncwarp();
+        if (bad) {
           for (int g = 0; g < kGroups; ++g)
-            if (sm.slot[par][8 * g + r8] != -2) {
-              *reinterpret_cast<uint4*>(mine + g * 1024 + ((c4 ^ r8) << 4)) = zero;
-              *reinterpret_cast<uint4*>(mine + g * 1024 + (((4 + c4) ^ r8) << 4)) = zero;
-            }
+            if ((bad >> g) & 1u) atomicOr(&sm.bad_cb[cb][g >> 2], 1u << (8 * (g & 3) + r8));
         }
-      }
-      if constexpr (kTree) {
-        // drafts' rows, and what takes the places of the last path's, four groups
-        // in flight
         __syncwarp();
-        const int n = sm.n_list[par];
-#pragma unroll 1
-        for (int g0 = 0; g0 < n; g0 += 32) {
-          uint4 d[4], e[4];
-          uint32_t byte[4];
-          int slot[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = g0 + 8 * i + r8;
-            slot[i] = -1;
-            d[i] = e[i] = zero;
-            byte[i] = 0u;
-            if (at >= n) continue;
-            slot[i] = sm.list[par][at];
-            const int what = sm.slot[par][slot[i]];
-            if (what == -1) continue;
-            const WinDrafts& x = p.d;
-            const int64_t row = what >= 0 ? (int64_t)t.draft0 + sm.draft[par][what]
-                                : slot[i] < W ? t.ring + slot[i] : t.first + slot[i] - kFirstSlot;
-            if (codes) {
-              d[i] = ldg_now_v4((what >= 0 ? x.codes : p.w.codes) + row * 448 + 64 * cb + 16 * c4);
-              byte[i] = ldg_now_u8((what >= 0 ? x.scales : p.w.scales) + row * 8 + cb);
-            } else {
-              const uint16_t* src = kFp8 ? (what >= 0 ? x.rope : p.w.rope) + row * 64
-                                         : (what >= 0 ? x.rows : p.w.rows) + row * kHeadDim + 64 * cb;
-              d[i] = ldg_now_v4(src + 8 * c4);
-              e[i] = ldg_now_v4(src + 32 + 8 * c4);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (slot[i] < 0) continue;
-            if (codes) {
-              const uint2 f = code_scales(byte[i]);
-              *piece(slot[i], cb, 2 * c4) = e4m3_piece(d[i].x, d[i].y, f);
-              *piece(slot[i], cb, 2 * c4 + 1) = e4m3_piece(d[i].z, d[i].w, f);
-            } else {
-              *piece(slot[i], cb, c4) = d[i];
-              *piece(slot[i], cb, 4 + c4) = e[i];
-            }
-          }
-        }
       }
+      if constexpr (kTree) listed_rows(t, par, cb, std::integral_constant<int, 1>(), [] {});
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.kv_full[par]);
@@ -603,7 +684,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0;
       for (int item = item0; item < item1 && ok; ++item) {
         const int now = tokens_of(item) * H / 64;   // boxes of the item: the last may have one
-        const int32_t row = first_token(item) * H;
         for (int cb = 0; cb < 8 && ok; ++cb, ++n) {
           const uint32_t s = n % stages, use = n / stages;
           if (use > 0) ok = mbar_wait(&sm.q_empty[s], (use - 1) & 1, err);
@@ -611,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&sm.q_full[s], now * kBox);
           uint8_t* dst = smem + kQOff + s * stage_bytes;
           for (int b = 0; b < now; ++b)
-            tma_load_2d(dst + b * kBox, &tm_q, 64 * cb, row + 64 * b, &sm.q_full[s]);
+            tma_load_2d(dst + b * kBox, &tm_q, 64 * cb,
+                        pair ? query_row(item, b) * H : query_row(item, 0) * H + 64 * b, &sm.q_full[s]);
         }
       }
       // the copies in flight must land before the CTA exits
@@ -717,9 +798,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // not before all warps have the last item's: a wait tells neighbouring
         // phases apart only
-        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1], ((k - 1) >> 1) & 1, err);
+        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
         item_tables(item);
         if (!ok) break;
+        // Of a tree whose rows are here already these warps bring the others, while
+        // the softmax warps have the last item's outputs to store.
+        if (same_tree(item)) {
+          listed_rows(query_of(base_of(item)), k & 1, lw, std::integral_constant<int, 4>(), [&] {
+            ok = mbar_wait(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
+          });
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane < kSoftWarps / kLoadWarps) mbar_arrive(&sm.kv_full[k & 1]);
+        }
       }
     }
   } else if (soft) {
@@ -732,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = item0; item < item1; ++item) {
       const uint32_t k = (uint32_t)(item - item0), ph = k & 1u;
       // (its last products are done: their outputs are stored)
-      if constexpr (!kChunk) cache_rows(item);
+      if (!kChunk && !same_tree(item)) cache_rows(item);
       const int n_rows = tokens_of(item) * H;
       const bool live = quad * 32 < n_rows;       // of the warp's rows, all or none
       const int tk = pair ? row >> 6 : 0;
@@ -741,26 +832,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // a thread has a half of its row: columns 0-79 or 80-143
       const int g0 = half ? 5 : 0, ng = half ? 4 : 5;
-      uint32_t s[5][16];
       float m = -INFINITY;
       if (live) {
+#pragma unroll 1
+        for (int g = g0; g < g0 + ng; ++g) {
+          uint32_t s[16];
+          tmem_ld16(tmem + lanes + kSCol + 16 * g, s);
+          const uint32_t v = sm.vis[ph][tk][g >> 1] >> (16 * (g & 1));
 #pragma unroll
-        for (int g = 0; g < 5; ++g)
-          if (g < ng) tmem_ld16_issue(tmem + lanes + kSCol + 16 * (g0 + g), s[g]);
-#pragma unroll
-        for (int g = 0; g < 5; ++g)
-          if (g < ng) tmem_ld16_wait(s[g]);
-#pragma unroll
-        for (int g = 0; g < 5; ++g) {
-          if (g < ng) {
-            const uint32_t v = sm.vis[ph][tk][(g0 + g) >> 1] >> (16 * ((g0 + g) & 1));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = (v >> i) & 1u ? __uint_as_float(s[g][i]) * p.scale_log2 : -INFINITY;
-              s[g][i] = __float_as_uint(x);
-              m = fmaxf(m, x);
-            }
-          }
+          for (int i = 0; i < 16; ++i)
+            m = fmaxf(m, (v >> i) & 1u ? __uint_as_float(s[i]) * p.scale_log2 : -INFINITY);
         }
         sm.red[half][row] = m;
       }
@@ -778,21 +859,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 5; ++i) b |= sm.vis[ph][tk][i] & sm.bad[i];
           bad = b != 0;
         }
-        const float m0 = m == -INFINITY ? 0.0f : m;
+        if constexpr (kTree || (kFp8 && !kChunk)) {
+          uint32_t b = 0;
 #pragma unroll
-        for (int g = 0; g < 5; ++g) {
-          if (g < ng) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = fast_exp2(__uint_as_float(s[g][2 * i]) - m0);
-              const float b = fast_exp2(__uint_as_float(s[g][2 * i + 1]) - m0);
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(a, b);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
-              sum += __uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xFFFF0000u);
-            }
-            tmem_st8(tmem + lanes + kPCol + 8 * (g0 + g), pk);
+          for (int i = 0; i < 2; ++i) {
+            const int w = lane + 32 * i;
+            if (w < kSoftWarps * 5) b |= sm.vis[ph][tk][w % 5] & sm.bad_cb[w / 5][w % 5];
           }
+          bad = __any_sync(0xffffffffu, b != 0);
+        }
+        const float m0 = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+        for (int g = g0; g < g0 + ng; ++g) {
+          uint32_t s[16], pk[8];
+          tmem_ld16(tmem + lanes + kSCol + 16 * g, s);
+          const uint32_t v = sm.vis[ph][tk][g >> 1] >> (16 * (g & 1));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float e[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = fast_exp2(fmaf(__uint_as_float(s[2 * i + h]), p.scale_log2, -m0));
+              e[h] = (v >> (2 * i + h)) & 1u ? x : 0.0f;
+            }
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e[0], e[1]);
+            pk[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            sum += __uint_as_float(pk[i] << 16) + __uint_as_float(pk[i] & 0xFFFF0000u);
+          }
+          tmem_st8(tmem + lanes + kPCol + 8 * g, pk);
         }
         sm.red[half][row] = sum;
         tmem_wait_st();
@@ -803,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.rope_out && half == 1 && (quad & 1) == 0) {
         // sines of the output rotation, by warps with fewer columns: of token
         // quad / 2 (all have left the item before this one)
-        const uint64_t turn = (uint64_t)(-(sm.at[ph] + (quad >> 1))) * p.turns[lane];
+        const uint64_t turn = (uint64_t)(-sm.at[ph][quad >> 1]) * p.turns[lane];
         float sn, cs;
         sincospif((float)(int64_t)turn * 0x1p-63f, &sn, &cs);
         sm.rope[quad >> 1][lane] = make_float2(cs, sn);
@@ -820,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         inv = L == 0.0f ? 0.0f : am / L;
         if (bad) inv = NAN;
         if (p.lse && half == 0)
-          p.lse[(int64_t)first_token(item) * H + row] =
+          p.lse[(int64_t)query_row(item, tk) * H + h] =
               inv != inv ? NAN
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
                                : (M + log2f(L)) * 0.69314718055994531f;
@@ -828,26 +922,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // outputs, 32 rows x 32 channels at a time: rounded, turned in the warp's own
       // box so that four lanes have 64 bytes of a row (a lane that stores its own
       // row touches 32 lines an instruction), the next ones on their way
-      uint16_t* out = p.out + ((int64_t)first_token(item) * H + 32 * quad + (lane >> 2)) * kHeadDim + 8 * (lane & 3);
+      uint16_t* out = p.out + 8 * (lane & 3);
+      if (live) out += ((int64_t)query_row(item, tk) * H + ((32 * quad) & (H - 1)) + (lane >> 2)) * kHeadDim;
       for (int h = 0; h < 2; ++h, ++chunk) {
         ok = mbar_wait(&sm.o_full, chunk & 1, err) && ok;
         tc_fence_after();
         const uint32_t from = tmem + lanes + kOCol + 128 * half;
-        uint32_t r[2][32];
-        if (live) tmem_ld32_issue(from, r[0]);
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           const int c = 128 * half + 32 * b;      // column of the half
-          if (live) tmem_ld32_wait(r[b & 1]);
-          if (b < 3) {
-            if (live) tmem_ld32_issue(from + 32 * (b + 1), r[(b + 1) & 1]);
-          } else {
+          uint32_t x[32];
+          if (live) tmem_ld32(from + 32 * b, x);
+          if (b == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_empty);
           }
           if (!live) continue;
-          uint32_t(&x)[32] = r[b & 1];
           if (p.rope_out && h == 1 && c >= 192) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -917,8 +1008,8 @@ cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q,
 }
 
 cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
-  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, p.nq, sms, s)
-                 : launch<WinTreeParams, false>(p, q, p.nq, sms, s);
+  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, p.n_items, sms, s)
+                 : launch<WinTreeParams, false>(p, q, p.n_items, sms, s);
 }
 
 cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {

@@ -329,22 +329,35 @@ def random_tree(n, seed):
     return [t - 1 if t and rng.random() < 0.5 else rng.randrange(-1, t) for t in range(n)]
 
 
+def tree_rows(model, tree, i, t, rows, first):
+    """The rows that draft t of tree i sees; its tree's rows begin at `first`."""
+    seq, pos0 = i if tree._seq is None else tree._seq[i], tree.pos0[i]
+    path = [k for k in range(t + 1) if (tree.paths[i][t] >> k) & 1]
+    vals = rows[[first + k for k in path]]
+    vals = round8(vals) if model.fp8 else vals.double()
+    held = {**{x: v for x, v in model.held[seq].items() if x < pos0},
+            **{pos0 + j: v for j, v in enumerate(vals)}}
+    p = pos0 + len(path) - 1
+    xs = sorted(x for x in held if p - x < model.swa or x < model.n_first)
+    return torch.stack([held[x] for x in xs])
+
+
 @pytest.mark.parametrize("heads,swa,n_first,fp8", [(64, 128, 4, True), (128, 128, 0, False),
                                                    (64, 9, 8, False), (128, 70, 3, True)])
 def test_tree_is_decoding_its_paths(heads, swa, n_first, fp8):
-    """Bit for bit: a tree's drafts, and their paths appended and decoded token
-    by token."""
+    """A tree's drafts, and their paths appended and decoded token by token."""
     c = C()
     pos0 = [0, 1, 150, 6, 2 ** 31 + 77]
     parents = [random_tree(12, 1), random_tree(64, 2), list(range(-1, 63)), [], random_tree(30, 4)]
     seqs = [3, 0, 4, 1, 2]
     tree = c.Tree(parents, pos0, seqs)
-    win = c.Window(5, swa, n_first, fp8)
+    win, model = c.Window(5, swa, n_first, fp8), Model(5, swa, n_first, fp8)
     counts = [min(p, swa + 5) for p in pos0]
     head = [min(p, n_first) for p in pos0]
-    c.csa2_window_append(win, make_rows(sum(head), 5), dev64([0] * 5), head, seqs)
-    c.csa2_window_append(win, make_rows(sum(counts), 6), dev64([p - n for p, n in zip(pos0, counts)]),
-                         counts, seqs)
+    for k, (n, at) in enumerate(((head, [0] * 5), (counts, [p - n for p, n in zip(pos0, counts)]))):
+        before = make_rows(sum(n), 5 + k)
+        c.csa2_window_append(win, before, dev64(at), n, seqs)
+        model.append(before, at, n, seqs)
     nq = tree.n_queries
     q, rows = make_q(nq, heads, 8), make_rows(nq, 9)
     draft = c.csa2_swa_fp8_quantise(rows) if fp8 else rows
@@ -365,7 +378,12 @@ def test_tree_is_decoding_its_paths(heads, swa, n_first, fp8):
             one = c.csa2_window_attn_decode(win, q[first + t:first + t + 1].contiguous(),
                                             dev64([pos0[i] + len(path) - 1]), SCALE, [seqs[i]],
                                             lse=l1, sink=sink, rope_out=True)
-            assert torch.equal(one[0], out[first + t]) and torch.equal(l1[0], lse[first + t]), (i, t)
+            if heads == 128:   # one query an item: the same sums in the same order
+                assert torch.equal(one[0], out[first + t]) and torch.equal(l1[0], lse[first + t]), (i, t)
+            ref = attend(q[first + t], tree_rows(model, tree, i, t, rows, first), sink=sink,
+                         at=pos0[i] + len(path) - 1)
+            check(out[first + t], lse[first + t], ref)
+            check(one[0], l1[0], ref)
         first += len(par)
     # acceptance writes what appending the path writes
     for a, b in zip(arrays, held):
@@ -393,8 +411,10 @@ def test_many_trees():
     n = 600
     parents = [random_tree(1 + i % 7, i) for i in range(n)]
     tree = c.Tree(parents, [10 + i for i in range(n)])
-    win = c.Window(n, 8, 1, False)
-    c.csa2_window_append(win, make_rows(n * 10, 1), dev64([i for i in range(n)]), [10] * n)
+    win, model = c.Window(n, 8, 1, False), Model(n, 8, 1, False)
+    before = make_rows(n * 10, 1)
+    c.csa2_window_append(win, before, dev64([i for i in range(n)]), [10] * n)
+    model.append(before, list(range(n)), [10] * n, range(n))
     q, rows = make_q(tree.n_queries, 64, 2), make_rows(tree.n_queries, 3)
     out = c.csa2_window_attn_tree(win, tree, q, rows, SCALE)
     acc = [len(p) - 1 for p in parents]
@@ -402,7 +422,54 @@ def test_many_trees():
     last = [sum(len(p) for p in parents[:i + 1]) - 1 for i in range(n)]
     at = dev64([10 + i + tree.depths[i][-1] for i in range(n)])
     again = c.csa2_window_attn_decode(win, q[last].contiguous(), at, SCALE)
-    assert torch.equal(again, out[last])
+    for i, x in enumerate(last):
+        kv = tree_rows(model, tree, i, acc[i], rows, x - acc[i])
+        ref = attend(q[x], kv)
+        check(out[x], None, ref)
+        check(again[i], None, ref)
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("swa,n_first", [(128, 8), (128, 0), (1, 0), (3, 2), (64, 5)])
+def test_branches(swa, n_first, fp8, heads):
+    """Neighbouring drafts of all kinds: of one parent, of far branches, deep and
+    shallow in turn; NaN and an infinity of a draft reach those who see it only."""
+    c = C()
+    star, comb = [-1] * 64, [x for k in range(32) for x in (2 * k - 2 if k else -1, 2 * k - 2 if k else -1)]
+    deep = list(range(-1, 29)) + [-1, 4, 31, 32, 33, 34, 35, 36, 37, 38, 39, 40, 41, 10, 43]
+    parents = [star, comb, deep, random_tree(64, 5), [-1], [-1, -1], [-1, 0, -1]]
+    pos0 = [200, 5, 0, 1000, 3, 64, 131]
+    bad = [7, 20, 12, 33, None, 1, 0]     # a draft of each tree
+    S = len(parents)
+    tree = c.Tree(parents, pos0)
+    win, model = c.Window(S, swa, n_first, fp8), Model(S, swa, n_first, fp8)
+    for part in range(2):
+        n = [min(p, n_first if part == 0 else swa) for p in pos0]
+        at = [0 if part == 0 else p - k for p, k in zip(pos0, n)]
+        before = make_rows(sum(n), 20 + part)
+        c.csa2_window_append(win, before, dev64(at), n)
+        model.append(before, at, n, range(S))
+    q, rows = make_q(tree.n_queries, heads, 8), make_rows(tree.n_queries, 9)
+    starts = [sum(len(p) for p in parents[:i]) for i in range(S)]
+    draft_rows = rows.clone()
+    for i, b in enumerate(bad):
+        if b is not None:
+            draft_rows[starts[i] + b, 13 * i] = math.nan if fp8 or i % 2 else math.inf
+    draft = c.csa2_swa_fp8_quantise(draft_rows) if fp8 else draft_rows
+    lse = torch.empty(tree.n_queries, heads, device="cuda")
+    out = c.csa2_window_attn_tree(win, tree, q, draft, SCALE, lse=lse)
+    for i, par in enumerate(parents):
+        for t in range(len(par)):
+            x = starts[i] + t
+            b = bad[i]
+            on = b is not None and (tree.paths[i][t] >> b) & 1
+            far = on and tree.depths[i][t] - tree.depths[i][b]   # behind the query
+            if on and (far < swa or pos0[i] + tree.depths[i][b] < n_first):
+                assert out[x].isnan().all() and lse[x].isnan().all(), (i, t)
+            else:
+                check(out[x], lse[x], attend(q[x], tree_rows(model, tree, i, t, rows, starts[i])))
+    assert win.device_error() == 0
 
 
 # ------------------------------------------------------------------ chunks
