@@ -48,6 +48,7 @@ constexpr int kMaxStages = 8;
 constexpr int kOutBox = 32 * 64;        // outputs: 32 rows x 32 channels
 constexpr int kLoadWarps = 2, kSoftWarps = 8;
 constexpr int kRowWarps = kLoadWarps + kSoftWarps;
+constexpr int kMaxParts = 4;            // of an item's rows, by channels
 
 constexpr int kKvOff = 0;
 constexpr int kQOff = kKvOff + 8 * kBlk;
@@ -73,7 +74,7 @@ struct Small {
   uint64_t q_full[kMaxStages], q_empty[kMaxStages];
   // a wait tells neighbouring phases of a barrier apart only: those whose two
   // sides may be two items apart are two, for items in turn
-  uint64_t kv_full[2], kv_empty[2], s_full, p_full, o_full, o_empty, tab_full, end;
+  uint64_t kv_full[2][kMaxParts], kv_empty[2], s_full, p_full, o_full, o_empty, tab_full, end;
 };
 constexpr int kSmemBytes = kSmallOff + (int)sizeof(Small);
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -160,8 +161,13 @@ __device__ __forceinline__ bool e4m3_sixteen(uint4 v, uint32_t byte, uint4& lo, 
 __device__ __forceinline__ void copy_async(void* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Until at most n groups of this thread's copies are left.
+template <int n>
 __device__ __forceinline__ void copy_async_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
 template <class P>
@@ -173,6 +179,8 @@ template <class P, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     k_window_attn(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_q) {
   constexpr bool kChunk = kIsChunk<P>, kTree = kIsTree<P>;
+  // parts of the rows that the products can begin with
+  constexpr int kParts = kChunk || kTree || kFp8 ? 1 : kMaxParts, kLast = kParts - 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* kv = smem + kKvOff;
   Small& sm = *reinterpret_cast<Small*>(smem + kSmallOff);
@@ -195,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.q_full[s], 1);
       mbar_init(&sm.q_empty[s], 1);
     }
-    mbar_init(&sm.kv_full[0], kChunk ? kLoadWarps : kSoftWarps);
-    mbar_init(&sm.kv_full[1], kChunk ? kLoadWarps : kSoftWarps);
+    for (int i = 0; i < 2 * kMaxParts; ++i)
+      mbar_init(&sm.kv_full[i / kMaxParts][i % kMaxParts], kChunk ? kLoadWarps : kSoftWarps);
     mbar_init(&sm.kv_empty[0], 1);
     mbar_init(&sm.kv_empty[1], 1);
     mbar_init(&sm.s_full, 1);
@@ -544,15 +552,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       } while (j0 < jobs);
     }
   };
-  // Rows of an item out of the cache, by the softmax warps: warp w has channels
-  // 64 w .. 64 w + 63 of all rows, 8 rows x 4 pieces of 16 bytes at a time (whole
-  // sectors, and stores without conflicts).  bf16 pieces go straight to their
-  // places; codes go to the first halves of their rows' places, from where the
-  // warp that has brought them takes them again.  Loops, not straight code: most
-  // CTAs come here once, and unrolled it was the fetching of instructions that
-  // took the time.
-  auto cache_rows = [&](int item) {
-    if constexpr (!kChunk) {
+  // Rows of an item out of the cache, by the softmax warps, 8 rows x 4 pieces of 16
+  // bytes at a time (whole sectors, and stores without conflicts).  Loops, not
+  // straight code: most CTAs come here once, and unrolled it was the fetching of
+  // instructions that took the time.
+  //
+  // bf16, one token a sequence: warp w has groups w and w + 8 of 8 slots, and of the
+  // first tokens' channels 64 w ..; the products begin with the first quarter of the
+  // channels, while the others are on their way.
+  auto quarter_rows = [&](int item) {
+    if constexpr (kParts > 1) {
+      const uint32_t k = (uint32_t)(item - item0);
+      const int par = k & 1, w = warp - 4, r8 = lane >> 2, c4 = lane & 3;
+      const Query t = query_of(item);
+      // unit u: its group's row of this lane, and where it goes in block 0
+      const uint16_t* from[3];
+      uint8_t* to[3];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const int j = 8 * (u < 2 ? w + 8 * u : 16) + r8;
+        const bool is = u == 2 ? r8 < F : j < W;
+        from[u] = is ? p.w.rows + (u == 2 ? t.first + r8 : t.ring + j) * kHeadDim + 8 * c4 : nullptr;
+        to[u] = kv + j * 128;
+      }
+      if (k > 0) ok = mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err) && ok;
+#pragma unroll 1
+      for (int cb = 0; cb < 8; ++cb) {
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          if (!from[u] || (u == 2 && cb != w)) continue;
+          copy_async(to[u] + cb * kBlk + ((c4 ^ r8) << 4), from[u] + 64 * cb);
+          copy_async(to[u] + cb * kBlk + (((4 + c4) ^ r8) << 4), from[u] + 64 * cb + 32);
+        }
+        if (cb & 1) copy_async_commit();
+      }
+      ok = mbar_wait(&sm.tab_full, par, err) && ok;
+      bool there[3];
+#pragma unroll
+      for (int u = 0; u < 3; ++u) there[u] = sm.slot[par][8 * (u < 2 ? w + 8 * u : 16) + r8] == -2;
+#pragma unroll 1
+      for (int cb = 0; cb < 8; ++cb) {
+        if (cb == 0) copy_async_wait<3>();
+        else if (cb == 2) copy_async_wait<2>();
+        else if (cb == 4) copy_async_wait<1>();
+        else if (cb == 6) copy_async_wait<0>();
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          if (there[u] || (u == 2 && cb != w)) continue;
+          *reinterpret_cast<uint4*>(to[u] + cb * kBlk + ((c4 ^ r8) << 4)) = zero;
+          *reinterpret_cast<uint4*>(to[u] + cb * kBlk + (((4 + c4) ^ r8) << 4)) = zero;
+        }
+        if (cb & 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.kv_full[par][cb >> 1]);
+        }
+      }
+    }
+  };
+  // FP8, and the first item of a tree: warp w has channels 64 w .. 64 w + 63 of all
+  // rows, and then of the path's drafts.  bf16 pieces go straight to their places;
+  // codes go to the first halves of their rows' places, from where the warp that has
+  // brought them takes them again.  (By quarters of the channels the codes take as
+  // long: the products slow the warps' own accesses down.)
+  auto block_rows = [&](int item) {
+    if constexpr (kTree || (kFp8 && !kChunk)) {
       const uint32_t k = (uint32_t)(item - item0);
       const int par = k & 1, cb = warp - 4;
       const Query t = query_of(base_of(item));
@@ -589,8 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      copy_async_commit();
       ok = mbar_wait(&sm.tab_full, par, err) && ok;
-      copy_async_wait();
+      copy_async_wait<0>();
       __syncwarp();
       if (codes) {
         // the next group's codes on their way while a group's are converted
@@ -620,11 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint4* const a = reinterpret_cast<uint4*>(mine + g * 1024 + ((c4 ^ r8) << 4));
           uint4* const b = reinterpret_cast<uint4*>(mine + g * 1024 + (((4 + c4) ^ r8) << 4));
           bool put = sm.slot[par][8 * g + r8] != -2;
-          if constexpr (kTree) {
-            if (!put && (not_finite(*a) || not_finite(*b))) {
-              put = true;
-              bad |= 1u << g;
-            }
+          if (kTree && !put && (not_finite(*a) || not_finite(*b))) {
+            put = true;
+            bad |= 1u << g;
           }
           if (put) *a = *b = zero;
         }
@@ -632,19 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Rows of a cache with infinities and NaN are zeros in the products (a
       // probability of 0 times such a value would not be 0): other queries of the
       // tree may not see them.  Those who do answer NaN.
-      if constexpr (kTree || kFp8) {
-        if (lane < 5) sm.bad_cb[cb][lane] = 0u;
-        __syncwarp();
-        if (bad) {
-          for (int g = 0; g < kGroups; ++g)
-            if ((bad >> g) & 1u) atomicOr(&sm.bad_cb[cb][g >> 2], 1u << (8 * (g & 3) + r8));
-        }
-        __syncwarp();
+      if (lane < 5) sm.bad_cb[cb][lane] = 0u;
+      __syncwarp();
+      if (bad) {
+        for (int g = 0; g < kGroups; ++g)
+          if ((bad >> g) & 1u) atomicOr(&sm.bad_cb[cb][g >> 2], 1u << (8 * (g & 3) + r8));
       }
+      __syncwarp();
       if constexpr (kTree) listed_rows(t, par, cb, std::integral_constant<int, 1>(), [] {});
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kv_full[par]);
+      if (lane == 0) mbar_arrive(&sm.kv_full[par][kLast]);
     }
   };
 
@@ -712,10 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // channel blocks c0 .. c1 - 1 of an item's S
       auto issue_s = [&](int item, int c0, int c1) {
         const uint32_t j = (uint32_t)(item - item0);
-        if (c0 == 0) ok = mbar_wait(&sm.kv_full[j & 1], (j >> 1) & 1, err);
         for (int cb = c0; cb < c1 && ok; ++cb, ++n) {
           const uint32_t s = n % stages;
-          ok = mbar_wait(&sm.q_full[s], (n / stages) & 1, err);
+          if (cb % (8 / kParts) == 0)
+            ok = mbar_wait(&sm.kv_full[j & 1][cb / (8 / kParts)], (j >> 1) & 1, err);
+          if (ok) ok = mbar_wait(&sm.q_full[s], (n / stages) & 1, err);
           if (!ok) break;
           tc_fence_after();
           for (int k = 0; k < 4; ++k)
@@ -794,11 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.kv_full[k & 1]);
+        if (lane == 0) mbar_arrive(&sm.kv_full[k & 1][0]);
       } else {
         // not before all warps have the last item's: a wait tells neighbouring
         // phases apart only
-        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
+        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1][kLast], ((k - 1) >> 1) & 1, err) && ok;
         item_tables(item);
         if (!ok) break;
         // Of a tree whose rows are here already these warps bring the others, while
@@ -809,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           });
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane < kSoftWarps / kLoadWarps) mbar_arrive(&sm.kv_full[k & 1]);
+          if (lane < kSoftWarps / kLoadWarps) mbar_arrive(&sm.kv_full[k & 1][0]);
         }
       }
     }
@@ -823,11 +885,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int item = item0; item < item1; ++item) {
       const uint32_t k = (uint32_t)(item - item0), ph = k & 1u;
       // (its last products are done: their outputs are stored)
-      if (!kChunk && !same_tree(item)) cache_rows(item);
+      if constexpr (kTree) {
+        if (!same_tree(item)) block_rows(item);
+      } else if constexpr (kParts > 1) {
+        quarter_rows(item);
+      } else if constexpr (!kChunk) {
+        block_rows(item);
+      }
       const int n_rows = tokens_of(item) * H;
       const bool live = quad * 32 < n_rows;       // of the warp's rows, all or none
       const int tk = pair ? row >> 6 : 0;
-      ok = mbar_wait(&sm.kv_full[ph], (k >> 1) & 1, err) && ok;
+      ok = mbar_wait(&sm.kv_full[ph][kLast], (k >> 1) & 1, err) && ok;
       ok = mbar_wait(&sm.s_full, ph, err) && ok;
       tc_fence_after();
       // a thread has a half of its row: columns 0-79 or 80-143
