@@ -1214,6 +1214,16 @@ def csa2_window_attn_prefill(q: torch.Tensor, pos0: int, rows: torch.Tensor, row
 
 
 # ------------------------------------------------------------------ verification of drafts
+def _value_rows(t: torch.Tensor, n: int, vocab: int, dtype, what: str, dev: int):
+    """Device pointer and row distance of [n, vocab] values on CUDA device `dev`,
+    a row's next to each other."""
+    step, one = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != (n, vocab) or t.dtype != dtype or t.get_device() != dev or (one != 1 and vocab > 1):
+        raise ValueError(f"{what}: expected {dtype} [{n}, {vocab}] on the current device, with the "
+                         f"values of a row next to each other")
+    return t.data_ptr(), step
+
+
 def csa2_verify_tree(tree: Tree, tokens: torch.Tensor, logits: torch.Tensor,
                      temperature: Optional[torch.Tensor] = None,
                      uniform: Optional[torch.Tensor] = None, noise: Optional[torch.Tensor] = None,
@@ -1241,44 +1251,34 @@ def csa2_verify_tree(tree: Tree, tokens: torch.Tensor, logits: torch.Tensor,
     if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{what}: logits bf16 or fp32 [n_queries, vocab] expected")
     vocab, dtype = logits.shape[1], logits.dtype
-    ld = None
-
-    def rows(t, n, ty, name):
-        if (t.dim() != 2 or t.shape != (n, vocab) or t.dtype != ty or t.get_device() != dev
-                or (vocab > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{name}: expected {ty} [{n}, {vocab}] on the current device, with the "
-                             f"values of a row next to each other")
-        return t.data_ptr()
-
-    def lrows(t, n, name):
-        nonlocal ld
+    f32, i32 = torch.float32, torch.int32
+    ld, at = None, []
+    for t, n, name in ((logits, nq, "logits"), (root_logits, S, "root_logits"),
+                       (draft_logits, nq, "draft_logits"), (draft_root, S, "draft_root")):
         if t is None:
-            return None
-        at = rows(t, n, dtype, name)
+            at.append(None)
+            continue
+        p, step = _value_rows(t, n, vocab, dtype, name, dev)
         if n > 1:   # a single row has no distance to the next
-            if ld is not None and t.stride(0) != ld:
+            if ld is not None and step != ld:
                 raise ValueError(f"{name}: the rows of all logits have to be equally far apart")
-            ld = t.stride(0)
-        return at
-
-    if accepted is None:
-        accepted = _empty((S,), torch.int32, logits.device, stream)
-    if next_token is None:
-        next_token = _empty((S,), torch.int32, logits.device, stream)
-    f32 = torch.float32
-    at = [lrows(logits, nq, "logits"), lrows(root_logits, S, "root_logits"),
-          lrows(draft_logits, nq, "draft_logits"), lrows(draft_root, S, "draft_root")]
-    noise_ld = 0
+            ld = step
+        at.append(p)
+    noise_at, noise_ld = None, 0
     if noise is not None:
-        noise_at = rows(noise, S, f32, "noise")
-        noise_ld = noise.stride(0) if S > 1 else (vocab + 3) // 4 * 4
+        noise_at, noise_ld = _value_rows(noise, S, vocab, f32, "noise", dev)
+        if S == 1:
+            noise_ld = (vocab + 3) // 4 * 4
+    if accepted is None:
+        accepted = _empty((S,), i32, logits.device, stream)
+    if next_token is None:
+        next_token = _empty((S,), i32, logits.device, stream)
     v = VerifyStruct(
-        vocab, int(dtype == f32), _shaped(tokens, (nq,), torch.int32, "tokens", dev), *at,
+        vocab, dtype is f32, _shaped(tokens, (nq,), i32, "tokens", dev), *at,
         (vocab + 7) // 8 * 8 if ld is None else ld,
         None if temperature is None else _shaped(temperature, (S,), f32, "temperature", dev),
         None if uniform is None else _shaped(uniform, (nq,), f32, "uniform", dev),
-        None if noise is None else noise_at, noise_ld,
-        _shaped(accepted, (S,), torch.int32, "accepted", dev),
-        _shaped(next_token, (S,), torch.int32, "next_token", dev))
+        noise_at, noise_ld, _shaped(accepted, (S,), i32, "accepted", dev),
+        _shaped(next_token, (S,), i32, "next_token", dev))
     _check(lib.csa2_verify_tree(tree.ref, ctypes.byref(v), _stream(stream, dev)), what)
     return accepted, next_token
