@@ -11,9 +11,14 @@
 // Bound: memory traffic, and for a decode step the launch.  A warp holds a
 // row: lane l has the 16-byte chunks l and l + 32 of 8 channels, so that every
 // access is contiguous over the lanes; the 8 lanes of a 64-channel block find
-// its largest magnitude by three shuffles.  No row is written twice by a call
-// (its segments are of different sequences, and a row that a later row of its
-// segment replaces is not stored), so there is nothing to order.
+// its largest magnitude by three shuffles of bf16 pairs.  No row is written twice
+// by a call (its segments are of different sequences, and a row that a later row of
+// its segment replaces is not stored), so there is nothing to order.
+//
+// Measured: 98000 rows of prompts, rounded into other memory (201 MB) and each
+// sequence's last 128 stored: 36.1 us, 5.6 TB/s or 82 % of the copy rate; with 192
+// windows read back behind it, 44.4 us.  A chunk of 8192 rows and its window back:
+// 4.9 us, 16 single rows and their windows: 3.5 us, two launches each.
 #include <cuda_fp16.h>
 
 #include "csa2_device.cuh"

@@ -17,11 +17,33 @@
 // memory; O is made in two halves of 256 channels, since both halves, S and P
 // do not fit the 512 columns together.  A CTA takes neighbouring items: in a
 // chunk the rows stay in shared memory as a ring of 17 blocks of 8 positions
-// (and one of first tokens), of which one is replaced every 8 tokens.
+// (and one of first tokens), of which one is replaced every 8 tokens; of a tree
+// they stay too, but for the slots that the next paths take otherwise.
+//
+// A tree's drafts of 64 heads go two an item, in the order of its branches, so
+// that neighbours have most of their paths in common: the slots are the less deep
+// one's, and what only the other's path has is in up to 8 more.  Each query has its
+// own mask of the 144 slots.  (One draft an item: 73 us where this takes 50, 1024
+// drafts.)
+//
+// What bounds it.  The chunk: HBM, q in and the outputs out (8192 tokens of 64 heads
+// are 1.08 GB: 215 us, 74 % of the copy rate); an item's S (32 MMAs of 155 cycles,
+// which read Q and the rows from shared memory), softmax, products and stores are a
+// chain of which only half of the next S and the second half of the stores run
+// beside something else.  Decode: the same chain once (27000 cycles, of which the
+// rows 11000, S 5000, the softmax 3000, products and outputs 5000): 13-14 us for one
+// sequence or 128.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
+// Trees: 1024 drafts 50 us, three to four items a CTA.
+//
+// Code is fetched cold by most CTAs, once for each instruction that a single pass
+// executes: the softmax and the outputs are loops over 16 and 32 columns although
+// they read tensor memory twice for it (unrolled, with all columns in registers, the
+// first item's softmax took 10700 cycles, now 4000; the chunk 224 us).
 //
 // Roles: warp 0 loads Q (TMA), warp 1 issues the MMAs, warps 2 and 3 load
 // rows, warps 4-11 (two for each quadrant of tensor memory lanes) do the
-// softmax and the outputs, which go to memory from registers.
+// softmax and the outputs and take rows out of a cache.  (Sixteen such warps, with 96
+// registers a thread: 224 us instead of 215, the trees 57 instead of 50.)
 #include <cuda_fp16.h>
 
 #include <type_traits>

@@ -141,3 +141,12 @@ def test_drafted_steps_are_greedy_decoding(fp8, swa, n_first):
         got, ref = (c.csa2_window_read(x, end, swa, [s]) for x in (win, want))
         assert torch.equal(got, ref) and ref.any()
     assert win.device_error() == 0
+
+
+def test_readme_window_example_runs():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), re.S)
+    code, = [b for b in blocks if "C.Window(" in b]
+    exec(compile(code, "README.md", "exec"), {})
