@@ -31,8 +31,8 @@
 // which read Q and the rows from shared memory), softmax, products and stores are a
 // chain of which only half of the next S and the second half of the stores run
 // beside something else.  Decode: the same chain once (27000 cycles, of which the
-// rows 11000, S 5000, the softmax 3000, products and outputs 5000): 13-14 us for one
-// sequence or 128.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
+// rows 11000, S 5000, the softmax 3000, products and outputs 5000): 14.5 us for 128
+// sequences; for one, four CTAs share the outputs: 11.5 us.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
 // Trees: 1024 drafts 50 us, three to four items a CTA.
 //
 // Code is fetched cold by most CTAs, once for each instruction that a single pass
@@ -199,7 +199,8 @@ constexpr bool kIsTree = std::is_same<P, WinTreeParams>::value;
 
 template <class P, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_window_attn(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_q) {
+    k_window_attn(const __grid_constant__ P p, const __grid_constant__ CUtensorMap tm_q,
+                  const int split) {
   constexpr bool kChunk = kIsChunk<P>, kTree = kIsTree<P>;
   // parts of the rows that the products can begin with
   constexpr int kParts = kChunk || kTree || kFp8 ? 1 : kMaxParts, kLast = kParts - 1;
@@ -212,8 +213,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int n_items = p.nq;
   if constexpr (kTree) n_items = p.n_items;
   else if (pair) n_items = (p.nq + 1) / 2;
-  const int item0 = (int)((int64_t)n_items * blockIdx.x / gridDim.x);
-  const int item1 = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+  // With few items each has `split` CTAs, which all make its S and softmax and a
+  // part of its output channels, 256 of them (or the 128 of a quarter) at a time.
+  const int part = (int)blockIdx.x % split;
+  const int item0 = split > 1 ? (int)blockIdx.x / split : (int)((int64_t)n_items * blockIdx.x / gridDim.x);
+  const int item1 = split > 1 ? item0 + 1 : (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+  const int width = split == 4 ? 128 : 256, ch0 = kHeadDim / split * part, ch1 = ch0 + kHeadDim / split;
   const int W = p.w.swa, F = p.w.n_first;
   // stages of Q: four of two boxes, or eight of one (the tensor core reads two
   // boxes' rows from each, those behind the first are of no account)
@@ -787,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMAs
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_bf16_f32(128, kSlots, false, false);
-      constexpr uint32_t id_o = idesc_bf16_f32(128, 256, false, true);
+      const uint32_t id_o = width == 256 ? idesc_bf16_f32(128, 256, false, true) : idesc_bf16_f32(128, 128, false, true);
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + kQOff), 16, 1024);
       const uint64_t d_k = sdesc_sw128(smem_u32(kv), 16, 1024);
       const uint64_t d_v = sdesc_sw128(smem_u32(kv), kBlk, 1024);
@@ -809,12 +814,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && c1 == 8) umma_commit(&sm.s_full);
       };
-      auto issue_o = [&](int h) {
+      auto issue_o = [&](int ch) {
         if (chunk > 0) ok = mbar_wait(&sm.o_empty, (chunk - 1) & 1, err);
         if (!ok) return;
         tc_fence_after();
         for (int ks = 0; ks < kSlots / 16; ++ks)
-          umma_bf16_ts(tmem + kOCol, tmem + kPCol + 8 * ks, d_v + ((4 * h * kBlk + ks * 2048) >> 4),
+          umma_bf16_ts(tmem + kOCol, tmem + kPCol + 8 * ks, d_v + ((ch / 64 * kBlk + ks * 2048) >> 4),
                        id_o, ks ? 1u : 0u);
         umma_commit(&sm.o_full);
         ++chunk;
@@ -823,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int item = item0; item < item1 && ok; ++item) {
         const uint32_t k = (uint32_t)(item - item0);
         ok = mbar_wait(&sm.p_full, k & 1, err);
-        if (ok) issue_o(0);
+        if (ok) issue_o(ch0);
         // half of the next S while the outputs' first half is read out, where the
         // rows stay as they are
         int c0 = 0;
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             c0 = 4;
           }
         }
-        if (ok) issue_o(1);
+        if (ok && split == 1) issue_o(256);
         if (ok) umma_commit(&sm.kv_empty[k & 1]);
         if (ok && item + 1 < item1) issue_s(item + 1, c0, 8);
       }
@@ -1003,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float L = l * am + (z == -INFINITY ? 0.0f : fast_exp2(z - M));
         inv = L == 0.0f ? 0.0f : am / L;
         if (bad) inv = NAN;
-        if (p.lse && half == 0)
+        if (p.lse && half == 0 && part == 0)
           p.lse[(int64_t)query_row(item, tk) * H + h] =
               inv != inv ? NAN
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
@@ -1014,25 +1019,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row touches 32 lines an instruction), the next ones on their way
       uint16_t* out = p.out + 8 * (lane & 3);
       if (live) out += ((int64_t)query_row(item, tk) * H + ((32 * quad) & (H - 1)) + (lane >> 2)) * kHeadDim;
-      for (int h = 0; h < 2; ++h, ++chunk) {
+      for (int ch = ch0; ch < ch1; ch += width, ++chunk) {
         ok = mbar_wait(&sm.o_full, chunk & 1, err) && ok;
         tc_fence_after();
-        const uint32_t from = tmem + lanes + kOCol + 128 * half;
+        const int mine = width / 2 * half;   // this warp's columns of the accumulator: mine ..
+        const uint32_t from = tmem + lanes + kOCol + mine;
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          const int c = 128 * half + 32 * b;      // column of the half
+        for (int b = 0; b < width / 64; ++b) {
+          const int c = ch + mine + 32 * b;       // channel
           uint32_t x[32];
           if (live) tmem_ld32(from + 32 * b, x);
-          if (b == 3) {
+          if (b == width / 64 - 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.o_empty);
           }
           if (!live) continue;
-          if (p.rope_out && h == 1 && c >= 192) {
+          if (p.rope_out && c >= 448) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 t = sm.rope[tk][(c - 192) / 2 + i];
+              const float2 t = sm.rope[tk][(c - 448) / 2 + i];
               const float u = __uint_as_float(x[2 * i]), v = __uint_as_float(x[2 * i + 1]);
               x[2 * i] = __float_as_uint(fmaf(u, t.x, -(v * t.y)));
               x[2 * i + 1] = __float_as_uint(fmaf(u, t.y, v * t.x));
@@ -1056,7 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row_ = 8 * i + (lane >> 2);
-              *reinterpret_cast<uint4*>(out + 8 * i * kHeadDim + 256 * h + c) = *reinterpret_cast<const uint4*>(
+              *reinterpret_cast<uint4*>(out + 8 * i * kHeadDim + c) = *reinterpret_cast<const uint4*>(
                   box + row_ * 64 + (((lane & 3) ^ ((row_ >> 1) & 3)) << 4));
             }
           }
@@ -1080,14 +1086,17 @@ cudaError_t launch(const P& p, const CUtensorMap& q, int items, int sms,
       k_window_attn<P, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
+  // CTAs an item: one sequence takes 11.5 us with four (13.8 with one), 70 take 12.9
+  // with two (14.6)
+  const int split = (int64_t)items * 4 <= sms ? 4 : (int64_t)items * 2 <= sms ? 2 : 1;
+  cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : items < sms ? items : sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_window_attn<P, kFp8>, p, q);
+  return cudaLaunchKernelEx(&cfg, k_window_attn<P, kFp8>, p, q, split);
 }
 
 }  // namespace
