@@ -29,7 +29,7 @@
 // the average's nodes and no more CTAs), with instructions, of which the exponentials
 // are the smaller part, and the joins of a cluster.  One chat
 // of 5 drafts over 32000 tokens: 8.7 us; 12 trees of 64 over 100003 tokens of fp32
-// without draft logits: 22 us.  Twice as many CTAs a sequence take 75 us for the
+// without draft logits: 20 us.  Twice as many CTAs a sequence take 75 us for the
 // mixed batch and a fifth longer for one of equal walks.
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
@@ -37,13 +37,13 @@
 namespace csa2 {
 namespace {
 
-// Blocks of 256 threads, two of them an SM, and clusters of up to 8: a batch's walks
+// Blocks of 256 threads, two of them an SM, and clusters of up to 16: a batch's walks
 // are of very different lengths, and with small shares the long ones have more SMs
 // left to them.
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 2;       // per SM
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 // What a pass gives: merged over a warp's lanes, then over all warps of the cluster.
 // `over(n, lane, scale)`: the merge of lanes 0 .. n - 1 (a power of two, the
@@ -149,7 +149,6 @@ struct Exact {   // a score in 64 bits
 
 constexpr int kPartWords = 4;
 constexpr int kParts = kMaxCluster * kWarps;   // warps of a cluster
-static_assert(kParts <= 64, "two parts a lane");
 struct Kid {       // a child of the node
   int32_t token;
   float u, lp, lq;
@@ -703,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     cluster_arrive();
     cluster_wait();
     x = lane < n_parts ? *reinterpret_cast<const Part*>(sm.part[par][lane]) : Part::none();
-    if (lane + 32 < n_parts) x.add(*reinterpret_cast<const Part*>(sm.part[par][lane + 32]), scale);
+    for (int i = lane + 32; i < n_parts; i += 32) x.add(*reinterpret_cast<const Part*>(sm.part[par][i]), scale);
     x.over(n_parts < 32 ? n_parts : 32, lane, scale);
     // (fewer parts than lanes: lane 0's)
     Part y;
@@ -743,11 +742,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
     }
     auto send_kids = [&] {
-      if (rank == 0 && warp < ctas) {
+      for (int to = rank == 0 ? warp : ctas; to < ctas; to += kWarps) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (parent[h] == node)
-            st_peer(&sm.kid[kid_par][lane + 32 * h], warp,
+            st_peer(&sm.kid[kid_par][lane + 32 * h], to,
                     Kid{token[h] >= 0 && token[h] < V ? token[h] : -1, uniform[h],
                         value_of<T>(lp[h]), value_of<T>(lq[h])});
       }
@@ -912,16 +911,22 @@ cudaError_t launch(const VerifyParams& p, int cluster, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  if (cluster > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(k_verify<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return cudaLaunchKernelEx(&cfg, k_verify<T>, p, cluster);
 }
 
 }  // namespace
 
 // CTAs of a sequence's cluster: as many as run at once over the whole GPU, with
-// a share of the vocabulary worth a pass each.
+// a share of the vocabulary worth a pass each.  Clusters of 16 (8 SMs of one of the
+// GPU's processing clusters) with room to spare, since they do not fill those: 8 trees of
+// 8 drafts over 131072 tokens take 25.6 us with 16 and 32.2 with 8, one 11.0 and 13.8.
 int verify_cluster(int64_t n_trees, int32_t vocab, int sms) {
   int c = 1;
-  while (c < kMaxCluster && n_trees * c * 2 <= (int64_t)sms * kBlocks && vocab >= 4096 * c) c *= 2;
+  while (c < kMaxCluster && n_trees * c * (c < 8 ? 2 : 3) <= (int64_t)sms * kBlocks && vocab >= 4096 * c) c *= 2;
   return c;
 }
 
