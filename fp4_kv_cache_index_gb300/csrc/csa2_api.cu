@@ -2178,6 +2178,10 @@ csa2_status_t csa2_window_append(const csa2_window_t* w, int32_t n_segs, const i
   if (total == 0) return CSA2_OK;
   if (!pos0 || !rows || !aligned8(pos0) || !aligned16(rows) || (rounded && !aligned16(rounded)))
     return CSA2_ERR_INVALID_ARG;
+  // in place, or apart: rows are read by the warps that round them
+  const uintptr_t from = reinterpret_cast<uintptr_t>(rows), to = reinterpret_cast<uintptr_t>(rounded);
+  if (rounded && to != from && (to < from ? from - to : to - from) < (uintptr_t)total * kHeadDim * 2)
+    return CSA2_ERR_INVALID_ARG;
   WinAppendParams* p = new (std::nothrow) WinAppendParams();
   if (!p) return CSA2_ERR_OOM;
   p->w = r;

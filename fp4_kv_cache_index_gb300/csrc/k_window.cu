@@ -124,9 +124,10 @@ __global__ void __launch_bounds__(kWarps * 32)
       seq = p.seq[seg];
     }
     const int64_t p0 = p.pos0[seg];
-    x[k] = p0 + in_seg;
-    to_ring[k] = p0 >= 0 && left <= w.swa ? ring_row(w, seq, x[k]) : -1;
-    to_first[k] = p0 >= 0 && x[k] < w.n_first ? first_row(w, seq, x[k]) : -1;
+    x[k] = (int64_t)((uint64_t)p0 + (uint64_t)in_seg);
+    const bool is = p0 >= 0 && in_seg <= INT64_MAX - p0;   // a position at all
+    to_ring[k] = is && left <= w.swa ? ring_row(w, seq, x[k]) : -1;
+    to_first[k] = is && x[k] < w.n_first ? first_row(w, seq, x[k]) : -1;
     need[k] = to_ring[k] >= 0 || to_first[k] >= 0 || p.rounded;
     if (!need[k]) continue;
     const uint4* src = reinterpret_cast<const uint4*>(p.rows + r * kHeadDim);

@@ -717,7 +717,8 @@ csa2_status_t csa2_window_reset(const csa2_window_t* w, int32_t seq, csa2_stream
  *   [n_segs];  rows: dev bf16 [sum n_rows, 512], at most 2^31 - 1 rows;
  *   rounded: nullable dev bf16 [sum n_rows, 512], all rows as the cache would
  *   hold them (bf16 holds them exactly), as csa2_window_attn_prefill reads
- *   them (may be `rows`).                                                   */
+ *   them (may be `rows`; CSA2_ERR_INVALID_ARG if it overlaps them otherwise).
+ *   Rows behind position 2^63 - 1 are not stored.                           */
 csa2_status_t csa2_window_append(const csa2_window_t* w, int32_t n_segs, const int32_t* seq_ids,
                                  const int32_t* n_rows, const int64_t* pos0, const void* rows,
                                  void* rounded, csa2_stream_t stream);

@@ -203,6 +203,28 @@ def test_large_tables():
         check(out[i], None, attend(q[i], got[i].double()))
 
 
+def test_rows_behind_the_last_position():
+    """Positions end at 2^63 - 1: rows behind it are rounded, and not stored."""
+    c = C()
+    win = c.Window(3, 4, 2, False)
+    win.rows.fill_(3.0)
+    top = 2 ** 63 - 1
+    rows = make_rows(9, 1)
+    rounded = torch.empty_like(rows)
+    # the newest four of the segment are 2^63 - 2 .. and two that are none
+    c.csa2_window_append(win, rows[:4].contiguous(), dev64([top - 1]), [4], [1], rounded=rounded[:4])
+    assert torch.equal(rounded[:4], rows[:4])
+    for x, row in ((top - 1, rows[0]), (top, rows[1])):
+        at = 4 + x % 4
+        assert win.pos[at].item() == x and torch.equal(win.rows[at], row)
+    kept = [4 + x % 4 for x in (top - 1, top)]
+    assert all((win.rows[r] == 3.0).all() for r in range(win.rows.shape[0]) if r not in kept)
+    q = make_q(1, 64, 2)
+    out = c.csa2_window_attn_decode(win, q, dev64([top]), SCALE, [1])
+    check(out[0], None, attend(q[0], rows[:2].double()))
+    assert win.device_error() == 0
+
+
 # ------------------------------------------------------------------ one token a sequence
 @pytest.mark.parametrize("heads,swa,n_first,fp8,extra", [
     (64, 128, 4, True, False), (64, 128, 0, False, True), (128, 128, 8, True, True),
@@ -246,6 +268,34 @@ def test_decode(heads, swa, n_first, fp8, extra):
     assert not out[none].any()
     assert torch.equal(lse[none], sink if extra else torch.full((heads,), -math.inf, device="cuda"))
     assert win.device_error() == 0
+
+
+@pytest.mark.parametrize("heads", [64, 128])
+def test_every_code_and_scale(heads):
+    """A query that sees one row answers that row: all codes but the NaNs, scales from
+    2^-126 to where bf16 ends, exact.  (Below, a bf16 has fewer bits.)"""
+    c = C()
+    code = torch.tensor([x for x in range(256) if x & 0x7F != 0x7F], dtype=torch.uint8, device="cuda")
+    # byte b: 2^(b - 127); the largest code is 448 < 2^9, the least 2^-9
+    bytes_ = [10, 64, 118, 127, 133, 134, 135, 136, 200, 244, 245]
+    win = c.Window(len(bytes_), 1)
+    win.codes.copy_(code.repeat(2)[:448].expand(len(bytes_), 448))
+    win.scales.copy_(torch.tensor(bytes_, dtype=torch.uint8, device="cuda")[:, None].expand(-1, 8))
+    win.rope.copy_(torch.randn(len(bytes_), 64, generator=gen(1), device="cuda"))
+    win.pos.zero_()
+    q = torch.zeros(len(bytes_), heads, 512, dtype=torch.bfloat16, device="cuda")
+    out = c.csa2_window_attn_decode(win, q, dev64([0] * len(bytes_)), SCALE)
+    x = code.repeat(2)[:448].long()
+    e, m, sign = (x >> 3) & 15, x & 7, 1.0 - 2.0 * (x >> 7).double()
+    power = ((e - 10 + 1023) << 52).view(torch.float64)   # 2^(e - 10), from its bits
+    value = sign * torch.where(e > 0, (8 + m).double() * power, m.double() * 2.0 ** -9)
+    for i, b in enumerate(bytes_):
+        want = torch.cat([value * 2.0 ** (b - 127), win.rope[i].double()])
+        assert torch.equal(out[i].double(), want.expand(heads, 512)), b
+    # the same rows of a tree's draft
+    tree = c.Tree([[-1]] * len(bytes_), [0] * len(bytes_))
+    again = c.csa2_window_attn_tree(win, tree, q, (win.codes, win.rope, win.scales), SCALE)
+    assert torch.equal(again, out)
 
 
 def test_rows_that_are_not_held_are_not_seen():

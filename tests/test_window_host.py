@@ -168,3 +168,11 @@ def test_verification(C):
         assert call(**bad) == INVALID, bad
     assert C.lib.csa2_verify_tree(t.ref, None, None) == INVALID
     assert C.lib.csa2_verify_tree(None, None, None) == INVALID
+
+
+@pytest.mark.parametrize("rows", [1, 100])
+def test_rounded_rows_lie_on_the_rows_or_apart(C, rows):
+    """Nothing is launched: a sequence's count of rows makes the call's."""
+    w, ref = window(C)
+    for off in (16, rows * 1024 - 16, -16, 16 - rows * 1024):
+        assert C.lib.csa2_window_append(ref, 1, None, ints([rows]), P, 2 * P, 2 * P + off, None) == INVALID
