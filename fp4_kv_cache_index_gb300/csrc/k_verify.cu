@@ -329,9 +329,11 @@ __device__ __forceinline__ void add_chunks(Sum& s, const Eight<T> (&l)[kN], floa
   s.z += z2.x + z2.y;
 }
 
-// Chunks of two rows that a thread has in flight.
-template <class T>
-constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
+// Chunks of two rows that a thread has in flight.  Few where a thread has two in all:
+// the code of a pass is then fetched for one use (5 drafts over 32000 tokens: 12.9 us,
+// with four 14.2; 64 sequences over 131072: 82 with four, 97 with two).
+template <class T, bool kSmall>
+constexpr int kRows = (kSmall ? 4 : 8) / (int)sizeof(T);
 
 // The CTA's share of one or two rows of logits (and of the noise) in chunks of
 // eight elements, kUnroll of them at a time: f(i0, x, y, z), chunk k the elements
@@ -405,12 +407,12 @@ __device__ __noinline__ double exact_score(bool leaf, float base, float temp, fl
 // registers (inlined into one kernel they spilled).
 
 // Of the logits: maxima and sums.
-template <class T>
+template <class T, bool kSmall>
 __device__ __forceinline__ Sums pass_sums(const T* tr, const T* dr, int32_t V, uint32_t rank,
                                           uint32_t ctas, float scale) {
   const uint64_t scale2 = pack2(scale, scale);
   Sums x = Sums::none();
-  for_rows<T, kRows<T>, false>(tr, dr, nullptr, V, rank, ctas,
+  for_rows<T, kRows<T, kSmall>, false>(tr, dr, nullptr, V, rank, ctas,
                                [&](auto&, auto& l, auto& d, auto&) {
                                  add_chunks(x.p, l, scale, scale2);
                                  if (dr) add_chunks(x.q, d, scale, scale2);
@@ -419,14 +421,14 @@ __device__ __forceinline__ Sums pass_sums(const T* tr, const T* dr, int32_t V, u
 }
 
 // The first largest logit.
-template <class T>
+template <class T, bool kSmall>
 __device__ __noinline__ Best pass_largest(const T* tr, int32_t V, uint32_t rank, uint32_t ctas) {
   Best x = Best::none();
-  for_rows<T, kRows<T>, false>(
+  for_rows<T, kRows<T, kSmall>, false>(
       tr, static_cast<const T*>(nullptr), nullptr, V, rank, ctas,
       [&](auto& i0, auto& l, auto&, auto&) {
 #pragma unroll
-        for (int j = 0; j < kRows<T>; ++j)
+        for (int j = 0; j < kRows<T, kSmall>; ++j)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float v = l[j].at(k);
@@ -441,17 +443,17 @@ __device__ __noinline__ Best pass_largest(const T* tr, int32_t V, uint32_t rank,
 }
 
 // What is left of p, sum max(p - a q, 0).
-template <class T>
+template <class T, bool kSmall>
 __device__ __noinline__ Total<float> pass_total(const T* tr, const T* dr, int32_t V, uint32_t rank,
                                                 uint32_t ctas, float scale, Sum sp, Sum sq, float a) {
   Total<float> y = {0.0f};
   const uint64_t bp = pack2(-sp.m, -sp.m), bq = pack2(-sq.m, -sq.m), scale2 = pack2(scale, scale);
   const float ip = 1.0f / sp.z, aq = a / sq.z;
-  for_rows<T, kRows<T>, false>(
+  for_rows<T, kRows<T, kSmall>, false>(
       tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
         float s = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kRows<T>; ++j)
+        for (int j = 0; j < kRows<T, kSmall>; ++j)
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float2 pe = exps(l[j].at(e), l[j].at(e + 1), bp, scale2);
@@ -540,10 +542,10 @@ struct Scores {
 };
 
 // The best score and the value of the second.
-template <class T>
+template <class T, bool kSmall>
 __device__ __noinline__ Best pass_token(const T* tr, const T* dr, const float* noise, int32_t V,
                                         uint32_t rank, uint32_t ctas, const Scores& sc) {
-  constexpr int kN = kRows<T> / 2;
+  constexpr int kN = kSmall ? 1 : kRows<T, false> / 2;
   Best x = Best::none();
   for_rows<T, kN, true>(
       tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
@@ -641,7 +643,7 @@ __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const 
   return kToken;
 }
 
-template <class T>
+template <class T, bool kSmall>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     k_verify(const __grid_constant__ VerifyParams p, const int ctas) {
   __shared__ Smem sm;
@@ -698,9 +700,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     const int par = pass & 1, n_parts = ctas * kWarps;
     ++pass;
     x.over(32, lane, scale);
-    if (lane < ctas) st_peer(sm.part[par][rank * kWarps + warp], lane, x);
-    cluster_arrive();
-    cluster_wait();
+    if (ctas == 1) {   // (a cluster's barrier takes 500 cycles longer)
+      if (lane == 0) *reinterpret_cast<Part*>(sm.part[par][warp]) = x;
+      __syncthreads();
+    } else {
+      if (lane < ctas) st_peer(sm.part[par][rank * kWarps + warp], lane, x);
+      cluster_arrive();
+      cluster_wait();
+    }
     x = lane < n_parts ? *reinterpret_cast<const Part*>(sm.part[par][lane]) : Part::none();
     for (int i = lane + 32; i < n_parts; i += 32) x.add(*reinterpret_cast<const Part*>(sm.part[par][i]), scale);
     x.over(n_parts < 32 ? n_parts : 32, lane, scale);
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     };
 
     if (greedy) {
-      Best x = pass_largest(tr, V, rank, ctas);
+      Best x = pass_largest<T, kSmall>(tr, V, rank, ctas);
       send_kids();
       x = join(x);
       take_kids();
@@ -781,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     int32_t n_removed = 0;
     uint32_t removed_bits[2] = {0u, 0u};   // of the removed tokens' last six bits
     if (!leaf) {
-      Sums x = pass_sums(tr, dr, V, rank, ctas, scale);
+      Sums x = pass_sums<T, kSmall>(tr, dr, V, rank, ctas, scale);
       send_kids();
       x = join(x);
       take_kids();
@@ -805,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           qk[h] = dr ? __fdividef(exp2f((kid[h].lq - sq.m) * scale), sq.z) : 1.0f;
         }
         while ((action = test_children<float>(s, dr, kid, pk, qk, lane)) == kSum) {
-          const Total<float> y = join(pass_total(tr, dr, V, rank, ctas, scale, sp, sq, s.a));
+          const Total<float> y = join(pass_total<T, kSmall>(tr, dr, V, rank, ctas, scale, sp, sq, s.a));
           if (y.t > 0.0f) s.b = y.t;
           else s.a = s.a_prev;
         }
@@ -869,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       sc.removed_bits[0] = removed_bits[0];
       sc.removed_bits[1] = removed_bits[1];
       sc.removed = sm.removed;
-      const Best top = join(pass_token(tr, dr, noise, V, rank, ctas, sc));
+      const Best top = join(pass_token<T, kSmall>(tr, dr, noise, V, rank, ctas, sc));
       if (leaf ? (top.bad || !(top.v > -INFINITY)) : !(top.v > 0.0f)) {
         // nothing is left: as before the last rejection
         if (dr && !again && left_a != left_a_prev) {
@@ -898,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   cluster_wait();
 }
 
-template <class T>
+template <class T, bool kSmall>
 cudaError_t launch(const VerifyParams& p, int cluster, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.n_trees * cluster));
@@ -912,10 +919,10 @@ cudaError_t launch(const VerifyParams& p, int cluster, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   if (cluster > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(k_verify<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(k_verify<T, kSmall>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return cudaLaunchKernelEx(&cfg, k_verify<T>, p, cluster);
+  return cudaLaunchKernelEx(&cfg, k_verify<T, kSmall>, p, cluster);
 }
 
 }  // namespace
@@ -933,7 +940,9 @@ int verify_cluster(int64_t n_trees, int32_t vocab, int sms) {
 cudaError_t launch_verify(const VerifyParams& p, bool fp32, int cluster, cudaStream_t s) {
   if (p.n_trees <= 0) return cudaSuccess;
   if (cluster < 1 || cluster > kMaxCluster) return cudaErrorInvalidValue;
-  return fp32 ? launch<float>(p, cluster, s) : launch<uint16_t>(p, cluster, s);
+  if (p.vocab <= 2 * 8 * kThreads * cluster)   // at most two chunks a thread
+    return fp32 ? launch<float, true>(p, cluster, s) : launch<uint16_t, true>(p, cluster, s);
+  return fp32 ? launch<float, false>(p, cluster, s) : launch<uint16_t, false>(p, cluster, s);
 }
 
 }  // namespace csa2
