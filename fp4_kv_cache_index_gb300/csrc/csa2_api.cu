@@ -2398,6 +2398,15 @@ csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t
       row += t->n_draft[i];
     }
     if (p->nq == 0) continue;
+    // The first item of a tree, and of a CTA, costs about half as much again (its rows
+    // come out of the cache): CTAs at a tree's border get fewer.  In halves of an item.
+    p->n_ctas = std::min({p->n_items, sms, kWinTreeCtas});
+    int b = 0;
+    for (int k = 0; k < p->n_items; ++k) {
+      const int64_t cost = 2 * k + p->tree[p->item[k] & 0x7FFF], all = 2 * p->n_items + p->tree[p->nq - 1] + 1;
+      while (b < p->n_ctas && cost * p->n_ctas >= b * all) p->start[b++] = (uint16_t)k;
+    }
+    while (b <= kWinTreeCtas) p->start[b++] = (uint16_t)p->n_items;
     const int64_t at = row0 * n_heads;
     p->lse = lse ? lse + at : nullptr;
     p->out = static_cast<uint16_t*>(out) + at * kHeadDim;

@@ -415,6 +415,7 @@ struct WinDecodeParams : WinAttnCommon {
 };
 constexpr int kWinTreeQueries = 1536;
 constexpr int kWinTreeTrees = 512;
+constexpr int kWinTreeCtas = 256;
 // Of a tree's two queries that share an item of 128 heads: drafts of the deeper
 // one's path that the other's has not.
 constexpr int kWinPairDrafts = 8;
@@ -429,6 +430,9 @@ struct WinTreeParams : WinAttnCommon {
   uint16_t query[kWinTreeQueries];    // its row of q and of the outputs
   uint16_t item[kWinTreeQueries];     // of an item: its first query; the top bit: it has two
   int32_t n_items;
+  // CTA b has items start[b] .. start[b + 1] - 1 (where an item has one CTA)
+  int32_t n_ctas;
+  uint16_t start[kWinTreeCtas + 1];
 };
 struct WinPrefillParams : WinAttnCommon {
   const uint16_t* band;

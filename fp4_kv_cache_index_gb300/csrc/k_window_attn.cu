@@ -216,8 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // With few items each has `split` CTAs, which all make its S and softmax and a
   // part of its output channels, 256 of them (or the 128 of a quarter) at a time.
   const int part = (int)blockIdx.x % split;
-  const int item0 = split > 1 ? (int)blockIdx.x / split : (int)((int64_t)n_items * blockIdx.x / gridDim.x);
-  const int item1 = split > 1 ? item0 + 1 : (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+  int item0 = (int)blockIdx.x / split, item1 = item0 + 1;
+  if (split == 1) {
+    if constexpr (kTree) {
+      item0 = p.start[blockIdx.x];
+      item1 = p.start[blockIdx.x + 1];
+    } else {
+      item0 = (int)((int64_t)n_items * blockIdx.x / gridDim.x);
+      item1 = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+    }
+  }
   const int width = split == 4 ? 128 : 256, ch0 = kHeadDim / split * part, ch1 = ch0 + kHeadDim / split;
   const int W = p.w.swa, F = p.w.n_first;
   // stages of Q: four of two boxes, or eight of one (the tensor core reads two
@@ -517,9 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and the first stores.
   auto listed_rows = [&](const Query& t, int par, int cb0, auto blocks, auto ready) {
     if constexpr (kTree) {
-      constexpr int kBlocks = decltype(blocks)::value, kFlight = kBlocks == 1 ? 4 : 8;
+      constexpr int kBlocks = decltype(blocks)::value, kFlight = 4;
       const int r8 = lane >> 2, c4 = lane & 3;
       const int n = sm.n_list[par], jobs = (n + 7) / 8 * kBlocks;
+      // whether any of these blocks' rows is marked in sm.bad_cb, or is to be
+      bool marks = lane < 5 * kBlocks && sm.bad_cb[cb0 + 2 * (lane / 5 % kBlocks)][lane % 5] != 0u;
       int j0 = 0;
 #pragma unroll 1
       do {
@@ -550,29 +560,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         bool bad[kFlight];
+        uint4* to[kFlight];
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
-          if (kFp8 && cb0 + 2 * (i % kBlocks) < 7) {
+          const int cb = cb0 + 2 * (i % kBlocks);
+          bad[i] = false;
+          if (kFp8 && cb < 7) {
             if (j0 + i < jobs) bad[i] = e4m3_sixteen(d[i], byte[i], d[i], e[i]);
           } else {
             bad[i] = not_finite(d[i]) || not_finite(e[i]);
             if (bad[i]) d[i] = e[i] = zero;
           }
+          marks |= bad[i];
+          // the second piece is 16 bytes away (codes) or 64, up or down
+          to[i] = piece(max(slot[i], 0), cb, kFp8 && cb < 7 ? 2 * c4 : c4);
         }
+        const bool mark = __any_sync(0xffffffffu, marks);
         if (j0 == 0) ready();
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
-          if (j0 + i >= jobs) break;
-          const int cb = cb0 + 2 * (i % kBlocks);
-          const int p0 = kFp8 && cb < 7 ? 2 * c4 : c4, p1 = kFp8 && cb < 7 ? 2 * c4 + 1 : 4 + c4;
-          const uint32_t any = __ballot_sync(0xffffffffu, bad[i]);
           if (slot[i] < 0) continue;
-          *piece(slot[i], cb, p0) = d[i];
-          *piece(slot[i], cb, p1) = e[i];
-          if (c4 == 0) {
-            const uint32_t bit = 1u << (slot[i] & 31);
-            if ((any >> lane) & 15u) atomicOr(&sm.bad_cb[cb][slot[i] >> 5], bit);
-            else atomicAnd(&sm.bad_cb[cb][slot[i] >> 5], ~bit);
+          const int turn = kFp8 && cb0 + 2 * (i % kBlocks) < 7 ? 1 : 4;
+          *to[i] = d[i];
+          *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(to[i]) ^ (uintptr_t)(16 * turn)) = e[i];
+        }
+        if (mark) {
+#pragma unroll 1
+          for (int i = 0; i < kFlight; ++i) {
+            const bool b = i == 0 ? bad[0] : i == 1 ? bad[1] : i == 2 ? bad[2] : bad[3];
+            const int at = i == 0 ? slot[0] : i == 1 ? slot[1] : i == 2 ? slot[2] : slot[3];
+            const uint32_t any = __ballot_sync(0xffffffffu, b);
+            if (at < 0 || c4 != 0) continue;
+            uint32_t* const word = &sm.bad_cb[cb0 + 2 * (i % kBlocks)][at >> 5];
+            if ((any >> lane) & 15u) atomicOr(word, 1u << (at & 31));
+            else atomicAnd(word, ~(1u << (at & 31)));
           }
         }
         j0 += kFlight;
@@ -1107,8 +1128,8 @@ cudaError_t launch_window_decode(const WinDecodeParams& p, const CUtensorMap& q,
 }
 
 cudaError_t launch_window_tree(const WinTreeParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
-  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, p.n_items, sms, s)
-                 : launch<WinTreeParams, false>(p, q, p.n_items, sms, s);
+  return p.w.fp8 ? launch<WinTreeParams, true>(p, q, p.n_items, sms < kWinTreeCtas ? sms : kWinTreeCtas, s)
+                 : launch<WinTreeParams, false>(p, q, p.n_items, sms < kWinTreeCtas ? sms : kWinTreeCtas, s);
 }
 
 cudaError_t launch_window_prefill(const WinPrefillParams& p, const CUtensorMap& q, int sms, cudaStream_t s) {
