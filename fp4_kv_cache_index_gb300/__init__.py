@@ -12,6 +12,7 @@ owns the device buffer of one CSA2 group's global cache and its handle.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import struct
@@ -230,7 +231,13 @@ def _stream(stream=None, device: Optional[int] = None):
 def _i32_array(xs: Optional[Sequence[int]]):
     if xs is None:
         return None
-    return (ctypes.c_int32 * len(xs))(*[int(x) for x in xs])
+    n = len(xs)
+    if n > 8 and isinstance(xs, (list, tuple)):
+        try:   # several times faster than one by one
+            return (ctypes.c_int32 * n).from_buffer(array.array("i", xs))
+        except (TypeError, OverflowError):
+            pass
+    return (ctypes.c_int32 * n)(*[int(x) for x in xs])
 
 
 def _i64_array(xs: Sequence[int]):
