@@ -135,6 +135,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 // once when there is no such predecessor).  Every kernel of this library
 // launched that way calls it before touching global memory.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// After the wait: lets the kernel behind this one be scheduled, for its set-up, as
+// soon as all blocks of this one run.  (It waits for this one's end as above.  Every
+// kernel launched that way has a block that waits, so its end comes after the end
+// of all kernels before it.)
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {

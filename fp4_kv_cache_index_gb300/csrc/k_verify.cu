@@ -25,7 +25,7 @@
 // is the one of 64-bit arithmetic, whatever the order of the sums.
 //
 // Measured: 64 sequences of up to 8 drafts over 131072 tokens, whose walks read 134
-// MB: 82 us.  The SMs are busy for 55 % of that (the longest walks have more than twice
+// MB: 80 us.  The SMs are busy for 55 % of that (the longest walks have more than twice
 // the average's nodes and no more CTAs), with instructions, of which the exponentials
 // are the smaller part, and the joins of a cluster.  One chat
 // of 5 drafts over 32000 tokens: 8.7 us; 12 trees of 64 over 100003 tokens of fp32
@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   for (int h = 0; h < 2; ++h) parent[h] = lane + 32 * h < n ? p.parent[d0 + lane + 32 * h] : -2;
   const int halves = n > 32 ? 2 : 1;
   griddep_wait();
+  griddep_launch();
   // the first CTA's: their tokens and numbers
   int32_t token[2] = {-1, -1};
   float uniform[2] = {0.0f, 0.0f};

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     seg = lo;
   }
   griddep_wait();
+  griddep_launch();
   const WinRows& w = p.w;
   uint4 a[kRows], b[kRows];
   int64_t x[kRows], to_ring[kRows], to_first[kRows];   // its position; rows of the cache, or -1
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int32_t seg = (int32_t)(i / per), j = (int32_t)(i - (int64_t)seg * per);
   const int32_t seq = p.identity ? p.seq0 + seg : p.seq[seg];
   griddep_wait();
+  griddep_launch();
   const int64_t end = p.end[seg];
   const bool first = j >= p.n_rows;
   const int64_t lo = end > p.n_rows ? end - p.n_rows : 0;
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   __shared__ int32_t path[64];   // the path's drafts, the accepted one first
   __shared__ int32_t len_s;
   griddep_wait();
+  griddep_launch();
   if (threadIdx.x == 0) {
     int32_t t = p.accepted[tree], len = 0;
     if (t < 0 || t >= n) t = -1;

@@ -27,12 +27,12 @@
 // drafts.)
 //
 // What bounds it.  The chunk: HBM, q in and the outputs out (8192 tokens of 64 heads
-// are 1.08 GB: 215 us, 74 % of the copy rate); an item's S (32 MMAs of 155 cycles,
+// are 1.08 GB: 214 us, 74 % of the copy rate); an item's S (32 MMAs of 155 cycles,
 // which read Q and the rows from shared memory), softmax, products and stores are a
 // chain of which only half of the next S and the second half of the stores run
 // beside something else.  Decode: the same chain once (27000 cycles, of which the
-// rows 11000, S 5000, the softmax 3000, products and outputs 5000): 14.5 us for 128
-// sequences; for one, four CTAs share the outputs: 11.5 us.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
+// rows 11000, S 5000, the softmax 3000, products and outputs 5000): 14.2 us for 128
+// sequences; for one, four CTAs share the outputs: 10.7 us.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
 // Trees: 1024 drafts 50 us, three to four items a CTA.
 //
 // Code is fetched cold by most CTAs, once for each instruction that a single pass
@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   griddep_wait();
+  griddep_launch();
   uint32_t* err = p.err;
 
   // warps that load rows: 0 and 1, and of a cache (and a chunk's first window)
@@ -1107,8 +1108,8 @@ cudaError_t launch(const P& p, const CUtensorMap& q, int items, int sms,
       k_window_attn<P, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  // CTAs an item: one sequence takes 11.5 us with four (13.8 with one), 70 take 12.9
-  // with two (14.6)
+  // CTAs an item: one sequence takes 11.5 us with four where it takes 13.8 with one,
+  // 70 take 12.9 with two (14.6 with one)
   const int split = (int64_t)items * 4 <= sms ? 4 : (int64_t)items * 2 <= sms ? 2 : 1;
   cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : items < sms ? items : sms));
   cfg.blockDim = dim3(kThreads);
