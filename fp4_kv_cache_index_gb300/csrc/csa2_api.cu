@@ -2403,7 +2403,8 @@ csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t
     p->n_ctas = std::min({p->n_items, sms, kWinTreeCtas});
     int b = 0;
     for (int k = 0; k < p->n_items; ++k) {
-      const int64_t cost = 2 * k + p->tree[p->item[k] & 0x7FFF], all = 2 * p->n_items + p->tree[p->nq - 1] + 1;
+      int64_t cost = 2 * k + p->tree[p->item[k] & 0x7FFF], all = 2 * p->n_items + p->tree[p->nq - 1] + 1;
+      if (p->n_ctas == p->n_items) cost = k, all = p->n_items;   // one each
       while (b < p->n_ctas && cost * p->n_ctas >= b * all) p->start[b++] = (uint16_t)k;
     }
     while (b <= kWinTreeCtas) p->start[b++] = (uint16_t)p->n_items;

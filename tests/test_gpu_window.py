@@ -744,3 +744,22 @@ def test_refusals():
     assert c.csa2_window_attn_decode(none, q[:0], pos[:0], SCALE).shape == (0, 64, 512)
     assert c.csa2_window_attn_prefill(q[:0], 0, rows[:0], 0, SCALE).shape == (0, 64, 512)
     assert win.device_error() == 0
+
+
+@pytest.mark.parametrize("n_trees,drafts", [(50, 4), (150, 1), (40, 9), (300, 3)])
+def test_items_over_the_multiprocessors(n_trees, drafts):
+    """About as many items as multiprocessors, fewer and more: each draft is answered."""
+    c = C()
+    parents = [random_tree(drafts, i) for i in range(n_trees)]
+    tree = c.Tree(parents, [20 + i for i in range(n_trees)])
+    win, model = c.Window(n_trees, 16), Model(n_trees, 16, 0, True)
+    before = make_rows(n_trees * 16, 1)
+    c.csa2_window_append(win, before, dev64([4 + i for i in range(n_trees)]), [16] * n_trees)
+    model.append(before, [4 + i for i in range(n_trees)], [16] * n_trees, range(n_trees))
+    q, rows = make_q(tree.n_queries, 64, 2), make_rows(tree.n_queries, 3)
+    out = torch.full_like(q, 7.0)
+    c.csa2_window_attn_tree(win, tree, q, c.csa2_swa_fp8_quantise(rows), SCALE, out=out)
+    for i in range(n_trees):
+        for t in range(drafts):
+            x = i * drafts + t
+            check(out[x], None, attend(q[x], tree_rows(model, tree, i, t, rows, i * drafts)))
