@@ -18,6 +18,10 @@
 // cluster's first CTA and taken from its shared memory by all, so that all
 // come to the same barriers.
 //
+// Where the two rows are alike and a child's token is masked in both, it is rejected and
+// max(p - a q, 0) is 0 everywhere: a and b then stay as they are.  So that this is seen,
+// the two products of a difference are rounded alike, never fused.
+//
 // Sums and tests in fp32 (64 bits take 64 times as long here).  A test whose two
 // sides are nearer to each other than fp32 can tell is made again, with its
 // node's sums, in 64 bits; likewise the token: if the second best score is that
@@ -298,6 +302,13 @@ struct Eight {
   }
 };
 
+// What is left of a token, max(p - a q, 0).  Both products are rounded before they are
+// subtracted: where p = a q they are the same bits and nothing is left, as the walk has
+// to know.  (These are never contracted; products and sums in pairs were.)
+__device__ __forceinline__ float left(float pe, float qe, float ip, float aq) {
+  return fmaxf(__fsub_rn(__fmul_rn(pe, ip), __fmul_rn(qe, aq)), 0.0f);
+}
+
 // exp2((x - base) * scale) of two values.
 __device__ __forceinline__ float2 exps(float x, float y, uint64_t neg_base, uint64_t scale2) {
   const float2 d = unpack2(mul2(add2(pack2(x, y), neg_base), scale2));
@@ -458,7 +469,7 @@ __device__ __noinline__ Total<float> pass_total(const T* tr, const T* dr, int32_
           for (int e = 0; e < 8; e += 2) {
             const float2 pe = exps(l[j].at(e), l[j].at(e + 1), bp, scale2);
             const float2 qe = exps(d[j].at(e), d[j].at(e + 1), bq, scale2);
-            s += fmaxf(fmaf(pe.x, ip, -qe.x * aq), 0.0f) + fmaxf(fmaf(pe.y, ip, -qe.y * aq), 0.0f);
+            s += left(pe.x, qe.x, ip, aq) + left(pe.y, qe.y, ip, aq);
           }
         y.t += s;
       });
@@ -488,8 +499,8 @@ __device__ __noinline__ Total<double> pass_total64(const T* tr, const T* dr, int
   for_rows<T, 1, false>(tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      y.t += fmax(exp2_64(((double)l[0].at(k) - (double)mp) * scale) * ip -
-                      exp2_64(((double)d[0].at(k) - (double)mq) * scale) * aq,
+      y.t += fmax(__dsub_rn(__dmul_rn(exp2_64(((double)l[0].at(k) - (double)mp) * scale), ip),
+                            __dmul_rn(exp2_64(((double)d[0].at(k) - (double)mq) * scale), aq)),
                   0.0);
   });
   return y;
@@ -525,8 +536,8 @@ struct Scores {
       v[k + 1] = pe.y * ip;
       if (two) {
         const float2 qe = exps(d.at(k), d.at(k + 1), bq, scale2);
-        v[k] = fmaxf(v[k] - qe.x * aq, 0.0f);
-        v[k + 1] = fmaxf(v[k + 1] - qe.y * aq, 0.0f);
+        v[k] = left(pe.x, qe.x, ip, aq);
+        v[k + 1] = left(pe.y, qe.y, ip, aq);
       }
       v[k] = __fdividef(v[k], e.at(k));
       v[k + 1] = __fdividef(v[k + 1], e.at(k + 1));
