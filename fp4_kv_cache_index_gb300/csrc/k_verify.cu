@@ -24,9 +24,11 @@
 //
 // Sums and tests in fp32 (64 bits take 64 times as long here).  A test whose two
 // sides are nearer to each other than fp32 can tell is made again, with its
-// node's sums, in 64 bits; likewise the token: if the second best score is that
-// near the best, all such candidates are scored again in 64 bits.  So the result
-// is the one of 64-bit arithmetic, whatever the order of the sums.
+// node's sums, in 64 bits.  Of the token's scores fp32 gives bounds, p and a q each a
+// few 1e-5 of itself off: if another token's upper bound reaches the best one's lower
+// bound (always, where p and a q all but cancel), the node's sums and tests are made
+// again in 64 bits, if they were not yet, and all such tokens are scored with those.
+// So the result is the one of 64-bit arithmetic, whatever the order of the sums.
 //
 // Measured: 64 sequences of up to 8 drafts over 131072 tokens, whose walks read 134
 // MB: 80 us.  The SMs are busy for 55 % of that (the longest walks have more than twice
@@ -35,6 +37,8 @@
 // of 5 drafts over 32000 tokens: 8.7 us; 12 trees of 64 over 100003 tokens of fp32
 // without draft logits: 20 us.  Twice as many CTAs a sequence take 75 us for the
 // mixed batch and a fifth longer for one of equal walks.
+#include <type_traits>
+
 #include "csa2_device.cuh"
 #include "csa2_kernels.h"
 
@@ -115,6 +119,29 @@ struct Best {
   }
   __device__ static Best none() { return {-INFINITY, -INFINITY, -1, 0u}; }
 };
+// Of the scores of what is left at a node: the largest upper bound, whose it is, the
+// second largest, and a lower bound of the first one's score.
+struct Most {
+  float v, second;
+  int32_t i;
+  float low;
+  __device__ __forceinline__ void add(const Most& b, float) {
+    const bool first = v > b.v || (v == b.v && (uint32_t)i < (uint32_t)b.i);
+    second = fmaxf(fmaxf(second, b.second), first ? b.v : v);
+    if (!first) {
+      v = b.v;
+      i = b.i;
+      low = b.low;
+    }
+  }
+  __device__ __forceinline__ void over(int n, int, float scale) {
+    for (int o = n / 2; o > 0; o >>= 1)
+      add({__shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, second, o),
+           __shfl_xor_sync(0xffffffffu, i, o), __shfl_xor_sync(0xffffffffu, low, o)},
+          scale);
+  }
+  __device__ static Most none() { return {-INFINITY, -INFINITY, -1, 0.0f}; }
+};
 template <class Real>
 struct Total {
   Real t;
@@ -164,6 +191,7 @@ enum Action { kSum, kExact, kGo, kToken, kEnd };
 template <class Real>
 struct Tests {
   Real a, a_prev, b;
+  float eps;                 // fp32: what p and a q are good to
   uint64_t todo;             // children that are still to be tested
   int32_t taken;
   int32_t removed[2], n_removed;   // lane r: removed tokens r and r + 32
@@ -175,6 +203,7 @@ struct Smem {
   alignas(16) Kid kid[2][64];
   float temperature;
   int32_t removed[64];       // for the last pass
+  double left_a[2], z[2];    // a, before the last rejection too, and the sums in 64 bits
 };
 
 // 16 bytes or less to `local` of another CTA of the cluster.
@@ -229,13 +258,16 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 2^x in 64 bits, good to 2e-11: the Taylor series of e^r, |r| <= ln 2 / 2, to
-// the ninth power (the next term is (ln 2 / 2)^10 / 10! = 7e-12).  The one of
-// the library takes three times as long, on a path of single threads.
+// 2^x in 64 bits, to their rounding: the Taylor series of e^r, |r| <= ln 2 / 2, to the
+// 13th power (the next term is (ln 2 / 2)^14 / 14! = 4e-18).
 __device__ __forceinline__ double exp2_64(double x) {
   if (!(x > -1000.0)) return x == x ? 0.0 : x;
   const double n = rint(x), r = (x - n) * 0.693147180559945309;
-  double s = 1.0 / 362880;
+  double s = 1.0 / 6227020800.0;
+  s = fma(s, r, 1.0 / 479001600);
+  s = fma(s, r, 1.0 / 39916800);
+  s = fma(s, r, 1.0 / 3628800);
+  s = fma(s, r, 1.0 / 362880);
   s = fma(s, r, 1.0 / 40320);
   s = fma(s, r, 1.0 / 5040);
   s = fma(s, r, 1.0 / 720);
@@ -404,13 +436,27 @@ __device__ __forceinline__ void for_rows(const T* a, const T* b, const float* c,
   }
 }
 
-// What is left of a token in 64 bits, over its noise; a leaf's relative to 2^base.
-__device__ __noinline__ double exact_score(bool leaf, float base, float temp, float l, const Sum& sp,
-                                           bool two, float d, const Sum& sq, double a, float e) {
-  const double c = 1.4426950408889634 / (double)temp;
-  if (leaf) return exp2((double)l * c - floor((double)base)) / (double)e;
-  double s = exp2(((double)l - (double)sp.m) * c) / (double)sp.z;
-  if (two) s = fmax(s - a * (exp2(((double)d - (double)sq.m) * c) / (double)sq.z), 0.0);
+// Logits to log2 units.  A function so that it is not computed ahead, where fp32 will do.
+__device__ __noinline__ double scale_64(float temp) { return 1.4426950408889634 / (double)temp; }
+
+__device__ __forceinline__ double probability_64(float l, float m, double scale, double z) {
+  return exp2(((double)l - (double)m) * scale) / z;
+}
+
+// A leaf's p over its noise in 64 bits, relative to 2^base.
+__device__ __noinline__ double exact_leaf(float base, double scale, float l, float e) {
+  return exp2((double)l * scale - floor((double)base)) / (double)e;
+}
+// What is left of a token in 64 bits, over its noise.
+struct Left64 {
+  double scale, ip, aq;      // 1 / z and a / z of the two rows
+  float mp, mq;
+  bool two;
+};
+__device__ __noinline__ double exact_left(const Left64& n, float l, float d, float e) {
+  double s = __dmul_rn(exp2_64(((double)l - (double)n.mp) * n.scale), n.ip);
+  if (n.two)
+    s = fmax(__dsub_rn(s, __dmul_rn(exp2_64(((double)d - (double)n.mq) * n.scale), n.aq)), 0.0);
   return s / (double)e;
 }
 
@@ -506,64 +552,72 @@ __device__ __noinline__ Total<double> pass_total64(const T* tr, const T* dr, int
   return y;
 }
 
-// The scores of the last pass: in log2 units where no sum is known (a leaf),
-// else what is left over the noise.
+// The scores of the last pass.  A leaf's in log2 units (no sum is known), the others'
+// as upper bounds of what is left over the noise: p good to a part eps of itself makes
+// that p (1 + eps) - a q (1 - eps).
 struct Scores {
-  bool leaf, two;
-  float scale, ip, aq;
-  Sum sp;
-  float mq;
+  float scale;
+  bool two;                 // the rest: not of a leaf
+  float mp, mq, ip, aq;     // for the upper bound
+  float ip_low, aq_high;    // for the lower one
   int32_t n_removed;
   uint32_t removed_bits[2];
   const int32_t* removed;   // in shared memory
-  template <class T>
+  template <bool kLeaf, class T>
   __device__ __forceinline__ void of(int32_t i0, const Eight<T>& l, const Eight<T>& d,
                                      const Eight<float>& e, float (&v)[8], uint32_t& bad) const {
-    if (leaf) {
+    if constexpr (kLeaf) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float lk = l.at(k);
         if (!(lk < INFINITY)) bad = 1u;
         v[k] = fmaf(lk, scale, -__log2f(e.at(k)));
       }
-      return;
-    }
-    const uint64_t bp = pack2(-sp.m, -sp.m), bq = pack2(-mq, -mq), scale2 = pack2(scale, scale);
+    } else {
+      const uint64_t bp = pack2(-mp, -mp), bq = pack2(-mq, -mq), scale2 = pack2(scale, scale);
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float2 pe = exps(l.at(k), l.at(k + 1), bp, scale2);
-      v[k] = pe.x * ip;
-      v[k + 1] = pe.y * ip;
-      if (two) {
-        const float2 qe = exps(d.at(k), d.at(k + 1), bq, scale2);
-        v[k] = left(pe.x, qe.x, ip, aq);
-        v[k + 1] = left(pe.y, qe.y, ip, aq);
+      for (int k = 0; k < 8; k += 2) {
+        const float2 pe = exps(l.at(k), l.at(k + 1), bp, scale2);
+        v[k] = pe.x * ip;
+        v[k + 1] = pe.y * ip;
+        if (two) {
+          const float2 qe = exps(d.at(k), d.at(k + 1), bq, scale2);
+          v[k] = fmaxf(v[k] - qe.x * aq, 0.0f);
+          v[k + 1] = fmaxf(v[k + 1] - qe.y * aq, 0.0f);
+        }
+        v[k] = __fdividef(v[k], e.at(k));
+        v[k + 1] = __fdividef(v[k + 1], e.at(k + 1));
       }
-      v[k] = __fdividef(v[k], e.at(k));
-      v[k + 1] = __fdividef(v[k + 1], e.at(k + 1));
-    }
-    if (n_removed) {
+      if (n_removed) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if ((removed_bits[((i0 + k) >> 5) & 1] >> ((i0 + k) & 31)) & 1u)
-          for (int r = 0; r < n_removed; ++r)
-            if (removed[r] == i0 + k) v[k] = 0.0f;
+        for (int k = 0; k < 8; ++k)
+          if ((removed_bits[((i0 + k) >> 5) & 1] >> ((i0 + k) & 31)) & 1u)
+            for (int r = 0; r < n_removed; ++r)
+              if (removed[r] == i0 + k) v[k] = -1.0f;
+      }
     }
+  }
+  // the least that is left of a token
+  __device__ __forceinline__ float low(float l, float d, float e) const {
+    float s = fast_exp2((l - mp) * scale) * ip_low;
+    if (two) s = fmaxf(s - fast_exp2((d - mq) * scale) * aq_high, 0.0f);
+    return __fdividef(s, e);
   }
 };
 
 // The best score and the value of the second.
-template <class T, bool kSmall>
-__device__ __noinline__ Best pass_token(const T* tr, const T* dr, const float* noise, int32_t V,
+template <class T, bool kSmall, bool kLeaf>
+__device__ __noinline__ auto pass_token(const T* tr, const T* dr, const float* noise, int32_t V,
                                         uint32_t rank, uint32_t ctas, const Scores& sc) {
   constexpr int kN = kSmall ? 1 : kRows<T, false> / 2;
-  Best x = Best::none();
+  std::conditional_t<kLeaf, Best, Most> x = decltype(x)::none();
+  uint32_t bad = 0u;
   for_rows<T, kN, true>(
       tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
           float v[8];
-          sc.of(i0[j], l[j], d[j], e[j], v, x.bad);
+          sc.of<kLeaf>(i0[j], l[j], d[j], e[j], v, bad);
           float m = v[0];
 #pragma unroll
           for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
@@ -584,31 +638,43 @@ __device__ __noinline__ Best pass_token(const T* tr, const T* dr, const float* n
           }
         }
       });
+  // (the best one's numbers are read again: keeping them took the batch from 80 to 84 us)
+  if constexpr (kLeaf) x.bad = bad;
+  else if (x.i >= 0)
+    x.low = sc.low(value_of<T>(bits_now(tr, x.i)), sc.two ? value_of<T>(bits_now(dr, x.i)) : 0.0f,
+                   __ldg(noise + x.i));
   return x;
 }
 
-// Again, the candidates from `near` up in 64 bits.
-template <class T>
+// Again, the candidates from `near` up in 64 bits (of a leaf: with scale n.scale, relative
+// to 2^top).
+template <class T, bool kLeaf>
 __device__ __noinline__ Exact pass_near(const T* tr, const T* dr, const float* noise, int32_t V,
                                         uint32_t rank, uint32_t ctas, const Scores& sc, float top,
-                                        float near, float temp, Sum sq, double a) {
+                                        float near, const Left64& n) {
   Exact best = Exact::none();
   for_rows<T, 1, true>(
       tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
         float v[8];
         uint32_t bad;
-        sc.of(i0[0], l[0], d[0], e[0], v, bad);
+        sc.of<kLeaf>(i0[0], l[0], d[0], e[0], v, bad);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int32_t i = i0[0] + k;
           if (!(v[k] >= near) || i < 0 || i >= V) continue;
-          const double s = exact_score(sc.leaf, top, temp, l[0].at(k), sc.sp, sc.two,
-                                       sc.two ? d[0].at(k) : 0.0f, sq, a, e[0].at(k));
+          const double s = kLeaf ? exact_leaf(top, n.scale, l[0].at(k), e[0].at(k))
+                                 : exact_left(n, l[0].at(k), d[0].at(k), e[0].at(k));
           best.add({s, i, 0}, 0.0f);
         }
       });
   return best;
 }
+
+// fp32's probabilities are good to 2e-6 of themselves (of a token 2^-30 as likely as the
+// first; to 1.1e-5 down to 2^-126), b to 2e-6 of 1 + a, and a to the sum of its b's: tests
+// with a margin of kEps and, for each rejection, kEpsMore are the right ones, bounds of
+// scores the right ones with kEpsLow on top.
+constexpr float kEps = 1e-5f, kEpsMore = 4e-6f, kEpsLow = 1e-5f;
 
 // Tests of the children in `todo`, in call order, by a whole warp (every warp of
 // the cluster does the same): lane k has what belongs to children k and k + 32;
@@ -628,11 +694,9 @@ __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const 
     // certain drafts: nothing is left of a token that was removed
     if (!two && __any_sync(0xffffffffu, s.removed[0] == t || s.removed[1] == t)) continue;
     const Real x = uk * qk * s.b, y = two ? pk - s.a * qk : pk;
-    // the probabilities are good to 2e-6 of themselves (of a token 2^-30 as likely
-    // as the first), a and b to 2e-6 (1 + a)
     if (kFast) {
       const float near = two ? (s.a + uk * (1.0f + s.a)) * qk : uk;
-      if (fabsf((float)(x - y)) <= 1e-5f * (float)(pk + near)) return kExact;
+      if (fabsf((float)(x - y)) <= s.eps * (float)(pk + near)) return kExact;
     }
     if (x < y) {
       s.taken = k;
@@ -641,6 +705,7 @@ __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const 
     if (two) {
       s.a_prev = s.a;
       s.a += s.b;
+      s.eps += kEpsMore;
       if (s.todo) return kSum;           // else the sum that is left is not needed
     } else if (s.b - pk > Real(0)) {
       s.b -= pk;
@@ -734,7 +799,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 
   int node = -1, last = -1;
   int32_t result = -1;
-  bool first = true;
+  // the node is gone through again with its numbers in 64 bits, where fp32 cannot tell
+  // (the whole of it: nothing is kept for that, and nothing of it computed ahead)
+  bool first = true, exact = false;
   if (!root) {
     // the root's only child is the token that the last step has drawn
     if (n > 0) node = last = 0;
@@ -796,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 
     // what is left at the node
     Sum sp = {0.0f, 1.0f}, sq = {0.0f, 1.0f};
-    float left_a = 0.0f, left_a_prev = 0.0f;
+    float left_a = 0.0f, left_a_prev = 0.0f, eps = kEps;
     int32_t n_removed = 0;
     uint32_t removed_bits[2] = {0u, 0u};   // of the removed tokens' last six bits
     if (!leaf) {
@@ -811,11 +878,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (dr && !(x.q.z < INFINITY && x.q.m > -INFINITY)) break;
       sp = x.p;
       if (dr) sq = x.q;
-      // ---- tests; those too near to call again with numbers in 64 bits
       Action action;
       int32_t taken, removed[2];
-      {
-        Tests<float> s = {0.0f, 0.0f, 1.0f, kids, -1, {-1, -1}, 0};
+      if (!exact) {
+        Tests<float> s = {0.0f, 0.0f, 1.0f, kEps, kids, -1, {-1, -1}, 0};
         float pk[2] = {0.0f, 0.0f}, qk[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -824,26 +890,30 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           qk[h] = dr ? __fdividef(exp2f((kid[h].lq - sq.m) * scale), sq.z) : 1.0f;
         }
         while ((action = test_children<float>(s, dr, kid, pk, qk, lane)) == kSum) {
-          const Total<float> y = join(pass_total<T, kSmall>(tr, dr, V, rank, ctas, scale, sp, sq, s.a));
-          if (y.t > 0.0f) s.b = y.t;
-          else s.a = s.a_prev;
+          const Total<float> y =
+              join(pass_total<T, kSmall>(tr, dr, V, rank, ctas, scale, sp, sq, s.a));
+          s.b = y.t;
+          if (!(y.t > s.eps * (1.0f + s.a))) {   // that may be nothing, or a part of it
+            action = kExact;
+            break;
+          }
         }
         taken = s.taken;
         left_a = s.a;
         left_a_prev = s.a_prev;
+        eps = s.eps;
         n_removed = s.n_removed;
         removed[0] = s.removed[0];
         removed[1] = s.removed[1];
-      }
-      if (action == kExact) {
-        const double c = 1.4426950408889634 / (double)temp;
+      } else {
+        const double c = scale_64(temp);
         const Sums64 z = join(pass_sums64(tr, dr, V, rank, ctas, c, sp.m, sq.m));
-        Tests<double> s = {0.0, 0.0, 1.0, kids, -1, {-1, -1}, 0};
+        Tests<double> s = {0.0, 0.0, 1.0, kEps, kids, -1, {-1, -1}, 0};
         double pk[2], qk[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          pk[h] = exp2(((double)kid[h].lp - (double)sp.m) * c) / z.p;
-          qk[h] = dr ? exp2(((double)kid[h].lq - (double)sq.m) * c) / z.q : 1.0;
+          pk[h] = probability_64(kid[h].lp, sp.m, c, z.p);
+          qk[h] = dr ? probability_64(kid[h].lq, sq.m, c, z.q) : 1.0;
         }
         while ((action = test_children<double>(s, dr, kid, pk, qk, lane)) == kSum) {
           const Total<double> y =
@@ -857,9 +927,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         n_removed = s.n_removed;
         removed[0] = s.removed[0];
         removed[1] = s.removed[1];
+        if (tid == 0) {
+          sm.left_a[0] = s.a;
+          sm.left_a[1] = s.a_prev;
+          sm.z[0] = z.p;
+          sm.z[1] = z.q;
+        }
+        __syncthreads();
+      }
+      if (action == kExact) {
+        exact = true;
+        continue;
       }
       if (action == kGo) {
         node = last = taken;
+        exact = false;
         continue;
       }
       if (n_removed) {
@@ -873,40 +955,55 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
 
     // ---- the next token
-    bool again = false;
-    while (true) {
-      Scores sc;
-      sc.leaf = leaf;
-      sc.two = dr != nullptr;
-      sc.scale = scale;
-      sc.sp = sp;
-      sc.ip = 1.0f / sp.z;
-      sc.mq = sq.m;
-      const float a = again ? left_a_prev : left_a;
-      sc.aq = dr ? a / sq.z : 0.0f;
-      sc.n_removed = n_removed;
-      sc.removed_bits[0] = removed_bits[0];
-      sc.removed_bits[1] = removed_bits[1];
-      sc.removed = sm.removed;
-      const Best top = join(pass_token<T, kSmall>(tr, dr, noise, V, rank, ctas, sc));
-      if (leaf ? (top.bad || !(top.v > -INFINITY)) : !(top.v > 0.0f)) {
-        // nothing is left: as before the last rejection
-        if (dr && !again && left_a != left_a_prev) {
-          again = true;
-          continue;
-        }
-        break;
-      }
+    Scores sc;
+    sc.scale = scale;
+    sc.two = dr != nullptr;
+    sc.mp = sp.m;
+    sc.mq = sq.m;
+    sc.n_removed = n_removed;
+    sc.removed_bits[0] = removed_bits[0];
+    sc.removed_bits[1] = removed_bits[1];
+    sc.removed = sm.removed;
+    if (leaf) {
+      const Best top = join(pass_token<T, kSmall, true>(tr, dr, noise, V, rank, ctas, sc));
+      if (top.bad || !(top.v > -INFINITY)) break;
       result = top.i;
-      // candidates that the fp32 scores may have in the wrong order: a leaf's
-      // are off by a few 2^-24 of the logit in log2 units, the others by less
-      // than 2^-14 of themselves unless p and a q are all but equal
-      const float near = leaf ? top.v - 2e-6f * (fabsf(top.v) + 256.0f) : top.v * (1.0f - 1e-4f);
+      // candidates that the fp32 scores may have in the wrong order: these are off by
+      // a few 2^-24 of the logit in log2 units
+      const float near = top.v - 2e-6f * (fabsf(top.v) + 256.0f);
       if (top.second >= near)
-        result = join(pass_near(tr, dr, noise, V, rank, ctas, sc, top.v, near, temp, sq, a)).i;
+        result = join(pass_near<T, true>(tr, dr, noise, V, rank, ctas, sc, top.v, near,
+                                         {scale_64(temp), 0.0, 0.0, 0.0f, 0.0f, false})).i;
       break;
     }
-    break;
+    eps += kEpsLow;
+    bool again = false;      // nothing is left: as before the last rejection
+    while (true) {
+      const float ip = 1.0f / sp.z, aq = dr ? (again ? left_a_prev : left_a) / sq.z : 0.0f;
+      sc.ip = ip * (1.0f + eps);
+      sc.ip_low = ip * (1.0f - eps);
+      sc.aq = aq * (1.0f - eps);
+      sc.aq_high = aq * (1.0f + eps);
+      const Most top = join(pass_token<T, kSmall, false>(tr, dr, noise, V, rank, ctas, sc));
+      if (top.low > 0.0f && top.second < top.low) {
+        result = top.i;
+        break;
+      }
+      if (dr && !exact) break;
+      // (without draft logits the sum is a factor that all have in common)
+      const Left64 n64 = {scale_64(temp), dr ? 1.0 / sm.z[0] : 1.0,
+                          dr ? sm.left_a[again] / sm.z[1] : 0.0, sp.m, sq.m, dr != nullptr};
+      const Exact x =
+          join(pass_near<T, false>(tr, dr, noise, V, rank, ctas, sc, 0.0f, top.low, n64));
+      if (x.v > 0.0) {
+        result = x.i;
+        break;
+      }
+      if (again || !dr || sm.left_a[0] == sm.left_a[1]) break;
+      again = true;
+    }
+    if (result >= 0 || !dr || exact) break;
+    exact = true;
   }
   if (rank == 0 && tid == 0) {
     p.accepted[tree] = last;
