@@ -119,6 +119,10 @@ struct Best {
   }
   __device__ static Best none() { return {-INFINITY, -INFINITY, -1, 0u}; }
 };
+// Below the first temperature only the largest logits count (a score in log2 units stays
+// a number for logits up to 1e8); above the second one, all alike.
+constexpr float kCold = 0x1p-100f, kHot = 0x1p100f;
+
 // Of the scores of what is left at a node: the largest upper bound, whose it is, the
 // second largest, and a lower bound of the first one's score.
 struct Most {
@@ -175,7 +179,7 @@ struct Exact {   // a score in 64 bits
     for (int o = n / 2; o > 0; o >>= 1)
       add({__shfl_xor_sync(0xffffffffu, v, o), __shfl_xor_sync(0xffffffffu, i, o), 0}, scale);
   }
-  __device__ static Exact none() { return {-1.0, -1, 0}; }
+  __device__ static Exact none() { return {-INFINITY, -1, 0}; }
 };
 
 constexpr int kPartWords = 4;
@@ -443,9 +447,10 @@ __device__ __forceinline__ double probability_64(float l, float m, double scale,
   return exp2(((double)l - (double)m) * scale) / z;
 }
 
-// A leaf's p over its noise in 64 bits, relative to 2^base.
-__device__ __noinline__ double exact_leaf(float base, double scale, float l, float e) {
-  return exp2((double)l * scale - floor((double)base)) / (double)e;
+// A leaf's p over its noise in 64 bits, in log2 units (as a number it is out of all ranges
+// at a small temperature), relative to a token with logit m.
+__device__ __noinline__ double exact_leaf(double scale, float l, float m, float e) {
+  return ((double)l - (double)m) * scale - log2((double)e);
 }
 // What is left of a token in 64 bits, over its noise.
 struct Left64 {
@@ -646,12 +651,11 @@ __device__ __noinline__ auto pass_token(const T* tr, const T* dr, const float* n
   return x;
 }
 
-// Again, the candidates from `near` up in 64 bits (of a leaf: with scale n.scale, relative
-// to 2^top).
+// Again, the candidates from `near` up in 64 bits (of a leaf: with n.scale and n.mp).
 template <class T, bool kLeaf>
 __device__ __noinline__ Exact pass_near(const T* tr, const T* dr, const float* noise, int32_t V,
-                                        uint32_t rank, uint32_t ctas, const Scores& sc, float top,
-                                        float near, const Left64& n) {
+                                        uint32_t rank, uint32_t ctas, const Scores& sc, float near,
+                                        const Left64& n) {
   Exact best = Exact::none();
   for_rows<T, 1, true>(
       tr, dr, noise, V, rank, ctas, [&](auto& i0, auto& l, auto& d, auto& e) {
@@ -662,7 +666,7 @@ __device__ __noinline__ Exact pass_near(const T* tr, const T* dr, const float* n
         for (int k = 0; k < 8; ++k) {
           const int32_t i = i0[0] + k;
           if (!(v[k] >= near) || i < 0 || i >= V) continue;
-          const double s = kLeaf ? exact_leaf(top, n.scale, l[0].at(k), e[0].at(k))
+          const double s = kLeaf ? exact_leaf(n.scale, l[0].at(k), n.mp, e[0].at(k))
                                  : exact_left(n, l[0].at(k), d[0].at(k), e[0].at(k));
           best.add({s, i, 0}, 0.0f);
         }
@@ -748,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
   if (rank == 0 && tid == 0) {
     const float t = p.temperature ? p.temperature[tree] : 0.0f;
-    sm.temperature = t > 0.0f ? t : 0.0f;
+    sm.temperature = t >= kCold ? fminf(t, kHot) : 0.0f;
   }
   // a row's share on its way to L2 while the cluster is not ready to read it
   auto prefetch = [&](const auto* r) {
@@ -971,9 +975,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       // candidates that the fp32 scores may have in the wrong order: these are off by
       // a few 2^-24 of the logit in log2 units
       const float near = top.v - 2e-6f * (fabsf(top.v) + 256.0f);
-      if (top.second >= near)
-        result = join(pass_near<T, true>(tr, dr, noise, V, rank, ctas, sc, top.v, near,
-                                         {scale_64(temp), 0.0, 0.0, 0.0f, 0.0f, false})).i;
+      if (top.second >= near) {
+        const float base = value_of<T>(bits_now(tr, top.i));
+        result = join(pass_near<T, true>(tr, dr, noise, V, rank, ctas, sc, near,
+                                         {scale_64(temp), 0.0, 0.0, base, 0.0f, false})).i;
+      }
       break;
     }
     eps += kEpsLow;
@@ -994,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       const Left64 n64 = {scale_64(temp), dr ? 1.0 / sm.z[0] : 1.0,
                           dr ? sm.left_a[again] / sm.z[1] : 0.0, sp.m, sq.m, dr != nullptr};
       const Exact x =
-          join(pass_near<T, false>(tr, dr, noise, V, rank, ctas, sc, 0.0f, top.low, n64));
+          join(pass_near<T, false>(tr, dr, noise, V, rank, ctas, sc, top.low, n64));
       if (x.v > 0.0) {
         result = x.i;
         break;

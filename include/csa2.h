@@ -932,7 +932,8 @@ csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t
  *   that the step before has drawn (a tree with several roots is refused, an
  *   empty one gives accepted -1 and token -1).  Rows of nodes that no walk
  *   comes to, and draft rows of drafts without children, are not read.
- *   temperature: nullable dev fp32 [n_seqs], 0 or more (NULL: all 0);
+ *   temperature: nullable dev fp32 [n_seqs], 0 or more (NULL: all 0; below
+ *   2^-100: 0, above 2^100, infinity too: 2^100);
  *   uniform: dev fp32 [n_queries] in [0, 1);  noise: dev fp32 [n_seqs, vocab],
  *   positive, rows noise_ld apart (both may be NULL where temperature is);
  *   accepted: dev int32 [n_seqs], the last accepted draft or -1;  next_token:
