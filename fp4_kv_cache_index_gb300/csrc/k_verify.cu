@@ -677,8 +677,9 @@ __device__ __noinline__ Exact pass_near(const T* tr, const T* dr, const float* n
 // fp32's probabilities are good to 2e-6 of themselves (of a token 2^-30 as likely as the
 // first; to 1.1e-5 down to 2^-126), b to 2e-6 of 1 + a, and a to the sum of its b's: tests
 // with a margin of kEps and, for each rejection, kEpsMore are the right ones, bounds of
-// scores the right ones with kEpsLow on top.
-constexpr float kEps = 1e-5f, kEpsMore = 4e-6f, kEpsLow = 1e-5f;
+// scores the right ones with kEpsLow on top.  A sum is off by half a step for each
+// addition that a thread makes in turn: kEpsAdd for those of both rows.
+constexpr float kEps = 1e-5f, kEpsMore = 4e-6f, kEpsLow = 1e-5f, kEpsAdd = 0x1p-23f;
 
 // Tests of the children in `todo`, in call order, by a whole warp (every warp of
 // the cluster does the same): lane k has what belongs to children k and k + 32;
@@ -806,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   // the node is gone through again with its numbers in 64 bits, where fp32 cannot tell
   // (the whole of it: nothing is kept for that, and nothing of it computed ahead)
   bool first = true, exact = false;
+  const float eps0 = kEps + kEpsAdd * (float)((uint32_t)V / ((uint32_t)ctas * kThreads * 8 * kRows<T, kSmall>));
   if (!root) {
     // the root's only child is the token that the last step has drawn
     if (n > 0) node = last = 0;
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 
     // what is left at the node
     Sum sp = {0.0f, 1.0f}, sq = {0.0f, 1.0f};
-    float left_a = 0.0f, left_a_prev = 0.0f, eps = kEps;
+    float left_a = 0.0f, left_a_prev = 0.0f, eps = eps0;
     int32_t n_removed = 0;
     uint32_t removed_bits[2] = {0u, 0u};   // of the removed tokens' last six bits
     if (!leaf) {
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       Action action;
       int32_t taken, removed[2];
       if (!exact) {
-        Tests<float> s = {0.0f, 0.0f, 1.0f, kEps, kids, -1, {-1, -1}, 0};
+        Tests<float> s = {0.0f, 0.0f, 1.0f, eps0, kids, -1, {-1, -1}, 0};
         float pk[2] = {0.0f, 0.0f}, qk[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       } else {
         const double c = scale_64(temp);
         const Sums64 z = join(pass_sums64(tr, dr, V, rank, ctas, c, sp.m, sq.m));
-        Tests<double> s = {0.0, 0.0, 1.0, kEps, kids, -1, {-1, -1}, 0};
+        Tests<double> s = {0.0, 0.0, 1.0, 0.0f, kids, -1, {-1, -1}, 0};
         double pk[2], qk[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
