@@ -41,7 +41,9 @@ __device__ __forceinline__ uint2 encode_chunk(const uint4& v, uint32_t& byte) {
   uint32_t m = larger2(larger2(w[0] & mag, w[1] & mag), larger2(w[2] & mag, w[3] & mag));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = larger2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const uint32_t ex = max(m & 0x7FFFu, m >> 16) >> 7;
+  // a maximum leaves NaN out, but is one where all of its half's channels are
+  const uint32_t even = m & 0xFFFFu, odd = m >> 16;
+  const uint32_t ex = max(even > 0x7F80u ? 0u : even, odd > 0x7F80u ? 0u : odd) >> 7;
   byte = ex >= 8u ? ex - 8u : 0u;
   // 2^(127 - byte), a normal number: byte is at most 247.  What a product in bf16
   // loses is below 2^-126, where the codes are zeros.
