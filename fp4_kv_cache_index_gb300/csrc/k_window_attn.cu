@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.draft0 = p.first[tr];
       seq = p.seq[tr];
     } else if constexpr (!kChunk) {
-      t.at = __ldg(p.pos + q);
+      t.at = max((long long)__ldg(p.pos + q), -1ll);   // (what is W below it has to stay negative)
       t.pos0 = INT64_MAX;
       seq = p.identity ? p.seq0 + q : p.seq[q];
     }
