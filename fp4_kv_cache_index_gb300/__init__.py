@@ -105,7 +105,8 @@ class WindowStruct(ctypes.Structure):
 class WindowOpts(ctypes.Structure):
     """csa2_window_opts_t."""
     _fields_ = [("sink", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("rope_out", ctypes.c_int32),
-                ("rope_base", ctypes.c_double), ("error", ctypes.c_void_p)]
+                ("rope_base", ctypes.c_double), ("error", ctypes.c_void_p),
+                ("wait_cycles", ctypes.c_int64), ("withhold", ctypes.c_int32)]
 
 
 class VerifyStruct(ctypes.Structure):
@@ -1012,6 +1013,7 @@ class Window:
         self.pos = empty((n,), torch.int64)
         self.error = empty((4,), torch.int32)
         self.device = self.pos.get_device()
+        self.waits = (0, 0)    # csa2_window_opts_t: wait_cycles, withhold
 
         def at(t):
             return None if t is None else t.data_ptr()
@@ -1034,6 +1036,20 @@ class Window:
         dev = self._here("csa2_window_reset")
         _check(lib.csa2_window_reset(self.ref, -1 if seq is None else seq, _stream(stream, dev)),
                "csa2_window_reset")
+
+    def set_wait_limit(self, cycles: int):
+        """Bound, in SM clock cycles, on every wait inside the attention kernels
+        that read this cache (0: the default); see csa2_window_opts_t."""
+        if cycles < 0:
+            raise ValueError("Window.set_wait_limit: 0 cycles or more expected")
+        self.waits = (cycles, self.waits[1])
+
+    def inject_fault(self, withhold: int):
+        """For tests: the queries of the withhold-th item that a CTA works on, and of
+        the ones behind it, are not loaded (0: all are); see csa2_window_opts_t."""
+        if withhold < 0:
+            raise ValueError("Window.inject_fault: 0 or more expected")
+        self.waits = (self.waits[0], withhold)
 
     @property
     def swa_kv(self) -> Optional[torch.Tensor]:
@@ -1116,14 +1132,14 @@ def csa2_window_read(win: Window, end: torch.Tensor, n_rows: Optional[int] = Non
     return out
 
 
-def _window_opts(what, nq, heads, lse, sink, rope_out, rope_base, dev, error=None):
-    if lse is None and sink is None and not rope_out and error is None:
+def _window_opts(what, nq, heads, lse, sink, rope_out, rope_base, dev, error=None, waits=(0, 0)):
+    if lse is None and sink is None and not rope_out and error is None and waits == (0, 0):
         return None
     return ctypes.byref(WindowOpts(
         None if sink is None else _shaped(sink, (heads,), torch.float32, "sink", dev),
         None if lse is None else _shaped(lse, (nq, heads), torch.float32, "lse", dev),
         1 if rope_out else 0, float(rope_base),
-        None if error is None else _shaped(error, error.shape, torch.int32, "error", dev)))
+        None if error is None else _shaped(error, error.shape, torch.int32, "error", dev), *waits))
 
 
 def _window_queries(what: str, q: torch.Tensor, nq: int, out, stream, dev: int):
@@ -1164,7 +1180,8 @@ def csa2_window_attn_decode(win: Window, q: torch.Tensor, pos: torch.Tensor, sca
     _check(lib.csa2_window_attn_decode(
         win.ref, q.shape[1], nq, _i32_array(seq_ids), q_at,
         _shaped(pos, (nq,), torch.int64, "pos", dev), scale, out_at,
-        _window_opts("csa2_window_attn_decode", nq, q.shape[1], lse, sink, rope_out, rope_base, dev),
+        _window_opts("csa2_window_attn_decode", nq, q.shape[1], lse, sink, rope_out, rope_base, dev,
+                     waits=win.waits),
         _stream(stream, dev)), "csa2_window_attn_decode")
     return out
 
@@ -1180,7 +1197,8 @@ def csa2_window_attn_tree(win: Window, tree: Tree, q: torch.Tensor, draft_kv, sc
     out, q_at, out_at = _window_queries("csa2_window_attn_tree", q, nq, out, stream, dev)
     _check(lib.csa2_window_attn_tree(
         win.ref, tree.ref, q.shape[1], q_at, *_draft_rows(win, draft_kv, nq, dev), scale, out_at,
-        _window_opts("csa2_window_attn_tree", nq, q.shape[1], lse, sink, rope_out, rope_base, dev),
+        _window_opts("csa2_window_attn_tree", nq, q.shape[1], lse, sink, rope_out, rope_base, dev,
+                     waits=win.waits),
         _stream(stream, dev)), "csa2_window_attn_tree")
     return out
 
@@ -1202,12 +1220,14 @@ def csa2_window_attn_prefill(q: torch.Tensor, pos0: int, rows: torch.Tensor, row
                              lse: Optional[torch.Tensor] = None,
                              sink: Optional[torch.Tensor] = None, rope_out: bool = False,
                              rope_base: float = 0.0, error: Optional[torch.Tensor] = None,
+                             wait_cycles: int = 0, withhold: int = 0,
                              stream=None) -> torch.Tensor:
     """The same for a chunk of one sequence: query i at position pos0 + i; row r
     of rows (bf16 [n, 512]) is that of position rows_pos0 + r, the chunk's rows
     and those before it (csa2_window_read); first: bf16 [n_first, 512], the
     first tokens' rows where rows_pos0 is not 0; error: int32, the sticky error
-    word of the call (Window.error)."""
+    word of the call (Window.error); wait_cycles, withhold: as Window.set_wait_limit
+    and Window.inject_fault set them."""
     what, dev, nq = "csa2_window_attn_prefill", torch.cuda.current_device(), q.shape[0]
     out, q_at, out_at = _window_queries(what, q, nq, out, stream, dev)
     n = rows.shape[0]
@@ -1215,7 +1235,8 @@ def csa2_window_attn_prefill(q: torch.Tensor, pos0: int, rows: torch.Tensor, row
         q.shape[1], nq, pos0, q_at, _shaped(rows, (n, 512), torch.bfloat16, "rows", dev), rows_pos0,
         n, swa, None if first is None else _shaped(first, (n_first, 512), torch.bfloat16, "first", dev),
         n_first, scale, out_at,
-        _window_opts(what, nq, q.shape[1], lse, sink, rope_out, rope_base, dev, error),
+        _window_opts(what, nq, q.shape[1], lse, sink, rope_out, rope_base, dev, error,
+                     (wait_cycles, withhold)),
         _stream(stream, dev)), what)
     return out
 

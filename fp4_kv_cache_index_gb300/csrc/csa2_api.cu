@@ -2106,10 +2106,13 @@ csa2_status_t window_attn_common(int32_t n_heads, float scale, const csa2_window
   if (n_heads != 64 && n_heads != 128) return CSA2_ERR_UNSUPPORTED;
   p->n_heads = n_heads;
   p->scale_log2 = scale * 1.4426950408889634f;
+  p->wait_cycles = kWaitCycles;
   if (!o) return CSA2_OK;
   if ((o->rope_out != 0 && o->rope_out != 1) || (o->sink && !aligned16(o->sink)) ||
-      (o->lse && !aligned16(o->lse)))
+      (o->lse && !aligned16(o->lse)) || o->wait_cycles < 0 || o->withhold < 0)
     return CSA2_ERR_INVALID_ARG;
+  if (o->wait_cycles) p->wait_cycles = o->wait_cycles;
+  p->withhold = o->withhold;
   p->sink = o->sink;
   p->lse = o->lse;
   if (o->rope_out) {

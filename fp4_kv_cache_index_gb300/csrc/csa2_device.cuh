@@ -34,9 +34,7 @@ __device__ __forceinline__ void set_error(uint32_t* err, uint32_t bit) {
 #define CSA2_IN_BOUNDS(cond, err) true
 #endif
 
-// ~2^31 cycles (about one second at GB300 clocks) before a wait gives up,
-// unless the launch sets a limit of its own (csa2_cache_set_wait_limit).
-constexpr long long kWaitCycles = 1ll << 31;
+// Limit of a launch's waits (kWaitCycles, unless it sets one of its own).
 __device__ __forceinline__ long long wait_limit(long long cycles) {
   return cycles > 0 ? cycles : kWaitCycles;
 }

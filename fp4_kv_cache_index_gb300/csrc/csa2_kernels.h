@@ -68,6 +68,9 @@ constexpr int kMaxIdxGroups = 1024;
 // issues no key loads, so the MMA and epilogue waits run out with nothing in
 // flight (no copy, no MMA).
 constexpr int32_t kInjectNoKeyLoads = 1;
+// ~2^31 cycles (about one second at GB300 clocks) before a wait gives up,
+// unless the launch sets a limit of its own (csa2_cache_set_wait_limit).
+constexpr long long kWaitCycles = 1ll << 31;
 struct IndexParams {
   const float* w;          // [nq, 32]
   float* scores;           // [nq, ld]
@@ -400,6 +403,8 @@ struct WinAttnCommon {
   float* lse;
   const float* sink;
   uint32_t* err;
+  long long wait_cycles;     // bounded-wait limit in cycles (kWaitCycles, if nothing else is asked for)
+  int32_t withhold;          // tests: from its n-th item on a CTA loads no queries (0: it does)
   int32_t n_heads;
   int32_t nq;                // queries of the launch
   float scale_log2;          // scale * log2(e)

@@ -44,6 +44,11 @@
 // rows, warps 4-11 (two for each quadrant of tensor memory lanes) do the
 // softmax and the outputs and take rows out of a cache.  (Sixteen such warps, with 96
 // registers a thread: 224 us instead of 215, the trees 57 instead of 50.)
+//
+// Every wait has a limit.  A warp whose wait ran out signals nothing more and goes on to
+// no rows, since tables that it has not seen complete may hold anything; it leaves with
+// the other warps of its role, where these meet at a named barrier (`ok` is then the
+// same in all of them), else at once.  What waits for it runs out in turn.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -259,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch();
   uint32_t* err = p.err;
+  const long long& wl = p.wait_cycles;
+  auto whole_warp = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
 
   // warps that load rows: 0 and 1, and of a cache (and a chunk's first window)
   // 2-9, the softmax's
@@ -405,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kTree) return item > item0 && p.tree[first_token(item)] == p.tree[first_token(item - 1)];
     else return false;
   };
-  // Tables of an item, by the two loading warps: the rows that each token sees
-  // (of a cache: what each slot takes), and its position.
+  // Tables of an item, by the two loading warps (a warp's `ok` is the same in its lanes):
+  // the rows that each token sees (of a cache: what each slot takes), and its position.
   auto item_tables = [&](int item) {
     const int par = (item - item0) & 1;
     const int n_tok = tokens_of(item), t0 = first_token(item);
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) sm.vis[par][mine][word] = m;
       }
       if constexpr (kTree) {
-        ok = named_bar_and(3, 32 * kLoadWarps, ok);   // both warps' halves
+        named_bar(3, 32 * kLoadWarps);   // both warps' halves
         if (lw == 1) {
           const bool same = same_tree(item);
           int n = 0;
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         from[u] = is ? p.w.rows + (u == 2 ? t.first + r8 : t.ring + j) * kHeadDim + 8 * c4 : nullptr;
         to[u] = kv + j * 128;
       }
-      if (k > 0) ok = mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err) && ok;
+      if (k > 0) ok = ok && mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err, wl);
 #pragma unroll 1
       for (int cb = 0; cb < 8; ++cb) {
 #pragma unroll
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (cb & 1) copy_async_commit();
       }
-      ok = mbar_wait(&sm.tab_full, par, err) && ok;
+      ok = whole_warp(ok && mbar_wait(&sm.tab_full, par, err, wl));
       bool there[3];
 #pragma unroll
       for (int u = 0; u < 3; ++u) there[u] = sm.slot[par][8 * (u < 2 ? w + 8 * u : 16) + r8] == -2;
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cb & 1) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.kv_full[par][cb >> 1]);
+          if (ok && lane == 0) mbar_arrive(&sm.kv_full[par][cb >> 1]);
         }
       }
     }
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* const mine = kv + cb * kBlk + r8 * 128;   // this lane's row of group 0
       uint32_t bad = 0u;         // groups in whose row this lane had an infinity or a NaN
       uint32_t sc[5] = {0u, 0u, 0u, 0u, 0u};             // of slots lane + 32 i
-      if (k > 0) ok = mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err) && ok;
+      if (k > 0) ok = ok && mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err, wl);
       if (codes) {
         const uint8_t* src = p.w.codes + (t.ring + r8) * 448 + 64 * cb + 16 * c4;
 #pragma unroll 1
@@ -703,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       copy_async_commit();
-      ok = mbar_wait(&sm.tab_full, par, err) && ok;
+      ok = whole_warp(ok && mbar_wait(&sm.tab_full, par, err, wl));
       copy_async_wait<0>();
       __syncwarp();
       if (codes) {
@@ -751,10 +758,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((bad >> g) & 1u) atomicOr(&sm.bad_cb[cb][g >> 2], 1u << (8 * (g & 3) + r8));
       }
       __syncwarp();
-      if constexpr (kTree) listed_rows(t, par, cb, std::integral_constant<int, 1>(), [] {});
+      if constexpr (kTree) {
+        if (ok) listed_rows(t, par, cb, std::integral_constant<int, 1>(), [] {});
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kv_full[par][kLast]);
+      if (ok && lane == 0) mbar_arrive(&sm.kv_full[par][kLast]);
     }
   };
 
@@ -793,10 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       uint32_t n = 0;
       for (int item = item0; item < item1 && ok; ++item) {
+        if (p.withhold && item - item0 >= p.withhold - 1) ok = false;   // tests: all waits run out
         const int now = tokens_of(item) * H / 64;   // boxes of the item: the last may have one
         for (int cb = 0; cb < 8 && ok; ++cb, ++n) {
           const uint32_t s = n % stages, use = n / stages;
-          if (use > 0) ok = mbar_wait(&sm.q_empty[s], (use - 1) & 1, err);
+          if (use > 0) ok = mbar_wait(&sm.q_empty[s], (use - 1) & 1, err, wl);
           if (!ok) break;
           mbar_arrive_expect_tx(&sm.q_full[s], now * kBox);
           uint8_t* dst = smem + kQOff + s * stage_bytes;
@@ -808,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the copies in flight must land before the CTA exits
       if (!ok)
         for (uint32_t k = n > stages ? n - stages : 0; k < n; ++k)
-          mbar_wait(&sm.q_full[k % stages], (k / stages) & 1, err, drain_limit(0));
+          mbar_wait(&sm.q_full[k % stages], (k / stages) & 1, err, drain_limit(wl));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
@@ -825,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int cb = c0; cb < c1 && ok; ++cb, ++n) {
           const uint32_t s = n % stages;
           if (cb % (8 / kParts) == 0)
-            ok = mbar_wait(&sm.kv_full[j & 1][cb / (8 / kParts)], (j >> 1) & 1, err);
-          if (ok) ok = mbar_wait(&sm.q_full[s], (n / stages) & 1, err);
+            ok = mbar_wait(&sm.kv_full[j & 1][cb / (8 / kParts)], (j >> 1) & 1, err, wl);
+          if (ok) ok = mbar_wait(&sm.q_full[s], (n / stages) & 1, err, wl);
           if (!ok) break;
           tc_fence_after();
           for (int k = 0; k < 4; ++k)
@@ -837,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && c1 == 8) umma_commit(&sm.s_full);
       };
       auto issue_o = [&](int ch) {
-        if (chunk > 0) ok = mbar_wait(&sm.o_empty, (chunk - 1) & 1, err);
+        if (chunk > 0) ok = mbar_wait(&sm.o_empty, (chunk - 1) & 1, err, wl);
         if (!ok) return;
         tc_fence_after();
         for (int ks = 0; ks < kSlots / 16; ++ks)
@@ -849,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (item0 < item1) issue_s(item0, 0, 8);
       for (int item = item0; item < item1 && ok; ++item) {
         const uint32_t k = (uint32_t)(item - item0);
-        ok = mbar_wait(&sm.p_full, k & 1, err);
+        ok = mbar_wait(&sm.p_full, k & 1, err, wl);
         if (ok) issue_o(ch0);
         // half of the next S while the outputs' first half is read out, where the
         // rows stay as they are
@@ -866,13 +876,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {   // the MMAs issued so far must end before the CTA exits
         umma_commit(&sm.end);
-        mbar_wait(&sm.end, 0, err, drain_limit(0));
+        mbar_wait(&sm.end, 0, err, drain_limit(wl));
       }
     }
   } else if (loader) {
     // ------------------------------------------------------------ rows, tables
     int64_t g_have = 0;
-    for (int item = item0; item < item1 && ok; ++item) {
+    for (int item = item0; item < item1; ++item) {
       const uint32_t k = (uint32_t)(item - item0);
       if constexpr (kChunk) {
         const int64_t g = block_of(item);
@@ -887,10 +897,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the tables' place was that of the item before the last one; the rows'
         // is needed where one comes in
-        if (k > 1) ok = mbar_wait_sleep(&sm.kv_empty[k & 1], ((k - 2) >> 1) & 1, err);
-        item_tables(item);
+        if (k > 1) ok = whole_warp(mbar_wait_sleep(&sm.kv_empty[k & 1], ((k - 2) >> 1) & 1, err, wl));
+        if (ok) item_tables(item);
         if (fresh) {
-          ok = mbar_wait_sleep(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
+          ok = whole_warp(ok && mbar_wait_sleep(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err, wl));
           if (ok) {
             chunk_store(a, 2 * lw, x[0]);
             chunk_store(a, 2 * lw + 1, x[1]);
@@ -909,18 +919,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // not before all warps have the last item's: a wait tells neighbouring
         // phases apart only
-        if (k > 0) ok = mbar_wait_sleep(&sm.kv_full[(k - 1) & 1][kLast], ((k - 1) >> 1) & 1, err) && ok;
-        item_tables(item);
+        if (k > 0) ok = ok && mbar_wait_sleep(&sm.kv_full[(k - 1) & 1][kLast], ((k - 1) >> 1) & 1, err, wl);
+        ok = whole_warp(ok);
+        if constexpr (kTree) ok = named_bar_and(3, 32 * kLoadWarps, ok);
         if (!ok) break;
+        item_tables(item);
         // Of a tree whose rows are here already these warps bring the others, while
         // the softmax warps have the last item's outputs to store.
         if (same_tree(item)) {
           listed_rows(query_of(base_of(item)), k & 1, lw, std::integral_constant<int, 4>(), [&] {
-            ok = mbar_wait(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err) && ok;
+            ok = mbar_wait(&sm.kv_empty[(k - 1) & 1], ((k - 1) >> 1) & 1, err, wl);
           });
           fence_proxy_async_smem();
-          __syncwarp();
-          if (lane < kSoftWarps / kLoadWarps) mbar_arrive(&sm.kv_full[k & 1][0]);
+          ok = whole_warp(ok);
+          if (ok && lane < kSoftWarps / kLoadWarps) mbar_arrive(&sm.kv_full[k & 1][0]);
         }
       }
     }
@@ -944,8 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_rows = tokens_of(item) * H;
       const bool live = quad * 32 < n_rows;       // of the warp's rows, all or none
       const int tk = pair ? row >> 6 : 0;
-      ok = mbar_wait(&sm.kv_full[ph][kLast], (k >> 1) & 1, err) && ok;
-      ok = mbar_wait(&sm.s_full, ph, err) && ok;
+      ok = mbar_wait(&sm.kv_full[ph][kLast], (k >> 1) & 1, err, wl) && ok;
+      ok = mbar_wait(&sm.s_full, ph, err, wl) && ok;
       tc_fence_after();
       // a thread has a half of its row: columns 0-79 or 80-143
       const int g0 = half ? 5 : 0, ng = half ? 4 : 5;
@@ -1042,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* out = p.out + 8 * (lane & 3);
       if (live) out += ((int64_t)query_row(item, tk) * H + ((32 * quad) & (H - 1)) + (lane >> 2)) * kHeadDim;
       for (int ch = ch0; ch < ch1; ch += width, ++chunk) {
-        ok = mbar_wait(&sm.o_full, chunk & 1, err) && ok;
+        ok = mbar_wait(&sm.o_full, chunk & 1, err, wl) && ok;
         tc_fence_after();
         const int mine = width / 2 * half;   // this warp's columns of the accumulator: mine ..
         const uint32_t from = tmem + lanes + kOCol + mine;

@@ -738,8 +738,15 @@ csa2_status_t csa2_window_read(const csa2_window_t* w, int32_t n_segs, const int
                                void* rope, uint8_t* scales, void* first, csa2_stream_t stream);
 
 /* Options of the window layers' attention (NULL: none): the sink logits, lse
- * and output rotation of csa2_sparse_attn_decode_ex.  rope_base: at least 1,
- * or 0 for 10000.                                                           */
+ * and output rotation of csa2_sparse_attn_decode_ex (sink and lse 16-byte
+ * aligned).  rope_base: at least 1, or 0 for 10000.  wait_cycles: the bound on
+ * every wait inside the kernel, as csa2_cache_set_wait_limit sets it for a
+ * cache (0: the default).  One that runs out records CSA2_ERR_TIMEOUT in the
+ * error word and ends the kernel; its outputs are then not to be used.
+ * withhold: for tests of that path, like csa2_cache_inject_fault: 0, or n:
+ * no queries are loaded for the n-th item (a query or two) that each CTA works
+ * on, nor for the ones behind it, so that all waits run out with no copy and
+ * no MMA in flight.                                                         */
 typedef struct {
   const float* sink;   /* nullable dev fp32 [n_heads]             */
   float* lse;          /* nullable dev fp32 [n_queries, n_heads]  */
@@ -747,6 +754,8 @@ typedef struct {
   double rope_base;
   uint32_t* error;     /* nullable dev word (csa2_window_attn_prefill only:
                         * the others use the cache's)             */
+  int64_t wait_cycles; /* 0 or more                               */
+  int32_t withhold;    /* 0 or more                               */
 } csa2_window_opts_t;
 
 /* Attention of a window layer: a query at position p sees the rows of the
