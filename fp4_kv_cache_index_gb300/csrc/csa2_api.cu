@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <memory>
 #include <mutex>
 #include <new>
@@ -2099,6 +2100,37 @@ void branch_order(int n, const int32_t* parent, int* order) {
   }
 }
 
+// Bytes that a call reads or writes (none where p is NULL).
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+// Whether nothing that is written lies over what is read, or over what else is written:
+// CTAs store outputs while others have yet to load.
+bool apart(std::initializer_list<Bytes> written, std::initializer_list<Bytes> read) {
+  auto over = [](const Bytes& a, const Bytes& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.n > 0 && b.n > 0 && (x < y ? y - x < (uintptr_t)a.n : x - y < (uintptr_t)b.n);
+  };
+  for (const Bytes* a = written.begin(); a != written.end(); ++a) {
+    for (const Bytes& b : read)
+      if (over(*a, b)) return false;
+    for (const Bytes* b = a + 1; b != written.end(); ++b)
+      if (over(*a, *b)) return false;
+  }
+  return true;
+}
+// The same for the outputs of an attention over a cache and drafts.
+bool apart_attn(const WinRows& w, const WinDrafts& d, int64_t nq, int32_t n_heads, const void* q,
+                const void* out, const WinAttnCommon& p) {
+  const int64_t n = (int64_t)w.n_seqs * (w.swa + w.n_first), size = nq * n_heads * kHeadDim * 2;
+  return apart({{out, size}, {p.lse, nq * n_heads * 4}},
+               {{q, size}, {p.sink, n_heads * 4},
+                {w.rows, n * kHeadDim * 2}, {w.codes, n * 448}, {w.rope, n * 128}, {w.scales, n * 8},
+                {w.pos, n * 8},
+                {d.rows, nq * kHeadDim * 2}, {d.codes, nq * 448}, {d.rope, nq * 128}, {d.scales, nq * 8}});
+}
+
 // What the three attention calls share.
 csa2_status_t window_attn_common(int32_t n_heads, float scale, const csa2_window_opts_t* o,
                                  WinAttnCommon* p) {
@@ -2109,7 +2141,8 @@ csa2_status_t window_attn_common(int32_t n_heads, float scale, const csa2_window
   p->wait_cycles = kWaitCycles;
   if (!o) return CSA2_OK;
   if ((o->rope_out != 0 && o->rope_out != 1) || (o->sink && !aligned16(o->sink)) ||
-      (o->lse && !aligned16(o->lse)) || o->wait_cycles < 0 || o->withhold < 0)
+      (o->lse && !aligned16(o->lse)) || o->wait_cycles < 0 || o->withhold < 0 ||
+      (reinterpret_cast<uintptr_t>(o->error) & 3u))
     return CSA2_ERR_INVALID_ARG;
   if (o->wait_cycles) p->wait_cycles = o->wait_cycles;
   p->withhold = o->withhold;
@@ -2314,7 +2347,10 @@ csa2_status_t csa2_window_attn_decode(const csa2_window_t* w, int32_t n_heads, i
   st = window_attn_common(n_heads, scale, opts, p);
   if (st == CSA2_OK && nq > kWinRowLimit) st = CSA2_ERR_UNSUPPORTED;
   if (st == CSA2_OK && nq > 0 &&
-      (!q || !out || !pos || !aligned16(q) || !aligned16(out) || !aligned8(pos) || q == out))
+      (!q || !out || !pos || !aligned16(q) || !aligned16(out) || !aligned8(pos) ||
+       !apart_attn(r, {}, nq, n_heads, q, out, *p) ||
+       !apart({{out, (int64_t)nq * n_heads * kHeadDim * 2}, {p->lse, (int64_t)nq * n_heads * 4}},
+              {{pos, (int64_t)nq * 8}})))
     st = CSA2_ERR_INVALID_ARG;
   int sms = 0;
   if (st == CSA2_OK && nq > 0 && !sm_count(&sms)) st = CSA2_ERR_CUDA;
@@ -2361,7 +2397,8 @@ csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* t
   WinDrafts d = {};
   if (st == CSA2_OK && nq > 0) {
     st = draft_rows(w, draft_kv, draft_codes, draft_rope, draft_scales, &d);
-    if (st == CSA2_OK && (!q || !out || !aligned16(q) || !aligned16(out) || q == out))
+    if (st == CSA2_OK && (!q || !out || !aligned16(q) || !aligned16(out) ||
+                          !apart_attn(r, d, nq, n_heads, q, out, *p)))
       st = CSA2_ERR_INVALID_ARG;
   }
   int sms = 0;
@@ -2440,8 +2477,16 @@ csa2_status_t csa2_window_attn_prefill(int32_t n_heads, int32_t nq, int64_t pos0
   if (nq > kWinRowLimit) return CSA2_ERR_UNSUPPORTED;
   if (pos0 > INT64_MAX - nq || rows_pos0 > pos0 || n_rows > INT64_MAX - rows_pos0 ||
       pos0 + nq > rows_pos0 + n_rows || !q || !rows || !out || !aligned16(q) || !aligned16(rows) ||
-      !aligned16(out) || q == out || (first && !aligned16(first)) ||
-      (n_first > 0 && rows_pos0 > 0 && !first))
+      !aligned16(out) || (first && !aligned16(first)) || (n_first > 0 && rows_pos0 > 0 && !first))
+    return CSA2_ERR_INVALID_ARG;
+  // rows that are loaded: the chunk's and its window's, in blocks of 8, and first tokens
+  const int64_t size = (int64_t)nq * n_heads * kHeadDim * 2, row = kHeadDim * 2;
+  const int64_t lo = std::max<int64_t>(pos0 - rows_pos0 - swa - 16, 0);
+  const Bytes band = {reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(rows) + (uintptr_t)lo * row),
+                      (pos0 - rows_pos0 - lo + nq + std::min<int64_t>(rows_pos0 + n_rows - pos0 - nq, 8)) * row};
+  if (!apart({{out, size}, {p.lse, (int64_t)nq * n_heads * 4}},
+             {{q, size}, {p.sink, n_heads * 4}, band, {rows, std::min<int64_t>(n_rows, n_first) * row},
+              {first, n_first * row}}))
     return CSA2_ERR_INVALID_ARG;
   p.w.swa = swa;
   p.w.n_first = n_first;

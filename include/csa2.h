@@ -767,8 +767,10 @@ typedef struct {
  * (csa2_window_append).
  *   seq_ids: host [n_queries] or NULL (query i is of sequence i), a sequence
  *   any number of times;  n_heads: 64 or 128;  q, out: dev bf16 [n_queries,
- *   n_heads, 512], out not q;  pos: dev int64 [n_queries], negative: the
- *   query sees nothing.                                                     */
+ *   n_heads, 512];  pos: dev int64 [n_queries], negative: the query sees
+ *   nothing.
+ * Of this call and the next two: CSA2_ERR_INVALID_ARG if out or lse lies over
+ * what the call reads, or they over each other.                             */
 csa2_status_t csa2_window_attn_decode(const csa2_window_t* w, int32_t n_heads, int32_t n_queries,
                                       const int32_t* seq_ids, const void* q, const int64_t* pos,
                                       float scale, void* out, const csa2_window_opts_t* opts,
