@@ -33,6 +33,10 @@ __device__ __forceinline__ void set_error(uint32_t* err, uint32_t bit) {
 #else
 #define CSA2_IN_BOUNDS(cond, err) true
 #endif
+// Whether a row is one of a window cache's.
+__device__ __forceinline__ bool is_window_row(const WinRows& w, int64_t row) {
+  return row >= 0 && row < (int64_t)w.n_seqs * (w.swa + w.n_first);
+}
 
 // Limit of a launch's waits (kWaitCycles, unless it sets one of its own).
 __device__ __forceinline__ long long wait_limit(long long cycles) {

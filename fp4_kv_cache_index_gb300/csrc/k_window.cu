@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       cb = encode_chunk(b[k], bb);   // lanes 24-31: not used
     }
     auto store = [&](int64_t row) {
+      if (!CSA2_IN_BOUNDS(is_window_row(w, row), w.err)) return;
       if (w.fp8) {
         uint2* c = reinterpret_cast<uint2*>(w.codes + row * 448);
         c[lane] = ca;
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t lo = end > p.n_rows ? end - p.n_rows : 0;
   const int64_t x = first ? j - p.n_rows : lo + j;
   const int64_t row = first ? first_row(w, seq, x) : ring_row(w, seq, x);
+  if (!CSA2_IN_BOUNDS(is_window_row(w, row) && j < p.n_rows + w.n_first, w.err)) return;
   // the row's tag and the row together: one that is not held is read for nothing
   const int64_t tag = __ldg(w.pos + row);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -253,6 +255,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int64_t x = p.pos0[tree] + d, src = first + path[len - 1 - d];
     const bool ring = len - d <= w.swa, head = x < w.n_first;
     auto copy = [&](int64_t row) {
+      if (!CSA2_IN_BOUNDS(is_window_row(w, row) && src >= first && src < p.first[tree + 1], w.err)) return;
       if (w.fp8) {
         const uint4* c = reinterpret_cast<const uint4*>(p.d.codes + src * 448);
         if (lane < 28) reinterpret_cast<uint4*>(w.codes + row * 448)[lane] = __ldg(c + lane);

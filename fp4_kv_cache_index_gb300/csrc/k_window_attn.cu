@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       row = t.first + x;
     }
     if (x < 0) return -1;
-    if (kTree && x >= t.pos0) return sm.draft[lw & 1][x - t.pos0];
+    if (kTree && x >= t.pos0) return CSA2_IN_BOUNDS(x - t.pos0 < 64, err) ? sm.draft[lw & 1][x - t.pos0] : -1;
+    if (!CSA2_IN_BOUNDS(is_window_row(p.w, row), err)) return -1;
     return p.w.pos[row] == x ? -2 : -1;
   };
 
@@ -552,11 +553,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           byte[i] = 0u;
           if (at >= n) continue;
           slot[i] = sm.list[par][at];
+          if (!CSA2_IN_BOUNDS(slot[i] < kSlots, err)) slot[i] = 0;
           const int what = sm.slot[par][slot[i]];
           if (what == -1) continue;
           const WinDrafts& x = p.d;
           const int64_t row = what >= 0 ? (int64_t)t.draft0 + what
                               : slot[i] < W ? t.ring + slot[i] : t.first + slot[i] - kFirstSlot;
+          if (!CSA2_IN_BOUNDS(what >= 0 ? row < p.nq : is_window_row(p.w, row), err)) continue;
           if (kFp8 && cb < 7) {
             d[i] = ldg_now_v4((what >= 0 ? x.codes : p.w.codes) + row * 448 + 64 * cb + 16 * c4);
             byte[i] = ldg_now_u8((what >= 0 ? x.scales : p.w.scales) + row * 8 + cb);
@@ -627,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         const int j = 8 * (u < 2 ? w + 8 * u : 16) + r8;
-        const bool is = u == 2 ? r8 < F : j < W;
+        const bool is = (u == 2 ? r8 < F : j < W) &&
+                        CSA2_IN_BOUNDS(is_window_row(p.w, u == 2 ? t.first + r8 : t.ring + j), err);
         from[u] = is ? p.w.rows + (u == 2 ? t.first + r8 : t.ring + j) * kHeadDim + 8 * c4 : nullptr;
         to[u] = kv + j * 128;
       }
@@ -682,18 +686,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* const mine = kv + cb * kBlk + r8 * 128;   // this lane's row of group 0
       uint32_t bad = 0u;         // groups in whose row this lane had an infinity or a NaN
       uint32_t sc[5] = {0u, 0u, 0u, 0u, 0u};             // of slots lane + 32 i
+      const bool held = CSA2_IN_BOUNDS(is_window_row(p.w, t.ring) && is_window_row(p.w, t.ring + W - 1) &&
+                                           (F == 0 || is_window_row(p.w, t.first + F - 1)), err);
       if (k > 0) ok = ok && mbar_wait(&sm.kv_empty[par ^ 1], ((k - 1) >> 1) & 1, err, wl);
       if (codes) {
         const uint8_t* src = p.w.codes + (t.ring + r8) * 448 + 64 * cb + 16 * c4;
 #pragma unroll 1
         for (int j = r8, g = 0; g < 16; ++g, j += 8, src += 8 * 448)
-          if (j < W) copy_async(mine + g * 1024 + 16 * c4, src);
-        if (r8 < F)
+          if (held && j < W) copy_async(mine + g * 1024 + 16 * c4, src);
+        if (held && r8 < F)
           copy_async(mine + 16 * 1024 + 16 * c4, p.w.codes + (t.first + r8) * 448 + 64 * cb + 16 * c4);
 #pragma unroll
         for (int i = 0; i < 5; ++i) {
           const int j = lane + 32 * i;
-          if (i < 4 ? j < W : lane < F)
+          if (held && (i < 4 ? j < W : lane < F))
             sc[i] = ldg_now_u8(p.w.scales + (i < 4 ? t.ring + j : t.first + lane) * 8 + cb);
         }
       } else {
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int j = r8, g = 0; g < kGroups; ++g, j += 8, src += 8 * step) {
           if (g == 16) src = base + (t.first + r8) * step;
-          if (g < 16 ? j < W : r8 < F) {
+          if (held && (g < 16 ? j < W : r8 < F)) {
             copy_async(mine + g * 1024 + ((c4 ^ r8) << 4), src);
             copy_async(mine + g * 1024 + (((4 + c4) ^ r8) << 4), src + 32);
           }
@@ -1042,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float L = l * am + (z == -INFINITY ? 0.0f : fast_exp2(z - M));
         inv = L == 0.0f ? 0.0f : am / L;
         if (bad) inv = NAN;
-        if (p.lse && half == 0 && part == 0)
+        if (p.lse && half == 0 && part == 0 && CSA2_IN_BOUNDS(query_row(item, tk) < p.nq, err))
           p.lse[(int64_t)query_row(item, tk) * H + h] =
               inv != inv ? NAN
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
@@ -1092,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
-          if (ok) {
+          if (ok && CSA2_IN_BOUNDS(query_row(item, tk) < p.nq && c >= 0 && c + 32 <= kHeadDim, err)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int row_ = 8 * i + (lane >> 2);
