@@ -377,8 +377,9 @@ __device__ __forceinline__ void add_chunks(Sum& s, const Eight<T> (&l)[kN], floa
 }
 
 // Chunks of two rows that a thread has in flight.  Few where a thread has two in all:
-// the code of a pass is then fetched for one use (5 drafts over 32000 tokens: 12.9 us,
-// with four 14.2; 64 sequences over 131072: 82 with four, 97 with two).
+// the code of a pass is then fetched for one use (replayed graphs, bf16 with draft logits:
+// 5 drafts over 32000 tokens 8.5 us, with four 9.2; 40 sequences over 1500 tokens 20.2
+// and 23.6; 64 sequences over 131072 79.3 with four, 93 with two).
 template <class T, bool kSmall>
 constexpr int kRows = (kSmall ? 4 : 8) / (int)sizeof(T);
 
@@ -741,7 +742,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   for (int h = 0; h < 2; ++h) parent[h] = lane + 32 * h < n ? p.parent[d0 + lane + 32 * h] : -2;
   const int halves = n > 32 ? 2 : 1;
   griddep_wait();
-  griddep_launch();
   // the first CTA's: their tokens and numbers
   int32_t token[2] = {-1, -1};
   float uniform[2] = {0.0f, 0.0f};
@@ -1013,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     if (result >= 0 || !dr || exact) break;
     exact = true;
   }
+  griddep_launch();
   if (rank == 0 && tid == 0) {
     p.accepted[tree] = last;
     p.next_token[tree] = result;
@@ -1047,7 +1048,7 @@ cudaError_t launch(const VerifyParams& p, int cluster, cudaStream_t s) {
 // CTAs of a sequence's cluster: as many as run at once over the whole GPU, with
 // a share of the vocabulary worth a pass each.  Clusters of 16 (8 SMs of one of the
 // GPU's processing clusters) with room to spare, since they do not fill those: 8 trees of
-// 8 drafts over 131072 tokens take 25.6 us with 16 and 32.2 with 8, one 11.0 and 13.8.
+// 8 drafts over 131072 tokens take 26.1 us with 16 and 30.0 with 8, one 11.2 and 13.8.
 int verify_cluster(int64_t n_trees, int32_t vocab, int sms) {
   int c = 1;
   while (c < kMaxCluster && n_trees * c * (c < 8 ? 2 : 3) <= (int64_t)sms * kBlocks && vocab >= 4096 * c) c *= 2;

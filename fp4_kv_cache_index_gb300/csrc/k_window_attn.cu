@@ -262,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   griddep_wait();
-  griddep_launch();
   uint32_t* err = p.err;
   const long long& wl = p.wait_cycles;
   auto whole_warp = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
@@ -1054,6 +1053,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
                                : (M + log2f(L)) * 0.69314718055994531f;
       }
+      if (item + 1 == item1) griddep_launch();
       // outputs, 32 rows x 32 channels at a time: rounded, turned in the warp's own
       // box so that four lanes have 64 bytes of a row (a lane that stores its own
       // row touches 32 lines an instruction), the next ones on their way
