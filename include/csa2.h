@@ -687,8 +687,12 @@ csa2_status_t csa2_norm_rope(int32_t n_parts, const csa2_norm_part_t* parts, flo
  *   are ignored), 16-byte aligned (scales: 8);  pos: dev int64 [rows];
  *   error: nullable dev word, the sticky error word of the calls that read
  *   the cache (csa2_window_device_error).
- * Everything that changes is in device memory: the calls may be captured into
- * a graph and replayed (with other positions in the same memory).           */
+ * Calls may be captured into a graph and replayed.  What csa2_window_append,
+ * _read and _attn_decode take of positions is in device memory: a replay finds
+ * others there.  The calls for trees and chunks (_attn_tree, _accept_tree,
+ * _attn_prefill) take positions and parents from the host: a replay has those
+ * of the capture, so a step at other positions is captured anew.  Host lists
+ * (seq_ids, n_rows) are those of the capture in all of them.                */
 #define CSA2_MAX_FIRST 8
 typedef struct {
   int32_t n_seqs;
