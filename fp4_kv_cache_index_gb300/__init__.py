@@ -1271,10 +1271,16 @@ def csa2_verify_tree(tree: Tree, tokens: torch.Tensor, logits: torch.Tensor,
     after the last committed token (None: the first draft of each tree is the
     token that the step before has drawn, and is kept); draft_logits and
     draft_root: likewise those of the model that drafted (None: drafts count as
-    certain); temperature: fp32 [n_seqs] (None: 0), 0 takes the largest logit;
+    certain); temperature: fp32 [n_seqs] (None: 0), 0 (or below 2^-100) takes the
+    largest logit;
     uniform: fp32 [n_queries] in [0, 1); noise: fp32 [n_seqs, vocab],
     exponential variates.  Rows may be further apart than vocab (the same for
-    all logits); rows at 16-byte boundaries are read faster."""
+    all logits); rows at 16-byte boundaries are read faster.
+
+    draft_logits are for children that were drawn from softmax(draft /
+    temperature) independently of each other, in call order; others (the most
+    likely ones, or drawn without replacement) are verified without, or the tokens
+    are not distributed as the target's."""
     what, dev, nq, S = "csa2_verify_tree", torch.cuda.current_device(), tree.n_queries, tree.n_seqs
     if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"{what}: logits bf16 or fp32 [n_queries, vocab] expected")

@@ -922,8 +922,13 @@ csa2_status_t csa2_sparse_attn_tree(const csa2_cache_t* cache, const csa2_tree_t
                                     size_t workspace_bytes, csa2_stream_t stream);
 
 /* Decides which drafts of each tree are kept, and the token that follows them,
- * by rejection sampling: the tokens that come out are distributed as the
- * target's.  The walk starts at the tree's root (the last committed token).
+ * by rejection sampling.  The tokens that come out are distributed as the
+ * target's if the drafts were chosen without regard to uniform and noise, and,
+ * with draft logits, each node's children were drawn from softmax(draft / T)
+ * at the same T, independently of each other (one may come twice) and in call
+ * order.  Children that were drawn without replacement, or are the draft's
+ * most likely ones, come without draft logits.
+ * The walk starts at the tree's root (the last committed token).
  * At a node, p = softmax(target / T) and, of the model that drafted, q =
  * softmax(draft / T); its children are tested in call order, child c with
  * token x against what is left of p, r = max(p - a q, 0) / b (a = 0, b = 1 at
