@@ -879,6 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) umma_commit(&sm.kv_empty[k & 1]);
         if (ok && item + 1 < item1) issue_s(item + 1, c0, 8);
       }
+      griddep_launch();
       if (!ok) {   // the MMAs issued so far must end before the CTA exits
         umma_commit(&sm.end);
         mbar_wait(&sm.end, 0, err, drain_limit(wl));
@@ -1053,7 +1054,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               : m == -INFINITY ? (p.sink ? __ldg(p.sink + h) : -INFINITY)
                                : (M + log2f(L)) * 0.69314718055994531f;
       }
-      if (item + 1 == item1) griddep_launch();
       // outputs, 32 rows x 32 channels at a time: rounded, turned in the warp's own
       // box so that four lanes have 64 bytes of a row (a lane that stores its own
       // row touches 32 lines an instruction), the next ones on their way
