@@ -28,7 +28,8 @@
 // few 1e-5 of itself off: if another token's upper bound reaches the best one's lower
 // bound (always, where p and a q all but cancel), the node's sums and tests are made
 // again in 64 bits, if they were not yet, and all such tokens are scored with those.
-// So the result is the one of 64-bit arithmetic, whatever the order of the sums.
+// There r is formed by one rejection after the other, each divided by its sum: p - a q
+// has lost a token that is left by 1e-9 of p twice.  So the result is the one of 64-bit arithmetic, whatever the order of the sums.
 //
 // Measured: 64 sequences of up to 8 drafts over 131072 tokens, whose walks read 134
 // MB: 80 us.  The SMs are busy for 55 % of that (the longest walks have more than twice
@@ -197,6 +198,7 @@ struct Tests {
   Real a, a_prev, b;
   float eps;                 // fp32: what p and a q are good to
   uint64_t todo;             // children that are still to be tested
+  bool last;                 // the last one was rejected, what then is left has no sum yet
   int32_t taken;
   int32_t removed[2], n_removed;   // lane r: removed tokens r and r + 32
 };
@@ -207,7 +209,8 @@ struct Smem {
   alignas(16) Kid kid[2][64];
   float temperature;
   int32_t removed[64];       // for the last pass
-  double left_a[2], z[2];    // a, before the last rejection too, and the sums in 64 bits
+  double z[2], inv[64][2];   // in 64 bits: the two sums; two factors that are 1 / the sum behind a rejection
+  int32_t n_inv, last;       // how many of these, and whether a rejection without follows
 };
 
 // 16 bytes or less to `local` of another CTA of the cluster.
@@ -265,7 +268,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // 2^x in 64 bits, to their rounding: the Taylor series of e^r, |r| <= ln 2 / 2, to the
 // 13th power (the next term is (ln 2 / 2)^14 / 14! = 4e-18).
 __device__ __forceinline__ double exp2_64(double x) {
-  if (!(x > -1000.0)) return x == x ? 0.0 : x;
+  if (!(x > -1080.0)) return x == x ? 0.0 : x;
   const double n = rint(x), r = (x - n) * 0.693147180559945309;
   double s = 1.0 / 6227020800.0;
   s = fma(s, r, 1.0 / 479001600);
@@ -281,7 +284,10 @@ __device__ __forceinline__ double exp2_64(double x) {
   s = fma(s, r, 0.5);
   s = fma(s, r, 1.0);
   s = fma(s, r, 1.0);
-  return s * __hiloint2double((int)(1023.0 + fmin(n, 1000.0)) << 20, 0);
+  // 2^n in two parts, of which both are normal numbers where it is not
+  const double low = fmax(n, -1000.0);
+  return s * __hiloint2double((int)(1023.0 + fmin(low, 1000.0)) << 20, 0) *
+         __hiloint2double((int)(1023.0 + (n - low)) << 20, 0);
 }
 
 // Eight neighbouring values of a row as they are in memory.
@@ -444,8 +450,13 @@ __device__ __forceinline__ void for_rows(const T* a, const T* b, const float* c,
 // Logits to log2 units.  A function so that it is not computed ahead, where fp32 will do.
 __device__ __noinline__ double scale_64(float temp) { return 1.4426950408889634 / (double)temp; }
 
-__device__ __forceinline__ double probability_64(float l, float m, double scale, double z) {
+// A child's probability, and what is left of both children's behind a rejection (out of
+// line as well: in the kernel they cost it registers).
+__device__ __noinline__ double probability_64(float l, float m, double scale, double z) {
   return exp2(((double)l - (double)m) * scale) / z;
+}
+__device__ __noinline__ void left_64(double (&p)[2], const double (&q)[2], double sum) {
+  for (int h = 0; h < 2; ++h) p[h] = fmax(p[h] - q[h], 0.0) / sum;
 }
 
 // A leaf's p over its noise in 64 bits, in log2 units (as a number it is out of all ranges
@@ -453,17 +464,28 @@ __device__ __forceinline__ double probability_64(float l, float m, double scale,
 __device__ __noinline__ double exact_leaf(double scale, float l, float m, float e) {
   return ((double)l - (double)m) * scale - log2((double)e);
 }
-// What is left of a token in 64 bits, over its noise.
+// What is left of p in 64 bits: behind each rejection max(r - q, 0) over its sum; behind
+// the last one (`last`) without.  (A sum may be subnormal, where its reciprocal is no
+// number: two factors.)
 struct Left64 {
-  double scale, ip, aq;      // 1 / z and a / z of the two rows
+  double scale, ip, iq;      // 1 / z of the two rows
+  const double (*inv)[2];    // in shared memory
+  int32_t n;
   float mp, mq;
-  bool two;
+  bool two, last;
+  __device__ __forceinline__ double of(float l, float d) const {
+    double r = __dmul_rn(exp2_64(((double)l - (double)mp) * scale), ip);
+    if (two) {
+      const double q = __dmul_rn(exp2_64(((double)d - (double)mq) * scale), iq);
+      for (int k = 0; k < n; ++k)
+        r = __dmul_rn(__dmul_rn(fmax(__dsub_rn(r, q), 0.0), inv[k][0]), inv[k][1]);
+      if (last) r = fmax(__dsub_rn(r, q), 0.0);
+    }
+    return r;
+  }
 };
 __device__ __noinline__ double exact_left(const Left64& n, float l, float d, float e) {
-  double s = __dmul_rn(exp2_64(((double)l - (double)n.mp) * n.scale), n.ip);
-  if (n.two)
-    s = fmax(__dsub_rn(s, __dmul_rn(exp2_64(((double)d - (double)n.mq) * n.scale), n.aq)), 0.0);
-  return s / (double)e;
+  return n.of(l, d) / (double)e;
 }
 
 // The passes over a node's rows, a function each so that each has its own
@@ -544,16 +566,11 @@ __device__ __noinline__ Sums64 pass_sums64(const T* tr, const T* dr, int32_t V, 
 }
 template <class T>
 __device__ __noinline__ Total<double> pass_total64(const T* tr, const T* dr, int32_t V, uint32_t rank,
-                                                   uint32_t ctas, double scale, float mp, float mq,
-                                                   double zp, double zq, double a) {
+                                                   uint32_t ctas, const Left64& n) {
   Total<double> y = {0.0};
-  const double ip = 1.0 / zp, aq = a / zq;
   for_rows<T, 1, false>(tr, dr, nullptr, V, rank, ctas, [&](auto&, auto& l, auto& d, auto&) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      y.t += fmax(__dsub_rn(__dmul_rn(exp2_64(((double)l[0].at(k) - (double)mp) * scale), ip),
-                            __dmul_rn(exp2_64(((double)d[0].at(k) - (double)mq) * scale), aq)),
-                  0.0);
+    for (int k = 0; k < 8; ++k) y.t += n.of(l[0].at(k), d[0].at(k));
   });
   return y;
 }
@@ -684,7 +701,7 @@ constexpr float kEps = 1e-5f, kEpsMore = 4e-6f, kEpsLow = 1e-5f, kEpsAdd = 0x1p-
 
 // Tests of the children in `todo`, in call order, by a whole warp (every warp of
 // the cluster does the same): lane k has what belongs to children k and k + 32;
-// `p`, `q`: of their tokens.
+// `p`, `q`: of their tokens (64 bits, with draft logits: what is left of p).
 template <class Real>
 __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const Kid (&kid)[2],
                                                 const Real (&p)[2], const Real (&q)[2], int lane) {
@@ -699,7 +716,7 @@ __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const 
     const Real uk = __shfl_sync(0xffffffffu, h ? kid[1].u : kid[0].u, l);
     // certain drafts: nothing is left of a token that was removed
     if (!two && __any_sync(0xffffffffu, s.removed[0] == t || s.removed[1] == t)) continue;
-    const Real x = uk * qk * s.b, y = two ? pk - s.a * qk : pk;
+    const Real x = uk * qk * (kFast || !two ? s.b : Real(1)), y = kFast && two ? pk - s.a * qk : pk;
     if (kFast) {
       const float near = two ? (s.a + uk * (1.0f + s.a)) * qk : uk;
       if (fabsf((float)(x - y)) <= s.eps * (float)(pk + near)) return kExact;
@@ -713,6 +730,7 @@ __device__ __forceinline__ Action test_children(Tests<Real>& s, bool two, const 
       s.a += s.b;
       s.eps += kEpsMore;
       if (s.todo) return kSum;           // else the sum that is left is not needed
+      if constexpr (!kFast) s.last = true;
     } else if (s.b - pk > Real(0)) {
       s.b -= pk;
       if (lane == (s.n_removed & 31)) {
@@ -887,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       Action action;
       int32_t taken, removed[2];
       if (!exact) {
-        Tests<float> s = {0.0f, 0.0f, 1.0f, eps0, kids, -1, {-1, -1}, 0};
+        Tests<float> s = {0.0f, 0.0f, 1.0f, eps0, kids, false, -1, {-1, -1}, 0};
         float pk[2] = {0.0f, 0.0f}, qk[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -914,18 +932,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       } else {
         const double c = scale_64(temp);
         const Sums64 z = join(pass_sums64(tr, dr, V, rank, ctas, c, sp.m, sq.m));
-        Tests<double> s = {0.0, 0.0, 1.0, 0.0f, kids, -1, {-1, -1}, 0};
+        Tests<double> s = {0.0, 0.0, 1.0, 0.0f, kids, false, -1, {-1, -1}, 0};
         double pk[2], qk[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           pk[h] = probability_64(kid[h].lp, sp.m, c, z.p);
           qk[h] = dr ? probability_64(kid[h].lq, sq.m, c, z.q) : 1.0;
         }
+        int32_t n64 = 0;
         while ((action = test_children<double>(s, dr, kid, pk, qk, lane)) == kSum) {
-          const Total<double> y =
-              join(pass_total64(tr, dr, V, rank, ctas, c, sp.m, sq.m, z.p, z.q, s.a));
-          if (y.t > 0.0) s.b = y.t;
-          else s.a = s.a_prev;
+          const Total<double> y = join(pass_total64(
+              tr, dr, V, rank, ctas, {c, 1.0 / z.p, 1.0 / z.q, sm.inv, n64, sp.m, sq.m, true, true}));
+          if (!(y.t > 0.0)) {   // nothing: as before this rejection
+            s.a = s.a_prev;
+            continue;
+          }
+          s.b *= y.t;
+          left_64(pk, qk, y.t);
+          if (tid == 0) {
+            sm.inv[n64][0] = y.t < 0x1p-900 ? 0x1p1000 : 1.0;
+            sm.inv[n64][1] = 1.0 / (y.t * sm.inv[n64][0]);
+          }
+          ++n64;
+          __syncthreads();
         }
         taken = s.taken;
         left_a = (float)s.a;
@@ -934,10 +963,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         removed[0] = s.removed[0];
         removed[1] = s.removed[1];
         if (tid == 0) {
-          sm.left_a[0] = s.a;
-          sm.left_a[1] = s.a_prev;
           sm.z[0] = z.p;
           sm.z[1] = z.q;
+          sm.n_inv = n64;
+          sm.last = s.last;
         }
         __syncthreads();
       }
@@ -980,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (top.second >= near) {
         const float base = value_of<T>(bits_now(tr, top.i));
         result = join(pass_near<T, true>(tr, dr, noise, V, rank, ctas, sc, near,
-                                         {scale_64(temp), 0.0, 0.0, base, 0.0f, false})).i;
+                                         {scale_64(temp), 0.0, 0.0, nullptr, 0, base, 0.0f, false, false})).i;
       }
       break;
     }
@@ -999,15 +1028,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
       if (dr && !exact) break;
       // (without draft logits the sum is a factor that all have in common)
-      const Left64 n64 = {scale_64(temp), dr ? 1.0 / sm.z[0] : 1.0,
-                          dr ? sm.left_a[again] / sm.z[1] : 0.0, sp.m, sq.m, dr != nullptr};
-      const Exact x =
-          join(pass_near<T, false>(tr, dr, noise, V, rank, ctas, sc, top.low, n64));
+      const bool last = dr && sm.last && !again;
+      const Left64 n = {scale_64(temp), dr ? 1.0 / sm.z[0] : 1.0, dr ? 1.0 / sm.z[1] : 0.0,
+                        sm.inv, dr ? sm.n_inv : 0, sp.m, sq.m, dr != nullptr, last};
+      const Exact x = join(pass_near<T, false>(tr, dr, noise, V, rank, ctas, sc, top.low, n));
       if (x.v > 0.0) {
         result = x.i;
         break;
       }
-      if (again || !dr || sm.left_a[0] == sm.left_a[1]) break;
+      if (!last) break;
       again = true;
     }
     if (result >= 0 || !dr || exact) break;
