@@ -31,12 +31,12 @@
 // There r is formed by one rejection after the other, each divided by its sum: p - a q
 // has lost a token that is left by 1e-9 of p twice.  So the result is the one of 64-bit arithmetic, whatever the order of the sums.
 //
-// Measured: 64 sequences of up to 8 drafts over 131072 tokens, whose walks read 134
-// MB: 80 us.  The SMs are busy for 55 % of that (the longest walks have more than twice
-// the average's nodes and no more CTAs), with instructions, of which the exponentials
-// are the smaller part, and the joins of a cluster.  One chat
-// of 5 drafts over 32000 tokens: 8.7 us; 12 trees of 64 over 100003 tokens of fp32
-// without draft logits: 20 us.  Twice as many CTAs a sequence take 75 us for the
+// Measured (replayed graphs of one call): 64 sequences of up to 8 drafts over 131072
+// tokens, whose walks read 134 MB: 79.6 us.  The SMs are busy for 55 % of that (the longest
+// walks have more than twice the average's nodes and no more CTAs), with instructions, of
+// which the exponentials are the smaller part, and the joins of a cluster.  One chat
+// of 5 drafts over 32000 tokens: 8.4 us; 12 trees of 64 over 100003 tokens of fp32
+// without draft logits: 20.4 us.  Twice as many CTAs a sequence take 77 us for the
 // mixed batch and a fifth longer for one of equal walks.
 #include <type_traits>
 

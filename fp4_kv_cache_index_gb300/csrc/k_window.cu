@@ -17,8 +17,8 @@
 //
 // Measured: 98000 rows of prompts, rounded into other memory (201 MB) and each
 // sequence's last 128 stored: 36.1 us, 5.6 TB/s or 82 % of the copy rate; with 192
-// windows read back behind it, 44.4 us.  A chunk of 8192 rows and its window back:
-// 4.9 us, 16 single rows and their windows: 3.5 us, two launches each.
+// windows read back behind it, 44.7 us.  A chunk of 8192 rows and its window back:
+// 5.2 us, 16 single rows and their windows: 3.7 us, two launches each.
 #include <cuda_fp16.h>
 
 #include "csa2_device.cuh"

@@ -766,7 +766,9 @@ typedef struct {
  * positions x <= p with p - x < swa or x < n_first that are held,
  *   l_x = scale * q . kv_x,   out = sum_x softmax(l)_x kv_x.
  * A query that sees none gives 0 (lse -inf, or the sink).  The probabilities
- * are rounded to bf16, in the sum as in the product.
+ * are rounded to bf16, in the sum as in the product.  A query that sees a row
+ * with an infinity or a NaN gives what the formula gives over a bf16 cache, NaN
+ * over one in 8 bits.
  * One query of each of n_queries sequences; its own row is written first
  * (csa2_window_append).
  *   seq_ids: host [n_queries] or NULL (query i is of sequence i), a sequence
@@ -785,7 +787,7 @@ typedef struct csa2_tree csa2_tree_t;
 /* The same for trees of drafted tokens (see below): a draft sees the held
  * rows of positions below pos0 and those of its own path, as decoding the path
  * token by token would.  With 128 heads the result is that of decoding, bit for
- * bit; with 64, where two drafts share a tile, the sums are of the same terms
+ * bit (over finite rows); with 64, where two drafts share a tile, the sums are of the same terms
  * in another order.  A row that holds an infinity or a NaN makes the outputs of
  * the drafts that see it NaN, no other's.  The drafts' rows come in the cache's
  * form: draft_kv dev bf16 [n_queries, 512], or the three FP8 arrays.        */
