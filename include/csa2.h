@@ -787,10 +787,11 @@ typedef struct csa2_tree csa2_tree_t;
 /* The same for trees of drafted tokens (see below): a draft sees the held
  * rows of positions below pos0 and those of its own path, as decoding the path
  * token by token would.  With 128 heads the result is that of decoding, bit for
- * bit (over finite rows); with 64, where two drafts share a tile, the sums are of the same terms
- * in another order.  A row that holds an infinity or a NaN makes the outputs of
- * the drafts that see it NaN, no other's.  The drafts' rows come in the cache's
- * form: draft_kv dev bf16 [n_queries, 512], or the three FP8 arrays.        */
+ * bit (over finite rows); with 64, where two drafts share a tile, the sums are
+ * of the same terms in another order.  A row that holds an infinity or a NaN
+ * makes the outputs of the drafts that see it NaN, no other's.  The drafts' rows
+ * come in the cache's form: draft_kv dev bf16 [n_queries, 512], or the three FP8
+ * arrays.                                                                   */
 csa2_status_t csa2_window_attn_tree(const csa2_window_t* w, const csa2_tree_t* tree,
                                     int32_t n_heads, const void* q, const void* draft_kv,
                                     const uint8_t* draft_codes, const void* draft_rope,
