@@ -13,9 +13,12 @@
 //                                                       B MN-major)
 // on tcgen05 with fp32 accumulators; the swizzled rows in shared memory serve
 // both products.  Q is needed once and streams through small stages in
-// channel blocks of 64; P (bf16) goes from the softmax's registers to tensor
-// memory; O is made in two halves of 256 channels, since both halves, S and P
-// do not fit the 512 columns together.  A CTA takes neighbouring items: in a
+// channel blocks of 64; P goes from the softmax's registers to tensor memory, as
+// bf16, the type that the MMA multiplies the rows in (their sum is one of the rounded
+// values, so the weights still add up to 1; outputs are off by 0.0019 of themselves
+// where fp32 probabilities and the same output rounding give 0.0017); O is made in
+// two halves of 256 channels, since both halves, S and P do not fit the 512 columns
+// together.  A CTA takes neighbouring items: in a
 // chunk the rows stay in shared memory as a ring of 17 blocks of 8 positions
 // (and one of first tokens), of which one is replaced every 8 tokens; of a tree
 // they stay too, but for the slots that the next paths take otherwise.
@@ -23,7 +26,7 @@
 // A tree's drafts of 64 heads go two an item, in the order of its branches, so
 // that neighbours have most of their paths in common: the slots are the less deep
 // one's, and what only the other's path has is in up to 8 more.  Each query has its
-// own mask of the 144 slots.  (One draft an item: 73 us where this takes 50, 1024
+// own mask of the 144 slots.  (One draft an item: 73 us where this took 50, 1024
 // drafts.)
 //
 // What bounds it.  The chunk: HBM, q in and the outputs out (8192 tokens of 64 heads
@@ -32,8 +35,8 @@
 // chain of which only half of the next S and the second half of the stores run
 // beside something else.  Decode: the same chain once (27000 cycles, of which the
 // rows 11000, S 5000, the softmax 3000, products and outputs 5000): 14.2 us for 128
-// sequences; for one, four CTAs share the outputs: 10.7 us.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
-// Trees: 1024 drafts 50 us, three to four items a CTA.
+// sequences; for one, four CTAs share the outputs: 10.9 us.  509 sequences of 128 heads, 186 MB: 51 us, four rounds of it.
+// Trees: 1024 drafts 48 us, three to four items a CTA.
 //
 // Code is fetched cold by most CTAs, once for each instruction that a single pass
 // executes: the softmax and the outputs are loops over 16 and 32 columns although
